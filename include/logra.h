@@ -646,6 +646,163 @@ logra_status logra_ts_update(const logra_matrix *m, const float *S_L, const floa
 logra_status logra_ts_apply(const logra_matrix *m, const void *ws, size_t ws_bytes, void *W, int w_dtype,
                             int64_t ldw, float lr, float scale, void *stream);
 
+/*
+ * Global gradient norm over many tensors, and clipping by it. A step's
+ * gradients are many: one sketch per projection (whose squared norm is an
+ * unbiased estimate of its gradient's, since E[A^T A] = I) and the dense
+ * gradients of what is not sketched.
+ *     norm = sqrt(sum over tensors and elements of g^2)
+ *     coef = max_norm / norm   where max_norm < norm < infinity, else 1
+ *     out  = coef * g          (rounded once, to nearest even)
+ * A norm that is not finite (some gradient is not) clips nothing: the caller
+ * reads it and skips the step, as with a sqnorm that is not finite. Squares
+ * and sums are fp64, so a finite gradient's norm neither overflows nor
+ * vanishes on the way; *norm is its fp32 value (infinity above the fp32
+ * range, where coef is still right).
+ *
+ * The tensors are described once, in a table that stays with the program:
+ *   logra_grad_list_pack (host code) checks n tensors, writes their table to
+ *   HOST memory (logra_grad_table_bytes(n) bytes, 8-byte aligned) and fills
+ *   *list; the caller copies the table to the device, puts that address
+ *   (16-byte aligned) into list->table, and keeps both while the tensors
+ *   stay where they are.
+ * logra_grad_tensor: rows x cols elements at `data` (device) with row stride
+ *   ld >= cols (one row: any ld >= cols); LOGRA_F32 or LOGRA_BF16, mixed in
+ *   one list as wished; rows or cols 0 for an empty tensor (data may then be
+ *   NULL). data needs only its element's alignment. The address ranges of a
+ *   list's tensors, first to last element, must not overlap (so neither may
+ *   two views that interleave).
+ * Errors of pack: INVALID_ARGUMENT (n outside [0, 2^20], nulls, negative
+ *   sizes, ld < cols, misaligned data or table, overlapping tensors),
+ *   UNSUPPORTED (dtype; a tensor of more than 2^40 elements or a list of
+ *   more than 2^44), WORKSPACE (table_bytes too small). *list is written on
+ *   success only.
+ */
+typedef struct logra_grad_tensor {
+    void *data;
+    int64_t rows, cols, ld;
+    int32_t dtype;
+    int32_t reserved;
+} logra_grad_tensor;
+typedef struct logra_grad_list {
+    const void *table;    /* device copy of the packed table (set by the caller) */
+    int64_t elements;     /* of all tensors (set by pack, as what follows)       */
+    int64_t chunks;
+    uint64_t shapes;      /* hash of every tensor's rows and cols                */
+    int32_t n;
+    int32_t reserved;
+} logra_grad_list;
+size_t logra_grad_table_bytes(int64_t n);
+logra_status logra_grad_list_pack(int64_t n, const logra_grad_tensor *tensors, void *table_host, size_t table_bytes,
+                                  logra_grad_list *list);
+
+/*
+ * logra_grad_norm -- norm[0] (device fp32) of the list.
+ * logra_grad_clip -- norm[0], coef[0] (device fp32) and the scaled tensors:
+ *   into the tensors of `out`, a list of the same shapes in the same order
+ *   (types may differ), or in place when out is NULL or has the same table.
+ *   In place nothing is written where coef is 1. max_norm >= 0 (infinity:
+ *   only the norm, and copies). The tensors of out must not overlap those of
+ *   the list.
+ *   ws: device, 16-byte aligned, >= logra_grad_workspace_bytes(list) bytes;
+ *   scratch, one for every call in flight.
+ * Errors: INVALID_ARGUMENT (nulls, table NULL or misaligned with n > 0,
+ *   lists of different shapes, max_norm negative or NaN), WORKSPACE, HIP.
+ */
+size_t logra_grad_workspace_bytes(const logra_grad_list *list);
+logra_status logra_grad_norm(const logra_grad_list *list, float *norm, void *ws, size_t ws_bytes, void *stream);
+logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list *out, float max_norm, float *norm,
+                             float *coef, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Expert layers: rows sorted by expert, and back. Token t takes topk
+ * experts, ids[t][0 .. topk - 1]; an id outside 0 .. n_experts - 1 is a
+ * dropped choice (a padding token, an expert without room). With N = T topk
+ * pairs p = t topk + j:
+ *
+ * logra_expert_sort -- the pairs sorted by expert, those of one expert in
+ *   their own order:
+ *     offsets[e] .. offsets[e + 1]  the places of expert e (n_experts + 1
+ *                                   int32; offsets[n_experts] pairs are kept)
+ *     order[place] = p              (N int32; -1 behind the last kept place)
+ *     slots[p] = place              (N int32, T x topk; -1 for a dropped pair)
+ *   ids: T x topk, row stride ld_ids, int32 (id_bytes 4) or int64 (8).
+ *   An expert may appear twice in a token's choices (two pairs, two places).
+ *   ws: >= logra_expert_sort_workspace_bytes bytes (0 for few pairs).
+ * logra_expert_gather -- Xs[slots[t][j]] = w[t][j] X[t].
+ * logra_expert_combine -- Y[t] = sum over kept j of w[t][j] Ys[slots[t][j]],
+ *   summed in fp32 in the order of j and rounded once; zero where a token
+ *   keeps none.
+ * logra_expert_combine_backward -- gradients of combine:
+ *     dYs[slots[t][j]] = w[t][j] dY[t],   dw[t][j] = <dY[t], Ys[slots[t][j]]>
+ *   (fp32 sums; dw is 0 for a dropped pair).
+ *   The gradient of gather is combine with the same weights (and the
+ *   weights' gradient <X[t], dXs[slots[t][j]]>, which combine_backward gives
+ *   with X in the place of dY).
+ *   dtype: LOGRA_F32 or LOGRA_BF16, of all rows of the call. Rows are h wide
+ *   with row strides ld >= h, aligned to their element. w: T x topk fp32,
+ *   contiguous, or NULL (gather, combine) for weights of 1 (then gather
+ *   copies bits). slots: T x topk int32, contiguous. n_rows: the rows of Xs,
+ *   Ys, dYs; a slot outside 0 .. n_rows - 1 counts as dropped. Rows that no
+ *   slot names are not written; two pairs must not name the same slot in
+ *   gather and combine_backward.
+ * Limits: topk in [1, 64], n_experts in [1, 1024], T <= 2^23 and
+ *   T topk <= 2^26.
+ * Errors: INVALID_ARGUMENT (nulls with something to do, negative sizes,
+ *   topk, n_experts or h < 1, ld, misalignment, id_bytes), UNSUPPORTED
+ *   (dtype, limits), WORKSPACE, HIP.
+ */
+size_t logra_expert_sort_workspace_bytes(int64_t T, int topk, int n_experts);
+logra_status logra_expert_sort(int64_t T, int topk, int n_experts, const void *ids, int id_bytes, int64_t ld_ids,
+                               int32_t *offsets, int32_t *order, int32_t *slots, void *ws, size_t ws_bytes,
+                               void *stream);
+logra_status logra_expert_gather(int64_t T, int topk, int64_t h, int dtype, const void *X, int64_t ldx,
+                                 const int32_t *slots, const float *w, void *Xs, int64_t ldxs, int64_t n_rows,
+                                 void *stream);
+logra_status logra_expert_combine(int64_t T, int topk, int64_t h, int dtype, const void *Ys, int64_t ldys,
+                                  int64_t n_rows, const int32_t *slots, const float *w, void *Y, int64_t ldy,
+                                  void *stream);
+logra_status logra_expert_combine_backward(int64_t T, int topk, int64_t h, int dtype, const void *dY, int64_t lddy,
+                                           const void *Ys, int64_t ldys, int64_t n_rows, const int32_t *slots,
+                                           const float *w, void *dYs, int64_t lddys, float *dw, void *stream);
+
+/*
+ * logra_sketch_experts -- logra_sketch_accumulate for the projections of all
+ * experts of a layer in one call, the experts' row counts read on the
+ * device:
+ *     S_e (+)= dY_e^T (X_e A_e^T)   for e = 0 .. n_experts - 1,
+ * rows offsets[e] .. offsets[e + 1] - 1 of dY, and of X the same rows
+ * (order NULL) or, with order and topk as logra_expert_sort made them, row
+ * order[i] / topk for the sorted row i: X is then the activations before the
+ * sort, and their sorted copy need not be kept for the backward pass.
+ * Sources: as logra_sketch_accumulate.
+ * Arguments:
+ *   m        d, k, r, seed and step of every expert; expert e's sign matrix
+ *            is that of matrix_id + e id_stride.
+ *   N        rows of dY (sorted), >= 0; offsets (n_experts + 1 int32, non-
+ *            decreasing; values outside 0 .. N count as the nearest bound).
+ *   X        x_rows x k, row stride ldx (x_rows >= N without order). A row
+ *            that order names outside 0 .. x_rows - 1 counts as zeros.
+ *   dY       N x d, row stride lddy; rows from offsets[n_experts] on are not
+ *            read.
+ *   S        n_experts x d x r fp32, contiguous. An expert without rows
+ *            keeps its S (accumulate != 0) or gets zeros.
+ *   act_dtype LOGRA_BF16: bf16 products with fp32 accumulation; the
+ *            projection is kept as two bf16 terms (within 2^-16 of its
+ *            fp32 value), so S is close to what fp32 products give. r in
+ *            {32, 64, 128, 256}; d, k, ldx, lddy multiples of 8; X, dY
+ *            16-byte aligned. LOGRA_F32: fp32 throughout, r in [1, 1024].
+ *   ws       device, 16-byte aligned, >= logra_sketch_experts_workspace_bytes
+ *            bytes; scratch, one for every call in flight.
+ * n_experts in [1, 1024], N <= 2^26.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE, HIP as there.
+ */
+size_t logra_sketch_experts_workspace_bytes(const logra_matrix *m, int n_experts, int64_t N, int act_dtype);
+logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t id_stride, int64_t N, int act_dtype,
+                                  const int32_t *offsets, const int32_t *order, int topk, const void *X, int64_t ldx,
+                                  int64_t x_rows, const void *dY, int64_t lddy, float *S, int accumulate, void *ws,
+                                  size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

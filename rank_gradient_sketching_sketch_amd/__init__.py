@@ -16,6 +16,10 @@ __all__ = [
     "logra_sqnorm_prepare", "logra_update_sqnorm_prepared", "logra_update_sqnorm_noalloc",
     "logra_sqnorm_batch_workspace_bytes", "logra_update_sqnorm_batch",
     "logra_kl_budget_at", "logra_kl_step_scale", "KLBudget",
+    "GradList", "logra_grad_workspace_bytes", "logra_grad_norm", "logra_grad_clip",
+    "logra_expert_sort_workspace_bytes", "logra_expert_sort", "logra_expert_gather",
+    "logra_expert_combine", "logra_expert_combine_backward",
+    "logra_sketch_experts_workspace_bytes", "logra_sketch_experts",
     "LograError", "MatrixDesc", "library_path", "load_library",
 ]
 

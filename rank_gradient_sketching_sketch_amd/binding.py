@@ -62,6 +62,18 @@ class LaunchOpts(ctypes.Structure):
                          int(backward_fold), addr)
 
 
+class _GradTensor(ctypes.Structure):
+    """logra_grad_tensor: one tensor of a gradient list."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _GradListDesc(ctypes.Structure):
+    """logra_grad_list: what pack says of a list, and its table's device address."""
+    _fields_ = [("table", ctypes.c_void_p), ("elements", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("shapes", ctypes.c_uint64), ("n", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class KLBudget(ctypes.Structure):
     """logra_kl_budget: KL budget annealed linearly from delta_start to
     delta_end over anneal_steps steps."""
@@ -148,6 +160,31 @@ def load_library():
     lib.logra_ts_update.argtypes = [D, P, P, P, P, P, P, P, f32, f32, f32, P, P, sz, P]
     lib.logra_ts_apply.restype = i32
     lib.logra_ts_apply.argtypes = [D, P, sz, P, i32, i64, f32, f32, P]
+    G = ctypes.POINTER(_GradListDesc)
+    lib.logra_grad_table_bytes.restype = sz
+    lib.logra_grad_table_bytes.argtypes = [i64]
+    lib.logra_grad_list_pack.restype = i32
+    lib.logra_grad_list_pack.argtypes = [i64, ctypes.POINTER(_GradTensor), P, sz, G]
+    lib.logra_grad_workspace_bytes.restype = sz
+    lib.logra_grad_workspace_bytes.argtypes = [G]
+    lib.logra_grad_norm.restype = i32
+    lib.logra_grad_norm.argtypes = [G, P, P, sz, P]
+    lib.logra_grad_clip.restype = i32
+    lib.logra_grad_clip.argtypes = [G, G, f32, P, P, P, sz, P]
+    lib.logra_expert_sort_workspace_bytes.restype = sz
+    lib.logra_expert_sort_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.logra_expert_sort.restype = i32
+    lib.logra_expert_sort.argtypes = [i64, i32, i32, P, i32, i64, P, P, P, P, sz, P]
+    lib.logra_expert_gather.restype = i32
+    lib.logra_expert_gather.argtypes = [i64, i32, i64, i32, P, i64, P, P, P, i64, i64, P]
+    lib.logra_expert_combine.restype = i32
+    lib.logra_expert_combine.argtypes = [i64, i32, i64, i32, P, i64, i64, P, P, P, i64, P]
+    lib.logra_expert_combine_backward.restype = i32
+    lib.logra_expert_combine_backward.argtypes = [i64, i32, i64, i32, P, i64, P, i64, i64, P, P, P, i64, P, P]
+    lib.logra_sketch_experts_workspace_bytes.restype = sz
+    lib.logra_sketch_experts_workspace_bytes.argtypes = [D, i32, i64, i32]
+    lib.logra_sketch_experts.restype = i32
+    lib.logra_sketch_experts.argtypes = [D, i32, u64, i64, i32, P, P, i32, P, i64, i64, P, i64, P, i32, P, sz, P]
     _lib = lib
     return lib
 
@@ -458,3 +495,243 @@ def logra_ts_apply(m: MatrixDesc, ws: torch.Tensor, W: torch.Tensor, lr: float, 
     _check(load_library().logra_ts_apply(
         ctypes.byref(m), _ptr(ws), _nbytes(ws), _ptr(W), _dtype_code(W), _ld(W), float(lr), float(scale),
         _stream(stream)), "logra_ts_apply")
+
+
+# ---- gradient clipping and expert layers ----
+
+class _On:
+    """One call's device: its tensors must all be on one GPU, the workspace
+    comes from the stream the call runs on (so that its memory is not handed
+    out to other work while the call still uses it), and the call is made
+    with that GPU current."""
+
+    def __init__(self, where, stream, tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if t.device.type != "cuda" or (dev is not None and t.device != dev):
+                raise LograError(1, "%s: tensors on one GPU expected" % where)
+            dev = t.device
+        if dev is None:
+            raise LograError(1, "%s: a tensor on a GPU expected" % where)
+        self.where, self.device = where, dev
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+            self.ambient = True
+        else:
+            self.ambient = False
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        self.stream = stream
+
+    def workspace(self, ws, nbytes):
+        """(tensor, pointer, bytes); the caller keeps the tensor until the call is made."""
+        if ws is None:
+            if nbytes == 0:
+                return None, None, 0
+            if self.ambient:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(self.stream):
+                    ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        elif ws.device != self.device or not ws.is_contiguous():
+            raise LograError(3, "%s: contiguous workspace on %s expected" % (self.where, self.device))
+        return ws, _ptr(ws), _nbytes(ws)
+
+    def call(self, fn, *args):
+        handle = ctypes.c_void_p(self.stream.cuda_stream)
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(*args, handle), self.where)
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(*args, handle), self.where)
+
+
+def _want(where, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise LograError(1, "%s: contiguous %s tensor of shape %s expected" % (where, dtype, tuple(shape)))
+
+
+def _one_float(where, t):
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise LograError(1, "%s: one-element float32 tensor expected" % where)
+
+
+def _rows(where, t, h=None, dtype=None):
+    """Row stride of a 2-D tensor of rows (unit column stride)."""
+    if t.dim() != 2 or (t.size(0) > 0 and t.size(1) > 1 and t.stride(1) != 1):
+        raise LograError(1, "%s: 2-D tensor with unit column stride expected" % where)
+    if h is not None and t.size(1) != h:
+        raise LograError(1, "%s: rows of %d elements expected" % (where, h))
+    if dtype is not None and t.dtype != dtype:
+        raise LograError(1, "%s: one dtype for all rows expected" % where)
+    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+
+
+class GradList:
+    """The gradients of a step, described to the library once: logra_grad_norm
+    and logra_grad_clip read them through a device table that holds their
+    addresses. The list keeps the tensors; they must stay where they are
+    (gradients written in place every step, as Step's sketches are).
+
+    tensors  float32 or bfloat16, on one GPU, contiguous of any shape or 2-D
+             with unit column stride and a longer row stride; none may overlap
+             another.
+    device   of an empty list."""
+
+    def __init__(self, tensors, device=None):
+        self.tensors = list(tensors)
+        where = "GradList"
+        self.device = self.tensors[0].device if self.tensors else torch.device(device or "cuda")
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        items = (_GradTensor * max(1, len(self.tensors)))()
+        for i, t in enumerate(self.tensors):
+            if t.device != self.device or self.device.type != "cuda":
+                raise LograError(1, where + ": tensors on one GPU expected")
+            items[i] = _GradTensor(t.data_ptr(), *self._rows_of(t), _dtype_code(t), 0)
+        lib = load_library()
+        host = torch.empty(max(8, int(lib.logra_grad_table_bytes(len(self.tensors)))), dtype=torch.uint8)
+        self.desc = _GradListDesc()
+        _check(lib.logra_grad_list_pack(len(self.tensors), items, _ptr(host), _nbytes(host),
+                                        ctypes.byref(self.desc)), "logra_grad_list_pack")
+        self.table = host.to(self.device)
+        self.desc.table = self.table.data_ptr()
+        self.elements = int(self.desc.elements)
+
+    @staticmethod
+    def _rows_of(t):
+        if t.is_contiguous():
+            cols = t.shape[-1] if t.dim() else 1
+            return (t.numel() // cols if cols else 0), cols, cols
+        if t.dim() == 2 and (t.stride(1) == 1 or t.size(1) == 1):
+            return t.size(0), t.size(1), t.stride(0)
+        raise LograError(1, "GradList: contiguous tensors, or 2-D ones with unit column stride, expected")
+
+
+def logra_grad_workspace_bytes(grads: GradList) -> int:
+    return int(load_library().logra_grad_workspace_bytes(ctypes.byref(grads.desc)))
+
+
+def logra_grad_norm(grads: GradList, norm: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """norm[0] = the L2 norm over all elements of all tensors of the list."""
+    where = "logra_grad_norm"
+    _one_float(where, norm)
+    on = _On(where, stream, (grads.table, norm))
+    ws, p, nb = on.workspace(ws, logra_grad_workspace_bytes(grads))
+    on.call(load_library().logra_grad_norm, ctypes.byref(grads.desc), _ptr(norm), p, nb)
+
+
+def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: torch.Tensor,
+                    out: Optional[GradList] = None, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """norm[0] as logra_grad_norm; coef[0] = max_norm / norm where the norm is
+    finite and above max_norm, else 1; every gradient times coef, in place or
+    into the tensors of `out` (a list of the same shapes)."""
+    where = "logra_grad_clip"
+    _one_float(where, norm)
+    _one_float(where, coef)
+    on = _On(where, stream, (grads.table, norm, coef, None if out is None else out.table))
+    ws, p, nb = on.workspace(ws, logra_grad_workspace_bytes(grads))
+    on.call(load_library().logra_grad_clip, ctypes.byref(grads.desc), None if out is None else ctypes.byref(out.desc),
+            float(max_norm), _ptr(norm), _ptr(coef), p, nb)
+
+
+def logra_expert_sort_workspace_bytes(T: int, topk: int, n_experts: int) -> int:
+    return int(load_library().logra_expert_sort_workspace_bytes(int(T), int(topk), int(n_experts)))
+
+
+def logra_expert_sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, order: torch.Tensor,
+                      slots: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The pairs (token, choice) of ids (T x topk, int32 or int64; ids outside
+    0 .. n_experts - 1 dropped) sorted by expert: offsets (n_experts + 1),
+    order (T topk, place -> pair) and slots (T x topk, pair -> place), int32."""
+    where = "logra_expert_sort"
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise LograError(1, where + ": 2-D int32 or int64 ids expected")
+    T, K = ids.shape
+    ld = _rows(where, ids)
+    _want(where, offsets, torch.int32, (n_experts + 1,))
+    _want(where, order, torch.int32, (T * K,))
+    _want(where, slots, torch.int32, (T, K))
+    on = _On(where, stream, (ids, offsets, order, slots))
+    ws, p, nb = on.workspace(ws, logra_expert_sort_workspace_bytes(T, K, n_experts))
+    on.call(load_library().logra_expert_sort, T, K, int(n_experts), _ptr(ids), ids.element_size(), ld, _ptr(offsets),
+            _ptr(order), _ptr(slots), p, nb)
+
+
+def _slots_of(where, slots, weights, T):
+    if slots.dim() != 2 or slots.size(0) != T:
+        raise LograError(1, "%s: slots of %d tokens expected" % (where, T))
+    _want(where, slots, torch.int32, slots.shape)
+    if weights is not None:
+        _want(where, weights, torch.float32, slots.shape)
+    return slots.size(1)
+
+
+def logra_expert_gather(X: torch.Tensor, slots: torch.Tensor, Xs: torch.Tensor,
+                        weights: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Xs[slots[t][j]] = weights[t][j] X[t] (no weights: copies); the other
+    rows of Xs stay as they are."""
+    where = "logra_expert_gather"
+    T, h = X.shape if X.dim() == 2 else (0, 0)
+    ldx, ldxs = _rows(where, X), _rows(where, Xs, h, X.dtype)
+    K = _slots_of(where, slots, weights, T)
+    on = _On(where, stream, (X, slots, Xs, weights))
+    on.call(load_library().logra_expert_gather, T, K, h, _dtype_code(X), _ptr(X), ldx, _ptr(slots), _ptr(weights),
+            _ptr(Xs), ldxs, Xs.size(0))
+
+
+def logra_expert_combine(Ys: torch.Tensor, slots: torch.Tensor, Y: torch.Tensor,
+                         weights: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Y[t] = sum_j weights[t][j] Ys[slots[t][j]] (no weights: the plain sum,
+    which is the gradient of gather)."""
+    where = "logra_expert_combine"
+    T, h = Y.shape if Y.dim() == 2 else (0, 0)
+    ldy, ldys = _rows(where, Y), _rows(where, Ys, h, Y.dtype)
+    K = _slots_of(where, slots, weights, T)
+    on = _On(where, stream, (Ys, slots, Y, weights))
+    on.call(load_library().logra_expert_combine, T, K, h, _dtype_code(Y), _ptr(Ys), ldys, Ys.size(0), _ptr(slots),
+            _ptr(weights), _ptr(Y), ldy)
+
+
+def logra_expert_combine_backward(dY: torch.Tensor, Ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
+                                  dYs: torch.Tensor, dweights: torch.Tensor, stream=None) -> None:
+    """dYs[slots[t][j]] = weights[t][j] dY[t] and dweights[t][j] = <dY[t],
+    Ys[slots[t][j]]>; the other rows of dYs stay as they are."""
+    where = "logra_expert_combine_backward"
+    T, h = dY.shape if dY.dim() == 2 else (0, 0)
+    lddy, ldys, lddys = _rows(where, dY), _rows(where, Ys, h, dY.dtype), _rows(where, dYs, h, dY.dtype)
+    if dYs.size(0) != Ys.size(0):
+        raise LograError(1, where + ": as many rows of dYs as of Ys expected")
+    K = _slots_of(where, slots, weights, T)
+    _want(where, dweights, torch.float32, slots.shape)
+    on = _On(where, stream, (dY, Ys, slots, weights, dYs, dweights))
+    on.call(load_library().logra_expert_combine_backward, T, K, h, _dtype_code(dY), _ptr(dY), lddy, _ptr(Ys), ldys,
+            Ys.size(0), _ptr(slots), _ptr(weights), _ptr(dYs), lddys, _ptr(dweights))
+
+
+def logra_sketch_experts_workspace_bytes(m: MatrixDesc, n_experts: int, N: int, act_dtype: int) -> int:
+    return int(load_library().logra_sketch_experts_workspace_bytes(ctypes.byref(m), int(n_experts), int(N),
+                                                                    int(act_dtype)))
+
+
+def logra_sketch_experts(m: MatrixDesc, offsets: torch.Tensor, X: torch.Tensor, dY: torch.Tensor, S: torch.Tensor,
+                         accumulate: bool, order: Optional[torch.Tensor] = None, topk: int = 1, id_stride: int = 1,
+                         ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """S[e] (+)= dY_e^T (X_e A_e^T) for every expert e: S is n_experts x d x r,
+    dY is N x d sorted by expert, X the same rows (N x k) or, with the sort's
+    order and topk, the activations before it (T x k); expert e's signs are
+    those of m.matrix_id + e id_stride."""
+    where = "logra_sketch_experts"
+    E, N = S.size(0), dY.size(0)
+    _want(where, S, torch.float32, (E, m.d, m.r))
+    _want(where, offsets, torch.int32, (E + 1,))
+    if order is not None:
+        _want(where, order, torch.int32, (N,))
+    ldx, lddy = _rows(where, X, m.k), _rows(where, dY, m.d, X.dtype)
+    code = _dtype_code(X)
+    on = _On(where, stream, (offsets, X, dY, S, order))
+    ws, p, nb = on.workspace(ws, logra_sketch_experts_workspace_bytes(m, E, N, code))
+    on.call(load_library().logra_sketch_experts, ctypes.byref(m), E, int(id_stride), N, code, _ptr(offsets),
+            _ptr(order), int(topk), _ptr(X), ldx, X.size(0), _ptr(dY), lddy, _ptr(S), 1 if accumulate else 0, p, nb)

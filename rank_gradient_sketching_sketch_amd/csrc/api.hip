@@ -4,6 +4,7 @@
 // every buffer, workspace included, comes from the caller.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "../../include/logra.h"
@@ -636,6 +637,262 @@ logra_status logra_ts_apply(const logra_matrix *m, const void *ws, size_t ws_byt
     if (!ws || ws_bytes < need || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
     return from_hip(launch_ts_apply(m->d, m->k, ws, W, w_dtype == LOGRA_BF16 ? 1 : 0, ldw, lr * scale,
                                     static_cast<hipStream_t>(stream)));
+}
+
+// ---- global gradient norm and clipping ----
+
+namespace {
+
+bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// A list as the launching calls take it.
+bool grad_list_ok(const logra_grad_list *g) {
+    return g && g->n >= 0 && g->chunks >= 0 && (g->n == 0 || (g->table && aligned16(g->table)));
+}
+
+struct GradSpan {
+    uint64_t begin, end;
+    bool operator<(const GradSpan &o) const { return begin < o.begin; }
+};
+
+}  // namespace
+
+size_t logra_grad_table_bytes(int64_t n) {
+    return n < 0 || n > (1 << 20) ? 0 : static_cast<size_t>(n) * sizeof(GradEntry);
+}
+
+logra_status logra_grad_list_pack(int64_t n, const logra_grad_tensor *tensors, void *table_host, size_t table_bytes,
+                                  logra_grad_list *list) {
+    if (n < 0 || n > (1 << 20) || !list || (n > 0 && (!tensors || !table_host)) || !aligned_to(table_host, 8))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (table_bytes < logra_grad_table_bytes(n)) return LOGRA_ERR_WORKSPACE;
+    constexpr int64_t kMost = 1ll << 40;
+    // the address ranges, in the table's memory before the table takes it
+    GradSpan *span = static_cast<GradSpan *>(table_host);
+    int64_t n_span = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const logra_grad_tensor &t = tensors[i];
+        if (t.rows < 0 || t.cols < 0 || t.ld < t.cols) return LOGRA_ERR_INVALID_ARGUMENT;
+        if (t.dtype != LOGRA_F32 && t.dtype != LOGRA_BF16) return LOGRA_ERR_UNSUPPORTED;
+        if (t.rows == 0 || t.cols == 0) continue;
+        const int64_t el = t.dtype == LOGRA_BF16 ? 2 : 4;
+        if (!t.data || !aligned_to(t.data, el)) return LOGRA_ERR_INVALID_ARGUMENT;
+        if (t.rows > kMost || t.cols > kMost || t.ld > kMost || t.rows > kMost / t.cols || t.rows > kMost / t.ld)
+            return LOGRA_ERR_UNSUPPORTED;
+        const uint64_t a = reinterpret_cast<uint64_t>(t.data);
+        span[n_span++] = GradSpan{a, a + static_cast<uint64_t>(((t.rows - 1) * t.ld + t.cols) * el)};
+    }
+    std::sort(span, span + n_span);
+    for (int64_t i = 1; i < n_span; ++i)
+        if (span[i].begin < span[i - 1].end) return LOGRA_ERR_INVALID_ARGUMENT;
+    GradEntry *table = static_cast<GradEntry *>(table_host);
+    logra_grad_list out = {};
+    uint64_t hash = 0xCBF29CE484222325ull;      // FNV-1a over rows and cols
+    auto mix = [&](int64_t v) {
+        for (int b = 0; b < 64; b += 8) hash = (hash ^ ((static_cast<uint64_t>(v) >> b) & 0xFF)) * 0x100000001B3ull;
+    };
+    for (int64_t i = 0; i < n; ++i) {
+        const logra_grad_tensor &t = tensors[i];
+        GradEntry e;
+        e.addr = reinterpret_cast<uint64_t>(t.data);
+        e.rows = t.rows;
+        e.cols = t.cols;
+        e.ld = t.rows == 1 ? t.cols : t.ld;
+        e.bf16 = t.dtype == LOGRA_BF16;
+        e.first = out.chunks;
+        if (t.rows > 0 && t.cols > 0) {
+            if (t.cols <= kGradChunk) {
+                e.rows_per_chunk = static_cast<int32_t>(kGradChunk / t.cols);
+                e.chunks = (t.rows + e.rows_per_chunk - 1) / e.rows_per_chunk;
+            } else {
+                const int64_t segs = (t.cols + kGradChunk - 1) / kGradChunk;
+                e.seg_len = static_cast<int32_t>(((t.cols + segs - 1) / segs + 7) / 8 * 8);
+                e.segs_per_row = static_cast<int32_t>((t.cols + e.seg_len - 1) / e.seg_len);
+                e.chunks = t.rows * e.segs_per_row;
+            }
+        }
+        out.chunks += e.chunks;
+        out.elements += t.rows * t.cols;
+        if (out.elements > (kMost << 4)) return LOGRA_ERR_UNSUPPORTED;
+        mix(t.rows);
+        mix(t.cols);
+        table[i] = e;
+    }
+    out.n = static_cast<int32_t>(n);
+    out.shapes = hash;
+    *list = out;
+    return LOGRA_OK;
+}
+
+size_t logra_grad_workspace_bytes(const logra_grad_list *list) {
+    return list && list->chunks >= 0 ? static_cast<size_t>(grad_workgroups(list->chunks)) * sizeof(double) : 0;
+}
+
+logra_status logra_grad_norm(const logra_grad_list *list, float *norm, void *ws, size_t ws_bytes, void *stream) {
+    if (!grad_list_ok(list) || !norm || !aligned_to(norm, 4)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
+    return from_hip(launch_grad_norm(static_cast<const GradEntry *>(list->table), list->n, list->chunks,
+                                     static_cast<double *>(ws), norm, static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list *out, float max_norm, float *norm,
+                             float *coef, void *ws, size_t ws_bytes, void *stream) {
+    if (!grad_list_ok(list) || !norm || !coef || norm == coef) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!aligned_to(norm, 4) || !aligned_to(coef, 4) || !(max_norm >= 0.f)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!out) out = list;
+    if (!grad_list_ok(out) || out->n != list->n || out->chunks != list->chunks || out->shapes != list->shapes)
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
+    return from_hip(launch_grad_clip(static_cast<const GradEntry *>(list->table),
+                                     static_cast<const GradEntry *>(out->table), list->n, list->chunks, max_norm,
+                                     static_cast<double *>(ws), norm, coef, static_cast<hipStream_t>(stream)));
+}
+
+// ---- rows sorted by expert, and back ----
+
+namespace {
+
+constexpr int64_t kMaxPairs = 1ll << 26, kMaxExpertTokens = 1ll << 23;
+
+logra_status check_pairs(int64_t T, int topk) {
+    if (T < 0 || topk < 1) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (topk > kMaxTopK || T > kMaxExpertTokens || T * topk > kMaxPairs) return LOGRA_ERR_UNSUPPORTED;
+    return LOGRA_OK;
+}
+
+// One array of rows: n of them, h wide.
+bool rows_ok(const void *p, int64_t ld, int64_t n, int64_t h, int dtype) {
+    return n == 0 || (p && ld >= h && aligned_to(p, dtype == LOGRA_BF16 ? 2 : 4));
+}
+
+logra_status check_rows(int64_t T, int topk, int64_t h, int dtype, const int32_t *slots, const float *w,
+                        int64_t n_rows) {
+    const logra_status e = check_pairs(T, topk);
+    if (e != LOGRA_OK) return e;
+    if (h < 1 || n_rows < 0) return LOGRA_ERR_INVALID_ARGUMENT;
+    if ((dtype != LOGRA_F32 && dtype != LOGRA_BF16) || h > (1ll << 30)) return LOGRA_ERR_UNSUPPORTED;
+    if (T > 0 && (!slots || !aligned_to(slots, 4) || !aligned_to(w, 4))) return LOGRA_ERR_INVALID_ARGUMENT;
+    return LOGRA_OK;
+}
+
+int elem_bytes(int dtype) { return dtype == LOGRA_BF16 ? 2 : 4; }
+
+}  // namespace
+
+size_t logra_expert_sort_workspace_bytes(int64_t T, int topk, int n_experts) {
+    if (check_pairs(T, topk) != LOGRA_OK || n_experts < 1 || n_experts > kMaxExperts) return 0;
+    return expert_sort_workspace(T * topk, n_experts);
+}
+
+logra_status logra_expert_sort(int64_t T, int topk, int n_experts, const void *ids, int id_bytes, int64_t ld_ids,
+                               int32_t *offsets, int32_t *order, int32_t *slots, void *ws, size_t ws_bytes,
+                               void *stream) {
+    const logra_status e = check_pairs(T, topk);
+    if (e != LOGRA_OK) return e;
+    if (n_experts < 1 || (id_bytes != 4 && id_bytes != 8) || !offsets || !aligned_to(offsets, 4))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (n_experts > kMaxExperts) return LOGRA_ERR_UNSUPPORTED;
+    if (T > 0 && (!ids || !aligned_to(ids, id_bytes) || ld_ids < topk || !order || !aligned_to(order, 4) || !slots ||
+                  !aligned_to(slots, 4)))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    const size_t need = expert_sort_workspace(T * topk, n_experts);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return LOGRA_ERR_WORKSPACE;
+    return from_hip(launch_expert_sort(T, topk, n_experts, ids, id_bytes, ld_ids, offsets, order, slots, ws,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_expert_gather(int64_t T, int topk, int64_t h, int dtype, const void *X, int64_t ldx,
+                                 const int32_t *slots, const float *w, void *Xs, int64_t ldxs, int64_t n_rows,
+                                 void *stream) {
+    const logra_status e = check_rows(T, topk, h, dtype, slots, w, n_rows);
+    if (e != LOGRA_OK) return e;
+    if (!rows_ok(X, ldx, T, h, dtype) || !rows_ok(Xs, ldxs, n_rows, h, dtype)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (T == 0 || n_rows == 0) return LOGRA_OK;
+    return from_hip(launch_expert_gather(T, topk, h, elem_bytes(dtype), X, ldx, slots, w, Xs, ldxs, n_rows,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_expert_combine(int64_t T, int topk, int64_t h, int dtype, const void *Ys, int64_t ldys,
+                                  int64_t n_rows, const int32_t *slots, const float *w, void *Y, int64_t ldy,
+                                  void *stream) {
+    const logra_status e = check_rows(T, topk, h, dtype, slots, w, n_rows);
+    if (e != LOGRA_OK) return e;
+    if (!rows_ok(Ys, ldys, n_rows, h, dtype) || !rows_ok(Y, ldy, T, h, dtype)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (T == 0) return LOGRA_OK;
+    return from_hip(launch_expert_combine(T, topk, h, elem_bytes(dtype), Ys, ldys, n_rows, slots, w, Y, ldy,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_expert_combine_backward(int64_t T, int topk, int64_t h, int dtype, const void *dY, int64_t lddy,
+                                           const void *Ys, int64_t ldys, int64_t n_rows, const int32_t *slots,
+                                           const float *w, void *dYs, int64_t lddys, float *dw, void *stream) {
+    const logra_status e = check_rows(T, topk, h, dtype, slots, w, n_rows);
+    if (e != LOGRA_OK) return e;
+    if (!rows_ok(dY, lddy, T, h, dtype) || !rows_ok(Ys, ldys, n_rows, h, dtype) ||
+        !rows_ok(dYs, lddys, n_rows, h, dtype))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!w || !dw || !aligned_to(dw, 4))) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (T == 0) return LOGRA_OK;
+    return from_hip(launch_expert_combine_backward(T, topk, h, elem_bytes(dtype), dY, lddy, Ys, ldys, slots, w, dYs,
+                                                   lddys, n_rows, dw, static_cast<hipStream_t>(stream)));
+}
+
+// ---- the sketch over experts ----
+
+static logra_status check_sketch_experts(const logra_matrix *m, int n_experts, int64_t N, int act_dtype) {
+    if (!matrix_ok(m) || n_experts < 1 || N < 0) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (act_dtype != LOGRA_F32 && act_dtype != LOGRA_BF16) return LOGRA_ERR_UNSUPPORTED;
+    if (n_experts > kMaxExperts || N > kMaxPairs) return LOGRA_ERR_UNSUPPORTED;
+    if (act_dtype == LOGRA_BF16 ? !bf16_rank_ok(m->r) || m->d % 8 || m->k % 8 : m->r > 1024)
+        return LOGRA_ERR_UNSUPPORTED;
+    return LOGRA_OK;
+}
+
+size_t logra_sketch_experts_workspace_bytes(const logra_matrix *m, int n_experts, int64_t N, int act_dtype) {
+    if (check_sketch_experts(m, n_experts, N, act_dtype) != LOGRA_OK) return 0;
+    return plan_expert_sketch(N, n_experts, m->d, m->k, static_cast<int>(m->r), act_dtype == LOGRA_BF16).total;
+}
+
+logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t id_stride, int64_t N, int act_dtype,
+                                  const int32_t *offsets, const int32_t *order, int topk, const void *X, int64_t ldx,
+                                  int64_t x_rows, const void *dY, int64_t lddy, float *S, int accumulate, void *ws,
+                                  size_t ws_bytes, void *stream) {
+    const logra_status e = check_sketch_experts(m, n_experts, N, act_dtype);
+    if (e != LOGRA_OK) return e;
+    const bool bf16 = act_dtype == LOGRA_BF16;
+    if (!offsets || !aligned_to(offsets, 4) || !S || !aligned16(S)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (x_rows < 0 || (order ? topk < 1 || !aligned_to(order, 4) : x_rows < N)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (N > 0) {
+        if (!dY || lddy < m->d || (x_rows > 0 && (!X || ldx < m->k))) return LOGRA_ERR_INVALID_ARGUMENT;
+        if (bf16 ? lddy % 8 || ldx % 8 || !aligned16(X) || !aligned16(dY) : !aligned_to(X, 4) || !aligned_to(dY, 4))
+            return LOGRA_ERR_INVALID_ARGUMENT;
+    }
+    const ExpertSketchPlan p = plan_expert_sketch(N, n_experts, m->d, m->k, static_cast<int>(m->r), bf16);
+    if (p.total > 0 && (!ws || ws_bytes < p.total || !aligned16(ws))) return LOGRA_ERR_WORKSPACE;
+    if (N == 0 && accumulate) return LOGRA_OK;
+    ExpertSketchArgs a;
+    a.E = n_experts;
+    a.R = static_cast<int>(m->r);
+    a.topk = order ? topk : 1;
+    a.N = N;
+    a.d = m->d;
+    a.k = m->k;
+    const auto h = [](uint64_t x) { return splitmix_finalize(x + kGolden); };
+    a.prefix = h(h(m->seed) ^ m->step);     // expert e's key is h(prefix ^ id), see stream_key
+    a.first_id = m->matrix_id;
+    a.id_stride = id_stride;
+    a.c = inv_sqrt_rank(m->r);
+    a.offsets = offsets;
+    a.order = order;
+    a.X = X;
+    a.dY = dY;
+    a.ldx = ldx;
+    a.x_rows = x_rows;
+    a.lddy = lddy;
+    a.S = S;
+    a.accumulate = accumulate ? 1 : 0;
+    a.ws = ws;
+    return from_hip(launch_expert_sketch(a, bf16 ? 1 : 0, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

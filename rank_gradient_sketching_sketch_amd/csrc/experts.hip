@@ -1,0 +1,393 @@
+// Rows sorted by expert and back: what stands between a token's activations
+// and the experts' projections (whose sketches are in sketch_experts.hip).
+//
+// Pair p = t K + j is token t's j-th choice of expert, ids[t][j]; choices
+// outside 0 .. E-1 are dropped. The pairs sorted by expert (pairs of one
+// expert in their own order) have places 0 .. N_kept - 1:
+//   offsets[e] .. offsets[e + 1]  the places of expert e's pairs
+//   order[place] = p              (-1 behind the last)
+//   slots[p] = place              (-1 for a dropped pair)
+// and with optional weights w[t][j] (absent: 1)
+//   gather            Xs[slots[t][j]] = w[t][j] X[t]
+//   combine           Y[t] = sum_j w[t][j] Ys[slots[t][j]]
+//   combine backward  dYs[slots[t][j]] = w[t][j] dY[t],  dw[t][j] = <dY[t], Ys[slots[t][j]]>.
+// The gradient of gather is combine, with the same weights.
+//
+// All of them are bound by memory. The row kernels give each token a
+// workgroup, so that a token's own row crosses the memory bus once however
+// many experts it goes to. Rows of Xs and dYs that no pair maps to are not
+// written.
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace logra {
+
+// ------------------------------------------------------------------- sort --
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortSingle = 8192;     // pairs one workgroup sorts alone
+constexpr int kSortMaxBlocks = 256;
+
+struct SortPlan {
+    int blocks = 1;
+    int chunk = 0;     // pairs per workgroup, a multiple of 1024
+};
+
+static SortPlan plan_sort(int64_t n) {
+    SortPlan p;
+    if (n <= kSortSingle) {
+        p.chunk = static_cast<int>((n + 1023) / 1024 * 1024);
+        return p;
+    }
+    const int64_t c = (n + kSortMaxBlocks - 1) / kSortMaxBlocks;
+    p.chunk = static_cast<int>((c < 2048 ? 2048 : c) + 1023) / 1024 * 1024;
+    p.blocks = static_cast<int>((n + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+struct SortIds {
+    const void *ids;
+    int64_t ld;
+    int K, E, wide;
+    // expert of pair p, E for a dropped one
+    __device__ __forceinline__ int operator()(int64_t p) const {
+        const uint32_t t = static_cast<uint32_t>(p) / static_cast<uint32_t>(K);
+        const int64_t at = t * ld + (static_cast<uint32_t>(p) - t * static_cast<uint32_t>(K));
+        const int64_t id = wide ? reinterpret_cast<const int64_t *>(ids)[at]
+                                : static_cast<int64_t>(reinterpret_cast<const int32_t *>(ids)[at]);
+        return id >= 0 && id < E ? static_cast<int>(id) : E;
+    }
+};
+
+// hist[block][e]: the pairs of expert e in the block's chunk.
+__global__ __launch_bounds__(kSortThreads) void sort_hist_kernel(SortIds ids, int64_t n, int chunk,
+                                                                 int32_t *__restrict__ hist) {
+    __shared__ int cnt[kMaxExperts];
+    const int E = ids.E;
+    for (int e = threadIdx.x; e < E; e += kSortThreads) cnt[e] = 0;
+    __syncthreads();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int64_t p1 = min(n, p0 + chunk);
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += kSortThreads) {
+        const int e = ids(p);
+        if (e < E) atomicAdd(&cnt[e], 1);   // whole numbers: the order does not matter
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kSortThreads) hist[static_cast<int64_t>(blockIdx.x) * E + e] = cnt[e];
+}
+
+// Lanes of the wave that hold the same value (bits of it compared).
+__device__ __forceinline__ uint64_t match_lanes(int v, int bits) {
+    uint64_t m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t s = __ballot((v >> b) & 1);
+        m &= ((v >> b) & 1) ? s : ~s;
+    }
+    return m;
+}
+
+// Places of one chunk's pairs. Each wave takes a contiguous part of the
+// chunk in groups of 64 and keeps its own counter per expert in LDS, so the
+// pairs of an expert keep their order: within a group the place follows from
+// the lanes before it that hold the same expert.
+__global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids, int64_t n, int chunk, int bits,
+                                                                    const int32_t *__restrict__ hist,
+                                                                    int32_t *__restrict__ offsets,
+                                                                    int32_t *__restrict__ order,
+                                                                    int32_t *__restrict__ slots) {
+    extern __shared__ int lds[];
+    const int E = ids.E;
+    int *cnt = lds;                              // [kSortWaves][E]
+    int *total = lds + kSortWaves * E;           // [E] pairs of the expert, then its first place
+    int *before = total + E;                     // [E] pairs of the expert in the chunks before this one
+    __shared__ int wave_sum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int i = tid; i < (kSortWaves + 2) * E; i += kSortThreads) lds[i] = 0;
+    __syncthreads();
+
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int per_wave = chunk / kSortWaves;     // a multiple of 64
+    const int64_t w0 = p0 + static_cast<int64_t>(wave) * per_wave;
+    int *mine = cnt + wave * E;
+    for (int64_t g = w0; g < w0 + per_wave && g < n; g += 64) {
+        const int e = g + lane < n ? ids(g + lane) : E;
+        if (e < E) atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+
+    if (hist) {
+        const int parts = max(1, kSortThreads / E);
+        const int part = tid / E;
+        if (part < parts)
+            for (int e = tid - part * E; e < E; e += kSortThreads) {
+                int t = 0, b = 0;
+                for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
+                    const int h = hist[static_cast<int64_t>(q) * E + e];
+                    t += h;
+                    b += q < static_cast<int>(blockIdx.x) ? h : 0;
+                }
+                atomicAdd(&total[e], t);
+                atomicAdd(&before[e], b);
+            }
+    } else {
+        for (int e = tid; e < E; e += kSortThreads) {
+            int t = 0;
+            for (int w = 0; w < kSortWaves; ++w) t += cnt[w * E + e];
+            total[e] = t;
+        }
+    }
+    __syncthreads();
+
+    // first place of every expert: exclusive sums of the totals (E <= 1024,
+    // one expert per thread)
+    const int own = tid < E ? total[tid] : 0;
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    int carry = 0, kept = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) carry += wave_sum[w];
+        kept += wave_sum[w];
+    }
+    if (tid < E) {
+        const int first = carry + incl - own;
+        int at = first + before[tid];
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = cnt[w * E + tid];
+            cnt[w * E + tid] = at;
+            at += c;
+        }
+        if (blockIdx.x == 0) offsets[tid] = first;
+    }
+    if (blockIdx.x == 0 && tid == 0) offsets[E] = kept;
+    __syncthreads();
+
+    for (int64_t g = w0; g < w0 + per_wave && g < n; g += 64) {
+        const int64_t p = g + lane;
+        const int e = p < n ? ids(p) : E;
+        const uint64_t same = match_lanes(e, bits);
+        const int rank = __popcll(same & ((1ull << lane) - 1ull));
+        int at = 0;
+        if (e < E) at = mine[e] + rank;
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        if (e < E && rank == 0) mine[e] += __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        if (p < n) {
+            slots[p] = e < E ? at : -1;
+            if (e < E) order[at] = static_cast<int32_t>(p);
+        }
+    }
+    // no pair has the places behind the last kept one
+    for (int64_t s = kept + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; s < n;
+         s += static_cast<int64_t>(gridDim.x) * kSortThreads)
+        order[s] = -1;
+}
+
+size_t expert_sort_workspace(int64_t n, int E) {
+    const SortPlan p = plan_sort(n);
+    return p.blocks > 1 ? static_cast<size_t>(p.blocks) * E * 4 : 0;
+}
+
+hipError_t launch_expert_sort(int64_t T, int K, int E, const void *ids, int id_bytes, int64_t ld_ids,
+                              int32_t *offsets, int32_t *order, int32_t *slots, void *ws, hipStream_t st) {
+    const int64_t n = T * K;
+    const SortPlan p = plan_sort(n);
+    const SortIds s{ids, ld_ids, K, E, id_bytes == 8 ? 1 : 0};
+    int bits = 1;
+    while ((1 << bits) <= E) ++bits;      // values 0 .. E
+    int32_t *hist = p.blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
+    if (hist) hipLaunchKernelGGL(sort_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, st, s, n, p.chunk, hist);
+    hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.blocks), dim3(kSortThreads), (kSortWaves + 2) * E * 4, st, s, n,
+                       p.chunk, bits, hist, offsets, order, slots);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------- rows --
+constexpr int kRowThreads = 256;
+
+typedef u32x4_t u32x4_e2_t __attribute__((aligned(2)));   // rows need only their element's alignment
+typedef u32x4_t u32x4_e4_t __attribute__((aligned(4)));
+
+// A row element type: bf16 (8 to a 16-byte access) or fp32 (4).
+template <int BF16>
+struct RowOf {
+    static constexpr int V = BF16 ? 8 : 4;
+    static __device__ __forceinline__ void load(const char *p, float (&v)[V]) {
+        if (BF16) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_e2_t *>(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = bf16_lo(w[e]);
+                v[(2 * e + 1) % V] = bf16_hi(w[e]);
+            }
+        } else {
+            const u32x4_t w = *reinterpret_cast<const u32x4_e4_t *>(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+        }
+    }
+    static __device__ __forceinline__ void store(char *p, const float (&v)[V]) {
+        u32x4_t w;
+        if (BF16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[(2 * e) % V], v[(2 * e + 1) % V]);
+            *reinterpret_cast<u32x4_e2_t *>(p) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
+            *reinterpret_cast<u32x4_e4_t *>(p) = w;
+        }
+    }
+    // the first n < V elements, the rest zero
+    static __device__ __forceinline__ void load_some(const char *p, int n, float (&v)[V]) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            v[e] = 0.f;
+            if (e < n)
+                v[e] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[e]) << 16)
+                            : reinterpret_cast<const float *>(p)[e];
+        }
+    }
+    static __device__ __forceinline__ void store_some(char *p, int n, const float (&v)[V]) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < n) {
+                if (BF16) reinterpret_cast<uint16_t *>(p)[e] = static_cast<uint16_t>(pack_bf16x2(v[e], 0.f));
+                else reinterpret_cast<float *>(p)[e] = v[e];
+            }
+    }
+    static __device__ __forceinline__ void get(const char *p, int n, float (&v)[V]) {
+        if (n >= V) load(p, v);
+        else load_some(p, n, v);
+    }
+    static __device__ __forceinline__ void put(char *p, int n, const float (&v)[V]) {
+        if (n >= V) store(p, v);
+        else store_some(p, n, v);
+    }
+};
+
+template <int BF16>
+__global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h, const char *__restrict__ X,
+                                                                    int64_t ldx, const int32_t *__restrict__ slots,
+                                                                    const float *__restrict__ w,
+                                                                    char *__restrict__ Xs, int64_t ldxs,
+                                                                    int64_t n_rows) {
+    using R = RowOf<BF16>;
+    constexpr int V = R::V, B = BF16 ? 2 : 4;
+    const int64_t t = blockIdx.x;
+    for (int c = threadIdx.x * V; c < h; c += kRowThreads * V) {
+        float x[V];
+        R::get(X + (t * ldx + c) * B, h - c, x);
+        for (int j = 0; j < K; ++j) {
+            const int64_t s = slots[t * K + j];
+            if (s < 0 || s >= n_rows) continue;
+            float y[V];
+            const float f = w ? w[t * K + j] : 1.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = w ? f * x[e] : x[e];
+            R::put(Xs + (s * ldxs + c) * B, h - c, y);
+        }
+    }
+}
+
+template <int BF16>
+__global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(int K, int h, const char *__restrict__ Ys,
+                                                                     int64_t ldys, int64_t n_rows,
+                                                                     const int32_t *__restrict__ slots,
+                                                                     const float *__restrict__ w,
+                                                                     char *__restrict__ Y, int64_t ldy) {
+    using R = RowOf<BF16>;
+    constexpr int V = R::V, B = BF16 ? 2 : 4;
+    const int64_t t = blockIdx.x;
+    for (int c = threadIdx.x * V; c < h; c += kRowThreads * V) {
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = 0.f;
+        for (int j = 0; j < K; ++j) {
+            const int64_t s = slots[t * K + j];
+            if (s < 0 || s >= n_rows) continue;
+            float x[V];
+            R::get(Ys + (s * ldys + c) * B, h - c, x);
+            const float f = w ? w[t * K + j] : 1.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = fmaf(f, x[e], y[e]);
+        }
+        R::put(Y + (t * ldy + c) * B, h - c, y);
+    }
+}
+
+template <int BF16>
+__global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(
+    int K, int h, const char *__restrict__ dY, int64_t lddy, const char *__restrict__ Ys, int64_t ldys,
+    const int32_t *__restrict__ slots, const float *__restrict__ w, char *__restrict__ dYs, int64_t lddys,
+    int64_t n_rows, float *__restrict__ dw) {
+    using R = RowOf<BF16>;
+    constexpr int V = R::V, B = BF16 ? 2 : 4;
+    __shared__ float part[kRowThreads / 64];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int j = 0; j < K; ++j) {
+        const int64_t s = slots[t * K + j];
+        const bool kept = s >= 0 && s < n_rows;
+        const float f = w[t * K + j];
+        float dot = 0.f;
+        if (kept)
+            for (int c = threadIdx.x * V; c < h; c += kRowThreads * V) {
+                float g[V], y[V];
+                R::get(dY + (t * lddy + c) * B, h - c, g);
+                R::get(Ys + (s * ldys + c) * B, h - c, y);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    dot = fmaf(g[e], y[e], dot);
+                    g[e] *= f;
+                }
+                R::put(dYs + (s * lddys + c) * B, h - c, g);
+            }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+        if (lane == 0) part[wave] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float d = 0.f;
+            for (int i = 0; i < kRowThreads / 64; ++i) d += part[i];
+            dw[t * K + j] = d;
+        }
+        __syncthreads();
+    }
+}
+
+hipError_t launch_expert_gather(int64_t T, int K, int64_t h, int elem, const void *X, int64_t ldx,
+                                const int32_t *slots, const float *w, void *Xs, int64_t ldxs, int64_t n_rows,
+                                hipStream_t st) {
+    auto kernel = elem == 2 ? expert_gather_kernel<1> : expert_gather_kernel<0>;
+    hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
+                       static_cast<const char *>(X), ldx, slots, w, static_cast<char *>(Xs), ldxs, n_rows);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(int64_t T, int K, int64_t h, int elem, const void *Ys, int64_t ldys,
+                                 int64_t n_rows, const int32_t *slots, const float *w, void *Y, int64_t ldy,
+                                 hipStream_t st) {
+    auto kernel = elem == 2 ? expert_combine_kernel<1> : expert_combine_kernel<0>;
+    hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
+                       static_cast<const char *>(Ys), ldys, n_rows, slots, w, static_cast<char *>(Y), ldy);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_backward(int64_t T, int K, int64_t h, int elem, const void *dY, int64_t lddy,
+                                          const void *Ys, int64_t ldys, const int32_t *slots, const float *w,
+                                          void *dYs, int64_t lddys, int64_t n_rows, float *dw, hipStream_t st) {
+    auto kernel = elem == 2 ? expert_combine_backward_kernel<1> : expert_combine_backward_kernel<0>;
+    hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
+                       static_cast<const char *>(dY), lddy, static_cast<const char *>(Ys), ldys, slots, w,
+                       static_cast<char *>(dYs), lddys, n_rows, dw);
+    return hipGetLastError();
+}
+
+}  // namespace logra

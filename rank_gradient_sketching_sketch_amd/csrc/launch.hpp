@@ -204,4 +204,66 @@ hipError_t launch_ts_update(int64_t d, int64_t k, const float *S_L, const float 
 hipError_t launch_ts_apply(int64_t d, int64_t k, const void *ws, void *W, int w_bf16, int64_t ldw, float step,
                            hipStream_t st);
 
+// Global gradient norm and clipping. One table entry per tensor (rows x cols,
+// row stride ld); its chunks are rows_per_chunk whole rows where a row is
+// shorter than a chunk, else segs_per_row segments of seg_len columns per row
+// (then rows_per_chunk is 0). The cut depends on rows and cols alone, so two
+// lists of the same shapes have the same chunks.
+constexpr int kGradChunk = 8192;        // elements of a chunk, at most
+constexpr int kGradMaxWGs = 2048;
+struct GradEntry {
+    uint64_t addr = 0;
+    int64_t rows = 0, cols = 0, ld = 0;
+    int64_t first = 0, chunks = 0;      // the tensor's chunks in the list
+    int32_t rows_per_chunk = 0, segs_per_row = 0, seg_len = 0;
+    int32_t bf16 = 0;
+};
+int grad_workgroups(int64_t chunks);
+hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, double *partials, float *norm,
+                            hipStream_t st);
+hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, float max_norm,
+                            double *partials, float *norm, float *coef, hipStream_t st);
+
+// Pairs (token, choice) sorted by expert and rows moved along. elem: bytes
+// of an element of the rows (2 = bf16, 4 = fp32).
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 64;
+size_t expert_sort_workspace(int64_t n_pairs, int n_experts);
+hipError_t launch_expert_sort(int64_t T, int K, int E, const void *ids, int id_bytes, int64_t ld_ids,
+                              int32_t *offsets, int32_t *order, int32_t *slots, void *ws, hipStream_t st);
+hipError_t launch_expert_gather(int64_t T, int K, int64_t h, int elem, const void *X, int64_t ldx,
+                                const int32_t *slots, const float *w, void *Xs, int64_t ldxs, int64_t n_rows,
+                                hipStream_t st);
+hipError_t launch_expert_combine(int64_t T, int K, int64_t h, int elem, const void *Ys, int64_t ldys,
+                                 int64_t n_rows, const int32_t *slots, const float *w, void *Y, int64_t ldy,
+                                 hipStream_t st);
+hipError_t launch_expert_combine_backward(int64_t T, int K, int64_t h, int elem, const void *dY, int64_t lddy,
+                                          const void *Ys, int64_t ldys, const int32_t *slots, const float *w,
+                                          void *dYs, int64_t lddys, int64_t n_rows, float *dw, hipStream_t st);
+
+// The sketch over experts. Workspace: the per-expert and per-item tables,
+// then the projection, then the partial sketches of experts whose rows are
+// split over several items.
+struct ExpertSketchPlan {
+    int chunk = 0;            // rows of an item at most (a multiple of 32)
+    int64_t p_blocks = 0;     // 32-row blocks of the projection, at most
+    int64_t items = 0;        // items at most
+    int64_t extras = 0;       // partial sketches at most
+    size_t table_bytes = 0, p_bytes = 0, total = 0;
+};
+ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int R, int bf16);
+struct ExpertSketchArgs {
+    int E = 0, R = 0, topk = 1;
+    int64_t N = 0, d = 0, k = 0;
+    uint64_t prefix = 0, first_id = 0, id_stride = 0;   // expert e's key: h(prefix ^ (first_id + e id_stride))
+    float c = 0.f;
+    const int32_t *offsets = nullptr, *order = nullptr;
+    const void *X = nullptr, *dY = nullptr;
+    int64_t ldx = 0, x_rows = 0, lddy = 0;
+    float *S = nullptr;
+    int accumulate = 0;
+    void *ws = nullptr;
+};
+hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t st);
+
 }  // namespace logra
