@@ -866,6 +866,9 @@ logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t
         if (!dY || lddy < m->d || (x_rows > 0 && (!X || ldx < m->k))) return LOGRA_ERR_INVALID_ARGUMENT;
         if (bf16 ? lddy % 8 || ldx % 8 || !aligned16(X) || !aligned16(dY) : !aligned_to(X, 4) || !aligned_to(dY, 4))
             return LOGRA_ERR_INVALID_ARGUMENT;
+        // X is read through one buffer view, dY through one per 32 rows
+        if (bf16 && ((x_rows > 0 && ldx > ((1ll << 31) - 1) / 2 / x_rows) || lddy > (1ll << 24)))
+            return LOGRA_ERR_UNSUPPORTED;
     }
     const ExpertSketchPlan p = plan_expert_sketch(N, n_experts, m->d, m->k, static_cast<int>(m->r), bf16);
     if (p.total > 0 && (!ws || ws_bytes < p.total || !aligned16(ws))) return LOGRA_ERR_WORKSPACE;

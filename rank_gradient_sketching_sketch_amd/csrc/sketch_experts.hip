@@ -12,12 +12,17 @@
 // The row counts live on the device, so the grids cover the most that any
 // counts could need and each workgroup finds its expert from the offsets.
 //
-// P is kept as two bf16 terms, P = hi + lo with hi = bf16(P) and
-// lo = bf16(P - hi): their sum is off by 2^-16 of P at most (each rounding is
-// 2^-8 of what it rounds), so S has nearly the precision of fp32 products
-// although dY^T P runs on the bf16 matrix cores (dY is bf16 exactly). One bf16
-// term alone would leave 2^-8.
+// P is kept in fp32 and taken apart by the second product into three bf16
+// terms, P = p0 + p1 + p2 with p0 = bf16(P), p1 = bf16(P - p0),
+// p2 = bf16(P - p0 - p1): each rounding is 2^-8 of what it rounds, so their
+// sum is within 2^-24 of P and S has the precision of fp32 products although
+// dY^T P runs on the bf16 matrix cores (dY is bf16 exactly). One term would
+// leave 2^-8 per product, two 2^-16. Storing the terms instead of the value
+// would cost half as many bytes again on the path that bounds that product.
+#include <type_traits>
+
 #include "common.hpp"
+#include "fold_body.hpp"
 #include "launch.hpp"
 #include "signs.hpp"
 
@@ -34,6 +39,28 @@ __device__ __forceinline__ EsRange es_range(const int32_t *offsets, int e, int N
     const int a = min(max(offsets[e], 0), N), b = min(max(offsets[e + 1], 0), N);
     return EsRange{a, max(0, b - a)};
 }
+// The same for an expert that all lanes of the wave name.
+__device__ __forceinline__ EsRange es_range_uniform(const int32_t *offsets, int e, int N) {
+    const EsRange r = es_range(offsets, e, N);
+    return EsRange{__builtin_amdgcn_readfirstlane(r.begin), __builtin_amdgcn_readfirstlane(r.count)};
+}
+
+// Buffer views: loads at or past num_records return zero, so kEsOob masks
+// one. (Loads under a condition instead would leave the number of requests in
+// flight unknown to the compiler, which then waits for all of them.)
+constexpr uint32_t kEsOob = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t es_view(const void *p, uint32_t bytes) {
+    // in scalar registers whatever the compiler knows of them: a view in
+    // vector registers costs a loop over the lanes at every use
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a)));
+    const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32)));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000);
+}
+__device__ __forceinline__ u32x4_t es_load(__amdgpu_buffer_rsrc_t v, uint32_t off) {
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(v, off, 0, 0));
+}
 
 // What every wave works out from the offsets: the expert that holds unit u
 // when expert e holds units(count_e) consecutive ones, and the sums before it.
@@ -44,11 +71,16 @@ struct EsPlace {
 
 __device__ __forceinline__ int es_items(int count, int chunk) { return count > chunk ? (count + chunk - 1) / chunk : 1; }
 
-// by_items: units are items (es_items), else 32-row blocks of P. All lanes
-// of the wave call it.
-__device__ __forceinline__ EsPlace es_find(const int32_t *offsets, int E, int N, int chunk, int u, bool by_items) {
+// unit_rows > 0: units of that many rows; 0: units are items (es_items), and
+// those of experts with more than half an item's rows come first, then those
+// with more than an eighth, then the rest, so that long items do not start
+// last. All lanes of the wave call it.
+__device__ __forceinline__ EsPlace es_find(const int32_t *offsets, int E, int N, int chunk, int u, int unit_rows) {
     const int lane = threadIdx.x & 63;
-    int before_u = 0, before_b = 0, before_x = 0;
+    EsPlace p{-1, 0, 0, 0};
+    int before_u = 0;
+    for (int size = unit_rows ? 2 : 0; size < 3 && p.expert < 0; ++size) {
+    int before_b = 0, before_x = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
         const int e = e0 + lane;
         int nb = 0, nx = 0, nu = 0;
@@ -56,7 +88,8 @@ __device__ __forceinline__ EsPlace es_find(const int32_t *offsets, int E, int N,
             const int count = es_range(offsets, e, N).count;
             nb = (count + kEsTokens - 1) / kEsTokens;
             nx = es_items(count, chunk) - 1;
-            nu = by_items ? nx + 1 : nb;
+            const int of = 2 * count > chunk ? 0 : 8 * count > chunk ? 1 : 2;
+            nu = unit_rows ? (count + unit_rows - 1) / unit_rows : of == size ? nx + 1 : 0;
         }
         int iu = nu, ib = nb, ix = nx;       // inclusive sums over the lanes
 #pragma unroll
@@ -71,18 +104,20 @@ __device__ __forceinline__ EsPlace es_find(const int32_t *offsets, int E, int N,
         const uint64_t past = __ballot(before_u + iu > u);
         if (past) {
             const int l = __builtin_ctzll(past);
-            EsPlace p;
             p.expert = e0 + l;
-            p.index = u - (before_u + __shfl(iu - nu, l));
-            p.blocks = before_b + __shfl(ib - nb, l);
-            p.extras = before_x + __shfl(ix - nx, l);
-            return p;
+            p.index = u - before_u - __builtin_amdgcn_readlane(iu - nu, l);
+            p.blocks = before_b + __builtin_amdgcn_readlane(ib - nb, l);
+            p.extras = before_x + __builtin_amdgcn_readlane(ix - nx, l);
+            break;
         }
-        before_u += __shfl(iu, 63);
-        before_b += __shfl(ib, 63);
-        before_x += __shfl(ix, 63);
+        before_u += __builtin_amdgcn_readlane(iu, 63);
+        before_b += __builtin_amdgcn_readlane(ib, 63);
+        before_x += __builtin_amdgcn_readlane(ix, 63);
     }
-    return EsPlace{-1, 0, 0, 0};
+    }
+    // the same in all lanes: kept in scalar registers
+    return EsPlace{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.index),
+                   __builtin_amdgcn_readfirstlane(p.blocks), __builtin_amdgcn_readfirstlane(p.extras)};
 }
 
 __device__ __forceinline__ uint64_t es_key(const ExpertSketchArgs &a, int e) {
@@ -108,7 +143,7 @@ constexpr int kEsWaves = 8, kEsWords = 8;
 
 template <int R>
 __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int chunk, int K,
-                                                         uint16_t *__restrict__ P) {
+                                                         float *__restrict__ P) {
     constexpr int RT = R < 128 ? R : 128, NB = RT / 16, MB = 2;
     constexpr int kTileLd = kEsTokens + 4;
     constexpr int kTable = kEsWaves * kEsWords * RT * 8, kTiles = kEsWaves * RT * kTileLd * 4;
@@ -119,9 +154,9 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int l0 = blockIdx.y * RT;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, false);
+    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, kEsTokens);
     if (at.expert < 0) return;
-    const EsRange rows = es_range(a.offsets, at.expert, static_cast<int>(a.N));
+    const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int n = min(kEsTokens, rows.count - at.index * kEsTokens);       // rows of this block
     const uint64_t key = es_key(a, at.expert);
 
@@ -189,66 +224,250 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
         for (int nb = 0; nb < NB; ++nb)
             *reinterpret_cast<f32x4_t *>(&tile[(wave * RT + 16 * nb + i16) * kTileLd + 16 * mb + 4 * g]) = acc[mb][nb];
     __syncthreads();
-    // eight rows of one column per thread: 16 bytes of each term
-    for (int q = tid; q < RT * 4; q += 512) {
-        const int col = q >> 2, t = 8 * (q & 3);
-        float v[8];
+    for (int q = tid; q < RT * 8; q += 512) {      // four rows of one column
+        const int col = q >> 3, t = 4 * (q & 7);
+        f32x4_t v = zero_f32x4();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int w = 0; w < kEsWaves; ++w) v += *reinterpret_cast<const f32x4_t *>(&tile[(w * RT + col) * kTileLd + t]);
+        *reinterpret_cast<f32x4_t *>(P + (static_cast<int64_t>(blockIdx.x) * R + l0 + col) * kEsTokens + t) = a.c * v;
+    }
+}
+
+// The same product for calls with many rows and r >= 128: up to 128 rows of
+// one expert and 128 columns per workgroup, on 32x32x16 matrix instructions.
+// Expanding a sign fragment costs nine vector instructions, as many issue
+// slots as four of the matrix instructions it feeds take, so the rows a
+// fragment serves set the rate: each wave holds all 128 rows (four row
+// blocks) of 64 columns, two waves across the columns, two across k, whose
+// tiles are added through LDS in order. X goes through LDS in steps of 64
+// columns of k per part, two buffers, requested two steps ahead; each lane
+// hashes the one sign word of its column and step, a step ahead. Row blocks
+// without rows are skipped.
+constexpr int kEsWideRows = 128, kEsWideCols = 128;
+constexpr int kEsXRow = 72;            // bf16 per LDS row of 64 (16 bytes of padding against bank conflicts)
+constexpr int kEsXBuf = 2 * kEsWideRows * kEsXRow;      // elements of one buffer (both k parts)
+constexpr int kEsTileLd = kEsWideRows + 4;
+static_assert(kEsWideCols * kEsTileLd * 4 <= 4 * kEsXBuf, "the added tile fits the X buffers");
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+
+// D = A(32x16 bf16) * B(16x32 bf16) + C. Lane L holds A[L%32][8*(L/32) .. +7],
+// B[8*(L/32) .. +7][L%32] and D[8*(i/4) + 4*(L/32) + i%4][L%32], i = 0 .. 15.
+__device__ __forceinline__ f32x16_t mfma_bf16_32(u32x4_t a, u32x4_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                  0, 0, 0);
+}
+
+// Byte `sel` of a sign word (its number in bytes 0 and 2 of sel, 0x0C in the
+// others) as eight bf16 +-1: the byte goes to both halves of a dword, then one
+// packed shift brings two of its bits to the sign positions.
+__device__ __forceinline__ u32x4_t es_signs(uint64_t word, uint32_t sel, uint32_t one) {
+    const uint32_t z = __builtin_amdgcn_perm(static_cast<uint32_t>(word >> 32), static_cast<uint32_t>(word), sel);
+    const u16x2_t v = __builtin_bit_cast(u16x2_t, z);
+    u32x4_t r;
 #pragma unroll
-        for (int w = 0; w < kEsWaves; ++w) {
-            const float *src = &tile[(w * RT + col) * kTileLd + t];
+    for (int q = 0; q < 4; ++q) {
+        const u16x2_t sh = {static_cast<unsigned short>(15 - 2 * q), static_cast<unsigned short>(14 - 2 * q)};
+        r[q] = (__builtin_bit_cast(uint32_t, v << sh) & 0x80008000u) | one;
+    }
+    return r;
+}
+
+template <int R>
+__global__ __launch_bounds__(256, 2) void es_project_wide_kernel(ExpertSketchArgs a, int chunk, int K,
+                                                                 int64_t p_blocks, float *__restrict__ P) {
+    constexpr int MB = kEsWideRows / 32, NB = 2;
+    __shared__ __attribute__((aligned(16))) char smem[4 * kEsXBuf];
+    __shared__ uint64_t words[4][64];
+    uint16_t *xs = reinterpret_cast<uint16_t *>(smem);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 1, wk = wave >> 1;
+    const int i32 = lane & 31, h = lane >> 5;
+    // both column tiles of a unit on one XCD (workgroup ids are dealt
+    // round-robin over the XCDs), whose L2 then serves the second one's X
+    constexpr int CT = R / kEsWideCols;
+    const int j = blockIdx.x / kXcds;
+    const int unit = j / CT * kXcds + static_cast<int>(blockIdx.x % kXcds);
+    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, unit, kEsWideRows);
+    if (at.expert < 0) return;
+    const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
+    const int r0 = at.index * kEsWideRows;
+    const int n = min(kEsWideRows, rows.count - r0);
+    const int blocks = __builtin_amdgcn_readfirstlane((n + 31) >> 5);
+    const int l0 = j % CT * kEsWideCols + 64 * wn;
+
+    // the four rows of X whose 16-byte pieces this thread moves
+    const int xr = tid >> 3, xc = 8 * (tid & 7);
+    const __amdgpu_buffer_rsrc_t xv = es_view(a.X, static_cast<uint32_t>(a.x_rows * a.ldx * 2));
+    uint32_t xoff[MB];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += src[e];
+    for (int q = 0; q < MB; ++q) {
+        const int i = xr + 32 * q;
+        const int64_t row = i < n ? es_x_row(a, rows.begin + r0 + i) : -1;
+        xoff[q] = row < 0 ? kEsOob : static_cast<uint32_t>((row * a.ldx + xc) * 2);
+    }
+    // columns of k past K are zeros in X, so their signs do not matter
+    const uint64_t first_word = es_key(a, at.expert) + ((static_cast<uint64_t>(l0 + lane) << 32) + 1ull) * kGolden;
+    auto word_at = [&](int i) { return splitmix_finalize(first_word + static_cast<uint64_t>(2 * i + wk) * kGolden); };
+    f32x16_t acc[MB][NB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[mb][nb][e] = 0.f;
+    const uint32_t one_pair = opaque_u32(0x3F803F80u);
+    const int steps = (K + 127) / 128;
+    // the loop over k with M row blocks
+    auto run = [&](auto m_blocks) {
+        constexpr int M = decltype(m_blocks)::value;
+        auto xload = [&](int i, u32x4_t (&x)[2][M]) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int k = 128 * i + 64 * p;
+                const uint32_t past = k + xc < K ? 0u : kEsOob;
+#pragma unroll
+                for (int q = 0; q < M; ++q) x[p][q] = es_load(xv, (xoff[q] + 2u * k) | past);
+            }
+        };
+        u32x4_t x0[2][M], x1[2][M];
+        xload(0, x0);
+        xload(1, x1);
+        uint64_t word = word_at(0);
+        auto step = [&](int i, u32x4_t (&x)[2][M]) {
+            uint16_t *buf = xs + (i & 1) * kEsXBuf;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int q = 0; q < M; ++q)
+                    *reinterpret_cast<u32x4_t *>(buf + (p * kEsWideRows + xr + 32 * q) * kEsXRow + xc) = x[p][q];
+            words[wave][lane] = word;
+            xload(i + 2, x);
+            lds_barrier();
+            const uint16_t *mine = buf + (wk * kEsWideRows + i32) * kEsXRow + 8 * h;
+            uint64_t w[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) w[nb] = words[wave][32 * nb + i32];
+            word = word_at(i + 1);
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                u32x4_t av[M];
+#pragma unroll
+                for (int mb = 0; mb < M; ++mb)
+                    av[mb] = *reinterpret_cast<const u32x4_t *>(mine + 32 * mb * kEsXRow + 16 * kb);
+                const uint32_t sel = 0x0C000C00u + 0x00010001u * (2 * kb + h);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const u32x4_t bf = es_signs(w[nb], sel, one_pair);
+#pragma unroll
+                    for (int mb = 0; mb < M; ++mb) acc[mb][nb] = mfma_bf16_32(av[mb], bf, acc[mb][nb]);
+                }
+            }
+        };
+        int i = 0;
+        for (; i + 1 < steps; i += 2) {
+            step(i, x0);
+            step(i + 1, x1);
         }
-        u32x4_t hi, lo;
+        if (i < steps) step(i, x0);
+    };
+    if (blocks == 1) run(std::integral_constant<int, 1>());
+    else if (blocks == 2) run(std::integral_constant<int, 2>());
+    else if (blocks == 3) run(std::integral_constant<int, 3>());
+    else run(std::integral_constant<int, 4>());
+    // lane (i32, h) of block (mb, nb): rows 32 mb + 8 q + 4 h .. +3 of column i32, q = 0 .. 3
+    float *tile = reinterpret_cast<float *>(smem);
+    auto at_tile = [&](int mb, int nb, int q) {
+        return reinterpret_cast<f32x4_t *>(&tile[(64 * wn + 32 * nb + i32) * kEsTileLd + 32 * mb + 8 * q + 4 * h]);
+    };
+    __syncthreads();
+    if (wk > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = a.c * v[2 * e], y = a.c * v[2 * e + 1];
-            hi[e] = pack_bf16x2(x, y);
-            lo[e] = pack_bf16x2(x - bf16_lo(hi[e]), y - bf16_hi(hi[e]));
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *at_tile(mb, nb, q) = f32x4_t{acc[mb][nb][4 * q], acc[mb][nb][4 * q + 1], acc[mb][nb][4 * q + 2],
+                                                  acc[mb][nb][4 * q + 3]};
+    }
+    __syncthreads();
+    if (wk > 0) return;
+    const int64_t block0 = static_cast<int64_t>(at.blocks) + MB * at.index;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        if (mb >= blocks || block0 + mb >= p_blocks) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                f32x4_t v = *at_tile(mb, nb, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = a.c * (acc[mb][nb][4 * q + e] + v[e]);
+                *reinterpret_cast<f32x4_t *>(P + ((block0 + mb) * R + l0 + 32 * nb + i32) * kEsTokens + 8 * q + 4 * h) = v;
+            }
         }
-        uint16_t *dst = P + (static_cast<int64_t>(blockIdx.x) * 2 * R + l0 + col) * kEsTokens + t;
-        *reinterpret_cast<u32x4_t *>(dst) = hi;
-        *reinterpret_cast<u32x4_t *>(dst + R * kEsTokens) = lo;
     }
 }
 
 // ---------------------------------------------------------- bf16, stage 2 --
 // A workgroup owns one item (at most `chunk` rows of one expert) and kEsRows
-// rows of its S, all r columns: dY is read once and S written once. Four
-// waves split the columns; each step of 32 rows brings the dY tile through
-// LDS (read transposed, the A operand) and P's fragments from the L2.
-constexpr int kEsRows = 64;
+// rows of its S, all r columns: dY is read once and S written once. The waves
+// split the columns; each step of 32 rows brings the dY tile through LDS (read
+// transposed, the A operand) and P from the L2, each piece of the next step
+// requested as soon as this step has taken it apart.
+constexpr int kEsRows = 128;
 
-typedef short es_i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) es_i16x4_t es_lds_i16x4_t;
-__device__ __forceinline__ u32x2_t es_read_tr(const uint16_t *p) {
-    const es_i16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((es_lds_i16x4_t *)p);
-    return __builtin_bit_cast(u32x2_t, v);
+// Eight values of P as MFMA fragments of their three terms.
+constexpr int kEsTerms = 3;
+__device__ __forceinline__ void es_split(u32x4_t lo, u32x4_t hi, u32x4_t (&p)[kEsTerms]) {
+    // what a term leaves, x - term, by a two-element dot product with (-1, 0)
+    // or (0, -1): one instruction instead of a shift and a subtraction. The
+    // constants stay in registers: folded into the instruction, (-1, 0) was
+    // built as the inline constant -1.0, which the hardware reads as (0, -1).
+    const bf16x2_t minus_lo = __builtin_bit_cast(bf16x2_t, opaque_u32(0x0000BF80u));
+    const bf16x2_t minus_hi = __builtin_bit_cast(bf16x2_t, opaque_u32(0xBF800000u));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float x = __uint_as_float(e < 2 ? lo[2 * e] : hi[2 * e - 4]);
+        float y = __uint_as_float(e < 2 ? lo[2 * e + 1] : hi[2 * e - 3]);
+#pragma unroll
+        for (int q = 0; q < kEsTerms; ++q) {
+            const uint32_t w = pack_bf16x2(x, y);
+            p[q][e] = w;
+            x = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), minus_lo, x, false);
+            y = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, w), minus_hi, y, false);
+        }
+    }
 }
 
 template <int R>
-__global__ __launch_bounds__(256) void es_fold_kernel(ExpertSketchArgs a, int chunk, int D, int64_t p_blocks,
-                                                      int64_t max_extras, const uint16_t *__restrict__ P,
-                                                      float *__restrict__ parts) {
-    constexpr int WN = R / 16 < 4 ? R / 16 : 4;         // waves across the columns
+__global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int chunk, int D, int tiles,
+                                                         int items, int64_t p_blocks, int64_t max_extras,
+                                                         const float *__restrict__ P, float *__restrict__ parts) {
+    constexpr int WN = R / 32 < 4 ? R / 32 : 4;         // waves across the columns
     constexpr int WM = 4 / WN;                          // waves across the rows
-    constexpr int NB = R / 16 / WN, MB = kEsRows / 16 / WM;
-    constexpr int kRow = kEsRows;                       // bf16 per LDS row
-    __shared__ __attribute__((aligned(16))) uint16_t lds[2][kEsTokens * kRow];
+    constexpr int NB = R / 32 / WN, MB = kEsRows / 32 / WM;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[2][kEsTokens * kEsRows];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int i16 = lane & 15, g = lane >> 4;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.y, true);
+    const int i32 = lane & 31, h = lane >> 5;
+    // workgroup ids are dealt round-robin over the XCDs: the tiles of an item
+    // go to one XCD, whose L2 then holds its P
+    const int j = blockIdx.x / kXcds;
+    const int item = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), d0 = j % tiles * kEsRows;
+    if (item >= items) return;
+    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, item, 0);
     if (at.expert < 0) return;
-    const EsRange rows = es_range(a.offsets, at.expert, static_cast<int>(a.N));
+    const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int r0 = at.index * chunk;
     const int n = min(chunk, rows.count - r0);
-    const int d0 = blockIdx.x * kEsRows;
     const int64_t block0 = static_cast<int64_t>(at.blocks) + r0 / kEsTokens;
-    const int steps = min(static_cast<int64_t>((n + kEsTokens - 1) / kEsTokens), max(static_cast<int64_t>(0), p_blocks - block0));
+    const int steps = static_cast<int>(min(static_cast<int64_t>((n + kEsTokens - 1) / kEsTokens),
+                                           max(static_cast<int64_t>(0), p_blocks - block0)));
     // where the tile goes: the first item of an expert to S, the others to a
     // partial sketch each, added to S by es_reduce_kernel
     float *dst = a.S + static_cast<int64_t>(at.expert) * D * R;
@@ -262,56 +481,102 @@ __global__ __launch_bounds__(256) void es_fold_kernel(ExpertSketchArgs a, int ch
         return;
     }
 
-    const uint16_t *dy = static_cast<const uint16_t *>(a.dY) + (static_cast<int64_t>(rows.begin) + r0) * a.lddy;
-    const int lt = tid >> 3, lc = 8 * (tid & 7);        // this thread's row and columns of a step's tile
-    const bool col_ok = d0 + lc < D;
-    auto gload = [&](int s) -> u32x4_t {
-        const int t = kEsTokens * s + lt;
-        return col_ok && t < n ? load_u32x4(dy + t * a.lddy + d0 + lc) : zero_u32x4();
-    };
-    const uint16_t *pb = P + block0 * 2 * R * kEsTokens;
-    f32x4_t acc[MB][NB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = zero_f32x4();
-    u32x4_t next = gload(0);
-    for (int s = 0; s < steps; ++s) {
-        uint16_t *buf = lds[s & 1];
-        *reinterpret_cast<u32x4_t *>(&buf[lt * kRow + lc]) = next;
-        next = gload(s + 1);
-        u32x4_t hi[NB], lo[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const uint16_t *src = pb + (static_cast<int64_t>(s) * 2 * R + 16 * (wn * NB + nb) + i16) * kEsTokens + 8 * g;
-            hi[nb] = load_u32x4(src);
-            lo[nb] = load_u32x4(src + R * kEsTokens);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const uint16_t *p = buf + (8 * g + (i16 >> 2)) * kRow + 16 * (wm + mb * WM) + 4 * (i16 & 3);
-            const u32x2_t x = es_read_tr(p), y = es_read_tr(p + 4 * kRow);
-            const u32x4_t av = {x.x, x.y, y.x, y.y};
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                acc[mb][nb] = mfma_bf16(av, lo[nb], acc[mb][nb]);
-                acc[mb][nb] = mfma_bf16(av, hi[nb], acc[mb][nb]);
-            }
-        }
-    }
-    // lane (i16, g) of block (mb, nb): rows 4 g .. +3, column i16
+    f32x16_t acc[MB][NB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = d0 + 16 * (wm + mb * WM) + 4 * g + q;
-                if (row >= D) continue;
-                float *p = dst + static_cast<int64_t>(row) * R + 16 * (wn * NB + nb) + i16;
-                *p = add ? *p + acc[mb][nb][q] : acc[mb][nb][q];
+            for (int e = 0; e < 16; ++e) acc[mb][nb][e] = 0.f;
+    if (steps > 0) {
+        // A dY tile in LDS: row t, 16-column block b at block b ^ swizzle(t)
+        // of the row, so that the rows a transposed read touches at once lie
+        // in different banks.
+        const uint16_t *dy = static_cast<const uint16_t *>(a.dY) + (static_cast<int64_t>(rows.begin) + r0) * a.lddy;
+        const uint32_t ld_bytes = static_cast<uint32_t>(a.lddy * 2);
+        const int lt = tid >> 4, lc = tid & 15;         // this thread's rows (lt, lt + 16) and 8-column piece
+        auto swizzle = [](int t) { return (t & 3) | ((t >> 1) & 4); };
+        const uint32_t goff = d0 + 8 * lc < D ? lt * ld_bytes + 2 * (d0 + 8 * lc) : kEsOob;
+        // (the views of a step's 32 rows start at their first one: an item may be longer than a view reaches)
+        auto gload = [&](int s, u32x4_t (&v)[2]) {
+            const uint32_t left = static_cast<uint32_t>(min(kEsTokens, max(0, n - kEsTokens * s)));
+            const __amdgpu_buffer_rsrc_t view = es_view(dy + static_cast<int64_t>(s) * kEsTokens * a.lddy, left * ld_bytes);
+            v[0] = es_load(view, goff);
+            v[1] = es_load(view, goff + 16 * ld_bytes);
+        };
+        constexpr uint32_t kStep = R * kEsTokens * 4;   // bytes of P per step
+        const __amdgpu_buffer_rsrc_t pview = es_view(P + block0 * R * kEsTokens, static_cast<uint32_t>(steps) * kStep);
+        const uint32_t poff = ((32 * wn * NB + i32) * kEsTokens + 8 * h) * 4;
+        auto pload = [&](uint32_t at_step, int nb, int kb, u32x4_t (&v)[2]) {
+            const uint32_t off = poff + at_step + (32 * nb * kEsTokens + 16 * kb) * 4;
+            v[0] = es_load(pview, off);
+            v[1] = es_load(pview, off + 16);
+        };
+        u32x4_t next0[2], next1[2], pv[2][NB][2];
+        gload(0, next0);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) pload(0, nb, kb, pv[kb][nb]);
+        gload(1, next1);
+        auto step = [&](int s, u32x4_t (&next)[2]) {
+            uint16_t *buf = lds[s & 1];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = lt + 16 * q;
+                *reinterpret_cast<u32x4_t *>(&buf[t * kEsRows + 16 * ((lc >> 1) ^ swizzle(t)) + 8 * (lc & 1)]) = next[q];
             }
+            gload(s + 2, next);
+            lds_barrier();
+            const uint32_t ahead = static_cast<uint32_t>(s + 1) * kStep;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                // 16 rows t = 16 kb ..: lanes of group g16 read columns 16 (g16 & 1) of a
+                // 32-column block, rows 8 (g16 >> 1) ..
+                u32x4_t av[MB];
+                const int t = 16 * kb + 8 * h + ((lane & 15) >> 2);
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    const int b16 = 2 * (wm * MB + mb) + ((lane >> 4) & 1);
+                    const uint16_t *src = buf + t * kEsRows + 16 * (b16 ^ swizzle(t)) + 4 * (lane & 3);
+                    const u32x2_t x = lds_read_tr(src), y = lds_read_tr(src + 4 * kEsRows);
+                    av[mb] = u32x4_t{x.x, x.y, y.x, y.y};
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    u32x4_t p[kEsTerms];
+                    es_split(pv[kb][nb][0], pv[kb][nb][1], p);
+                    pload(ahead, nb, kb, pv[kb][nb]);
+                    __builtin_amdgcn_sched_barrier(0);      // the request stays a step ahead of its use
+#pragma unroll
+                    for (int q = kEsTerms - 1; q >= 0; --q)
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) acc[mb][nb] = mfma_bf16_32(av[mb], p[q], acc[mb][nb]);
+                }
+            }
+        };
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            step(s, next0);
+            step(s + 1, next1);
+        }
+        if (s < steps) step(s, next0);
+    }
+    // lane (i32, h) of block (mb, nb): rows 8 q + 4 h + e of column i32
+    float *out = dst + static_cast<int64_t>(d0) * R + 32 * wn * NB + i32;
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int row = 32 * (wm * MB + mb) + 8 * (q >> 2) + 4 * h + (q & 3);
+                if (d0 + row < D)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) f(out + row * R + 32 * nb, acc[mb][nb][q]);
+            }
+    };
+    if (add) each([](float *p, float v) { *p += v; });
+    else each([](float *p, float v) { *p = v; });
 }
 
 // S_e += the partial sketches of expert e, in their order.
@@ -346,9 +611,9 @@ __global__ __launch_bounds__(256) void es_project_f32_kernel(ExpertSketchArgs a,
     __shared__ uint64_t words[32];
     __shared__ int64_t row_of[32];
     const int R = a.R, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, false);
+    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, kEsTokens);
     if (at.expert < 0) return;
-    const EsRange rows = es_range(a.offsets, at.expert, static_cast<int>(a.N));
+    const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int i0 = rows.begin + at.index * 32, n = min(32, rows.count - at.index * 32);
     const int l0 = blockIdx.y * 32, l = l0 + tx;
     const uint64_t key = es_key(a, at.expert);
@@ -419,6 +684,9 @@ __global__ __launch_bounds__(256) void es_fold_f32_kernel(ExpertSketchArgs a, in
 }
 
 // ------------------------------------------------------------------ plans --
+constexpr int64_t kEsMaxChunk = 1 << 20;   // an item's part of P stays within a view (r <= 256)
+constexpr int64_t kEsWideFrom = 4096;   // rows from which the wide projection is used
+
 ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int R, int bf16) {
     ExpertSketchPlan p;
     (void)k;
@@ -431,11 +699,12 @@ ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int 
         return p;
     }
     int64_t chunk = 2 * N / E;
-    chunk = (chunk < 1024 ? 1024 : chunk + 31) / 32 * 32;
+    chunk = (chunk < 512 ? 512 : chunk + 31) / 32 * 32;
+    if (chunk > kEsMaxChunk) chunk = kEsMaxChunk;
     p.chunk = static_cast<int>(chunk);
     p.extras = N / p.chunk;
     p.items = E + p.extras;
-    p.p_bytes = static_cast<size_t>(p.p_blocks) * 2 * R * kEsTokens * 2;
+    p.p_bytes = static_cast<size_t>(p.p_blocks) * R * kEsTokens * 4;
     p.total = p.p_bytes + static_cast<size_t>(p.extras) * d * R * 4;
     return p;
 }
@@ -443,19 +712,32 @@ ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int 
 template <int R>
 static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st) {
     const ExpertSketchPlan p = plan_expert_sketch(a.N, a.E, a.d, a.k, R, 1);
-    uint16_t *P = static_cast<uint16_t *>(a.ws);
+    float *P = static_cast<float *>(a.ws);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(a.ws) + p.p_bytes);
     const int D = static_cast<int>(a.d), K = static_cast<int>(a.k);
-    if (p.p_blocks > 0)
-        hipLaunchKernelGGL(es_project_kernel<R>, dim3(p.p_blocks, R < 128 ? 1 : R / 128), dim3(512), 0, st, a,
-                           p.chunk, K, P);
-    hipLaunchKernelGGL(es_fold_kernel<R>, dim3((D + kEsRows - 1) / kEsRows, p.items), dim3(256), 0, st, a, p.chunk, D,
-                       p.p_blocks, p.extras, P, parts);
+    const int64_t wide = a.N / kEsWideRows + (a.N < a.E ? a.N : a.E);      // kEsWideRows-row units at most
+    if (p.p_blocks > 0) {
+        bool done = false;
+        if constexpr (R >= 128) {
+            done = a.N >= kEsWideFrom;
+            if (done)
+                hipLaunchKernelGGL(es_project_wide_kernel<R>, dim3((wide + kXcds - 1) / kXcds * kXcds * (R / kEsWideCols)),
+                                   dim3(256), 0, st, a, p.chunk,
+                                   K, p.p_blocks, P);
+        }
+        if (!done)
+            hipLaunchKernelGGL(es_project_kernel<R>, dim3(p.p_blocks, R < 128 ? 1 : R / 128), dim3(512), 0, st, a,
+                               p.chunk, K, P);
+    }
+    const int tiles = (D + kEsRows - 1) / kEsRows;
+    const int64_t wgs = (p.items + kXcds - 1) / kXcds * kXcds * tiles;
+    hipLaunchKernelGGL(es_fold_kernel<R>, dim3(wgs), dim3(256), 0, st, a, p.chunk, D, tiles,
+                       static_cast<int>(p.items), p.p_blocks, p.extras, P, parts);
     if (p.extras > 0) {
         const int64_t size = a.d * R;
-        const int64_t wgs = (size + 4095) / 4096;
-        hipLaunchKernelGGL(es_reduce_kernel, dim3(wgs < 64 ? wgs : 64, a.E), dim3(256), 0, st, a, p.chunk, size,
-                           p.extras, parts);
+        const int64_t n = (size + 4095) / 4096;
+        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 32 ? n : 32, a.E), dim3(256), 0, st, a, p.chunk, size, p.extras,
+                           parts);
     }
     return hipGetLastError();
 }
