@@ -499,74 +499,84 @@ def logra_ts_apply(m: MatrixDesc, ws: torch.Tensor, W: torch.Tensor, lr: float, 
 
 # ---- gradient clipping and expert layers ----
 
-class _On:
-    """One call's device: its tensors must all be on one GPU, the workspace
-    comes from the stream the call runs on (so that its memory is not handed
-    out to other work while the call still uses it), and the call is made
-    with that GPU current."""
+# These calls may be short against the checks around them (a few rows, a few
+# short tensors), so the checks read each property of a tensor once and pass
+# plain integers.
 
-    def __init__(self, where, stream, tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if t.device.type != "cuda" or (dev is not None and t.device != dev):
-                raise LograError(1, "%s: tensors on one GPU expected" % where)
-            dev = t.device
-        if dev is None:
-            raise LograError(1, "%s: a tensor on a GPU expected" % where)
-        self.where, self.device = where, dev
+def _enter(where, stream, tensors):
+    """(device index, raw stream) of one call: its tensors must all be on one
+    GPU; without a stream it runs on that GPU's current one."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or d != dev:
+                if d < 0 or dev >= 0:
+                    raise LograError(1, where + ": tensors on one GPU expected")
+                dev = d
+    if dev < 0:
+        raise LograError(1, where + ": a tensor on a GPU expected")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _call(where, dev, fn, *args):
+    """The C call with its GPU current."""
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != 0:
+        raise LograError(status, where)
+
+
+def _workspace(where, dev, stream, handle, ws, nbytes):
+    """(tensor, address, bytes). One made here comes from the stream the call
+    runs on, so that its memory is not handed to other work while the call
+    still uses it; the caller keeps the tensor until the call is made."""
+    if ws is None:
+        if nbytes == 0:
+            return None, None, 0
+        device = torch.device("cuda", dev)
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
-            self.ambient = True
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
-            self.ambient = False
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        self.stream = stream
-
-    def workspace(self, ws, nbytes):
-        """(tensor, pointer, bytes); the caller keeps the tensor until the call is made."""
-        if ws is None:
-            if nbytes == 0:
-                return None, None, 0
-            if self.ambient:
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            else:
-                with torch.cuda.stream(self.stream):
-                    ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        elif ws.device != self.device or not ws.is_contiguous():
-            raise LograError(3, "%s: contiguous workspace on %s expected" % (self.where, self.device))
-        return ws, _ptr(ws), _nbytes(ws)
-
-    def call(self, fn, *args):
-        handle = ctypes.c_void_p(self.stream.cuda_stream)
-        if torch.cuda.current_device() == self.device.index:
-            _check(fn(*args, handle), self.where)
-        else:
-            with torch.cuda.device(self.device):
-                _check(fn(*args, handle), self.where)
+                stream = torch.cuda.ExternalStream(handle, device=device)
+            with torch.cuda.stream(stream):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws, ws.data_ptr(), nbytes
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise LograError(3, "%s: contiguous workspace on GPU %d expected" % (where, dev))
+    return ws, ws.data_ptr(), _nbytes(ws)
 
 
 def _want(where, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise LograError(1, "%s: contiguous %s tensor of shape %s expected" % (where, dtype, tuple(shape)))
 
 
 def _one_float(where, t):
-    if t.dtype != torch.float32 or t.numel() != 1:
-        raise LograError(1, "%s: one-element float32 tensor expected" % where)
+    if t.dtype is not torch.float32 or t.numel() != 1:
+        raise LograError(1, where + ": one-element float32 tensor expected")
 
 
 def _rows(where, t, h=None, dtype=None):
-    """Row stride of a 2-D tensor of rows (unit column stride)."""
-    if t.dim() != 2 or (t.size(0) > 0 and t.size(1) > 1 and t.stride(1) != 1):
-        raise LograError(1, "%s: 2-D tensor with unit column stride expected" % where)
-    if h is not None and t.size(1) != h:
-        raise LograError(1, "%s: rows of %d elements expected" % (where, h))
-    if dtype is not None and t.dtype != dtype:
-        raise LograError(1, "%s: one dtype for all rows expected" % where)
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+    """(rows, columns, row stride) of a 2-D tensor of rows (unit column
+    stride), of h columns and of dtype if those are given."""
+    shape = t.shape
+    if len(shape) == 2:
+        n, cols = shape
+        ld, unit = t.stride()
+        if unit == 1 or cols <= 1 or n == 0:
+            if h is not None and cols != h:
+                raise LograError(1, "%s: rows of %d elements expected" % (where, h))
+            if dtype is not None and t.dtype is not dtype:
+                raise LograError(1, where + ": one dtype for all rows expected")
+            return n, cols, ld if n > 1 else max(ld, cols)
+    raise LograError(1, where + ": 2-D tensor with unit column stride expected")
 
 
 class GradList:
@@ -598,7 +608,9 @@ class GradList:
                                         ctypes.byref(self.desc)), "logra_grad_list_pack")
         self.table = host.to(self.device)
         self.desc.table = self.table.data_ptr()
+        self.ref = ctypes.byref(self.desc)
         self.elements = int(self.desc.elements)
+        self.workspace_bytes = int(lib.logra_grad_workspace_bytes(self.ref))
 
     @staticmethod
     def _rows_of(t):
@@ -611,16 +623,16 @@ class GradList:
 
 
 def logra_grad_workspace_bytes(grads: GradList) -> int:
-    return int(load_library().logra_grad_workspace_bytes(ctypes.byref(grads.desc)))
+    return grads.workspace_bytes
 
 
 def logra_grad_norm(grads: GradList, norm: torch.Tensor, ws: Optional[torch.Tensor] = None, stream=None) -> None:
     """norm[0] = the L2 norm over all elements of all tensors of the list."""
     where = "logra_grad_norm"
     _one_float(where, norm)
-    on = _On(where, stream, (grads.table, norm))
-    ws, p, nb = on.workspace(ws, logra_grad_workspace_bytes(grads))
-    on.call(load_library().logra_grad_norm, ctypes.byref(grads.desc), _ptr(norm), p, nb)
+    dev, handle = _enter(where, stream, (grads.table, norm))
+    ws, p, nb = _workspace(where, dev, stream, handle, ws, grads.workspace_bytes)
+    _call(where, dev, load_library().logra_grad_norm, grads.ref, norm.data_ptr(), p, nb, handle)
 
 
 def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: torch.Tensor,
@@ -631,14 +643,14 @@ def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: 
     where = "logra_grad_clip"
     _one_float(where, norm)
     _one_float(where, coef)
-    on = _On(where, stream, (grads.table, norm, coef, None if out is None else out.table))
-    ws, p, nb = on.workspace(ws, logra_grad_workspace_bytes(grads))
-    on.call(load_library().logra_grad_clip, ctypes.byref(grads.desc), None if out is None else ctypes.byref(out.desc),
-            float(max_norm), _ptr(norm), _ptr(coef), p, nb)
+    dev, handle = _enter(where, stream, (grads.table, norm, coef, None if out is None else out.table))
+    ws, p, nb = _workspace(where, dev, stream, handle, ws, grads.workspace_bytes)
+    _call(where, dev, load_library().logra_grad_clip, grads.ref, None if out is None else out.ref, max_norm,
+          norm.data_ptr(), coef.data_ptr(), p, nb, handle)
 
 
 def logra_expert_sort_workspace_bytes(T: int, topk: int, n_experts: int) -> int:
-    return int(load_library().logra_expert_sort_workspace_bytes(int(T), int(topk), int(n_experts)))
+    return int(load_library().logra_expert_sort_workspace_bytes(T, topk, n_experts))
 
 
 def logra_expert_sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, order: torch.Tensor,
@@ -647,26 +659,27 @@ def logra_expert_sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, 
     0 .. n_experts - 1 dropped) sorted by expert: offsets (n_experts + 1),
     order (T topk, place -> pair) and slots (T x topk, pair -> place), int32."""
     where = "logra_expert_sort"
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
-        raise LograError(1, where + ": 2-D int32 or int64 ids expected")
-    T, K = ids.shape
-    ld = _rows(where, ids)
+    T, K, ld = _rows(where, ids)
+    wide = ids.dtype is torch.int64
+    if not wide and ids.dtype is not torch.int32:
+        raise LograError(1, where + ": int32 or int64 ids expected")
     _want(where, offsets, torch.int32, (n_experts + 1,))
     _want(where, order, torch.int32, (T * K,))
     _want(where, slots, torch.int32, (T, K))
-    on = _On(where, stream, (ids, offsets, order, slots))
-    ws, p, nb = on.workspace(ws, logra_expert_sort_workspace_bytes(T, K, n_experts))
-    on.call(load_library().logra_expert_sort, T, K, int(n_experts), _ptr(ids), ids.element_size(), ld, _ptr(offsets),
-            _ptr(order), _ptr(slots), p, nb)
+    dev, handle = _enter(where, stream, (ids, offsets, order, slots))
+    ws, p, nb = _workspace(where, dev, stream, handle, ws, logra_expert_sort_workspace_bytes(T, K, n_experts))
+    _call(where, dev, load_library().logra_expert_sort, T, K, n_experts, ids.data_ptr(), 8 if wide else 4, ld,
+          offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), p, nb, handle)
 
 
 def _slots_of(where, slots, weights, T):
-    if slots.dim() != 2 or slots.size(0) != T:
-        raise LograError(1, "%s: slots of %d tokens expected" % (where, T))
-    _want(where, slots, torch.int32, slots.shape)
+    """topk of contiguous T x topk slots (and weights)."""
+    shape = slots.shape
+    if len(shape) != 2 or shape[0] != T or slots.dtype is not torch.int32 or not slots.is_contiguous():
+        raise LograError(1, "%s: contiguous int32 slots of %d tokens expected" % (where, T))
     if weights is not None:
-        _want(where, weights, torch.float32, slots.shape)
-    return slots.size(1)
+        _want(where, weights, torch.float32, shape)
+    return shape[1]
 
 
 def logra_expert_gather(X: torch.Tensor, slots: torch.Tensor, Xs: torch.Tensor,
@@ -674,12 +687,12 @@ def logra_expert_gather(X: torch.Tensor, slots: torch.Tensor, Xs: torch.Tensor,
     """Xs[slots[t][j]] = weights[t][j] X[t] (no weights: copies); the other
     rows of Xs stay as they are."""
     where = "logra_expert_gather"
-    T, h = X.shape if X.dim() == 2 else (0, 0)
-    ldx, ldxs = _rows(where, X), _rows(where, Xs, h, X.dtype)
+    T, h, ldx = _rows(where, X)
+    N, _, ldxs = _rows(where, Xs, h, X.dtype)
     K = _slots_of(where, slots, weights, T)
-    on = _On(where, stream, (X, slots, Xs, weights))
-    on.call(load_library().logra_expert_gather, T, K, h, _dtype_code(X), _ptr(X), ldx, _ptr(slots), _ptr(weights),
-            _ptr(Xs), ldxs, Xs.size(0))
+    dev, handle = _enter(where, stream, (X, slots, Xs, weights))
+    _call(where, dev, load_library().logra_expert_gather, T, K, h, _dtype_code(X), X.data_ptr(), ldx,
+          slots.data_ptr(), None if weights is None else weights.data_ptr(), Xs.data_ptr(), ldxs, N, handle)
 
 
 def logra_expert_combine(Ys: torch.Tensor, slots: torch.Tensor, Y: torch.Tensor,
@@ -687,12 +700,12 @@ def logra_expert_combine(Ys: torch.Tensor, slots: torch.Tensor, Y: torch.Tensor,
     """Y[t] = sum_j weights[t][j] Ys[slots[t][j]] (no weights: the plain sum,
     which is the gradient of gather)."""
     where = "logra_expert_combine"
-    T, h = Y.shape if Y.dim() == 2 else (0, 0)
-    ldy, ldys = _rows(where, Y), _rows(where, Ys, h, Y.dtype)
+    T, h, ldy = _rows(where, Y)
+    N, _, ldys = _rows(where, Ys, h, Y.dtype)
     K = _slots_of(where, slots, weights, T)
-    on = _On(where, stream, (Ys, slots, Y, weights))
-    on.call(load_library().logra_expert_combine, T, K, h, _dtype_code(Y), _ptr(Ys), ldys, Ys.size(0), _ptr(slots),
-            _ptr(weights), _ptr(Y), ldy)
+    dev, handle = _enter(where, stream, (Ys, slots, Y, weights))
+    _call(where, dev, load_library().logra_expert_combine, T, K, h, _dtype_code(Y), Ys.data_ptr(), ldys, N,
+          slots.data_ptr(), None if weights is None else weights.data_ptr(), Y.data_ptr(), ldy, handle)
 
 
 def logra_expert_combine_backward(dY: torch.Tensor, Ys: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor,
@@ -700,20 +713,21 @@ def logra_expert_combine_backward(dY: torch.Tensor, Ys: torch.Tensor, slots: tor
     """dYs[slots[t][j]] = weights[t][j] dY[t] and dweights[t][j] = <dY[t],
     Ys[slots[t][j]]>; the other rows of dYs stay as they are."""
     where = "logra_expert_combine_backward"
-    T, h = dY.shape if dY.dim() == 2 else (0, 0)
-    lddy, ldys, lddys = _rows(where, dY), _rows(where, Ys, h, dY.dtype), _rows(where, dYs, h, dY.dtype)
-    if dYs.size(0) != Ys.size(0):
+    T, h, lddy = _rows(where, dY)
+    N, _, ldys = _rows(where, Ys, h, dY.dtype)
+    N2, _, lddys = _rows(where, dYs, h, dY.dtype)
+    if N2 != N:
         raise LograError(1, where + ": as many rows of dYs as of Ys expected")
     K = _slots_of(where, slots, weights, T)
     _want(where, dweights, torch.float32, slots.shape)
-    on = _On(where, stream, (dY, Ys, slots, weights, dYs, dweights))
-    on.call(load_library().logra_expert_combine_backward, T, K, h, _dtype_code(dY), _ptr(dY), lddy, _ptr(Ys), ldys,
-            Ys.size(0), _ptr(slots), _ptr(weights), _ptr(dYs), lddys, _ptr(dweights))
+    dev, handle = _enter(where, stream, (dY, Ys, slots, weights, dYs, dweights))
+    _call(where, dev, load_library().logra_expert_combine_backward, T, K, h, _dtype_code(dY), dY.data_ptr(), lddy,
+          Ys.data_ptr(), ldys, N, slots.data_ptr(), weights.data_ptr(), dYs.data_ptr(), lddys, dweights.data_ptr(),
+          handle)
 
 
 def logra_sketch_experts_workspace_bytes(m: MatrixDesc, n_experts: int, N: int, act_dtype: int) -> int:
-    return int(load_library().logra_sketch_experts_workspace_bytes(ctypes.byref(m), int(n_experts), int(N),
-                                                                    int(act_dtype)))
+    return int(load_library().logra_sketch_experts_workspace_bytes(ctypes.byref(m), n_experts, N, act_dtype))
 
 
 def logra_sketch_experts(m: MatrixDesc, offsets: torch.Tensor, X: torch.Tensor, dY: torch.Tensor, S: torch.Tensor,
@@ -724,14 +738,17 @@ def logra_sketch_experts(m: MatrixDesc, offsets: torch.Tensor, X: torch.Tensor, 
     order and topk, the activations before it (T x k); expert e's signs are
     those of m.matrix_id + e id_stride."""
     where = "logra_sketch_experts"
-    E, N = S.size(0), dY.size(0)
+    rows, _, ldx = _rows(where, X, m.k)
+    N, _, lddy = _rows(where, dY, m.d, X.dtype)
+    E = S.size(0) if S.dim() else 0
     _want(where, S, torch.float32, (E, m.d, m.r))
     _want(where, offsets, torch.int32, (E + 1,))
     if order is not None:
         _want(where, order, torch.int32, (N,))
-    ldx, lddy = _rows(where, X, m.k), _rows(where, dY, m.d, X.dtype)
     code = _dtype_code(X)
-    on = _On(where, stream, (offsets, X, dY, S, order))
-    ws, p, nb = on.workspace(ws, logra_sketch_experts_workspace_bytes(m, E, N, code))
-    on.call(load_library().logra_sketch_experts, ctypes.byref(m), E, int(id_stride), N, code, _ptr(offsets),
-            _ptr(order), int(topk), _ptr(X), ldx, X.size(0), _ptr(dY), lddy, _ptr(S), 1 if accumulate else 0, p, nb)
+    dev, handle = _enter(where, stream, (offsets, X, dY, S, order))
+    ws, p, nb = _workspace(where, dev, stream, handle, ws,
+                           logra_sketch_experts_workspace_bytes(m, E, N, code) if ws is None else 0)
+    _call(where, dev, load_library().logra_sketch_experts, ctypes.byref(m), E, id_stride, N, code,
+          offsets.data_ptr(), None if order is None else order.data_ptr(), topk, X.data_ptr(), ldx, rows,
+          dY.data_ptr(), lddy, S.data_ptr(), 1 if accumulate else 0, p, nb, handle)

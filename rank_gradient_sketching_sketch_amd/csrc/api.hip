@@ -732,7 +732,7 @@ logra_status logra_grad_norm(const logra_grad_list *list, float *norm, void *ws,
     if (!grad_list_ok(list) || !norm || !aligned_to(norm, 4)) return LOGRA_ERR_INVALID_ARGUMENT;
     if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
     return from_hip(launch_grad_norm(static_cast<const GradEntry *>(list->table), list->n, list->chunks,
-                                     static_cast<double *>(ws), norm, static_cast<hipStream_t>(stream)));
+                                     list->elements, static_cast<double *>(ws), norm, static_cast<hipStream_t>(stream)));
 }
 
 logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list *out, float max_norm, float *norm,
@@ -744,8 +744,8 @@ logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list 
         return LOGRA_ERR_INVALID_ARGUMENT;
     if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
     return from_hip(launch_grad_clip(static_cast<const GradEntry *>(list->table),
-                                     static_cast<const GradEntry *>(out->table), list->n, list->chunks, max_norm,
-                                     static_cast<double *>(ws), norm, coef, static_cast<hipStream_t>(stream)));
+                                     static_cast<const GradEntry *>(out->table), list->n, list->chunks,
+                                     list->elements, max_norm, static_cast<double *>(ws), norm, coef, static_cast<hipStream_t>(stream)));
 }
 
 // ---- rows sorted by expert, and back ----
@@ -871,8 +871,8 @@ logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t
             return LOGRA_ERR_UNSUPPORTED;
     }
     const ExpertSketchPlan p = plan_expert_sketch(N, n_experts, m->d, m->k, static_cast<int>(m->r), bf16);
-    if (p.total > 0 && (!ws || ws_bytes < p.total || !aligned16(ws))) return LOGRA_ERR_WORKSPACE;
     if (N == 0 && accumulate) return LOGRA_OK;
+    if (p.total > 0 && (!ws || ws_bytes < p.total || !aligned16(ws))) return LOGRA_ERR_WORKSPACE;
     ExpertSketchArgs a;
     a.E = n_experts;
     a.R = static_cast<int>(m->r);

@@ -7,20 +7,27 @@
 // plus the dense gradients of what is not sketched), so the kernels walk a
 // device table of them, cut into chunks of at most kGradChunk elements; each
 // workgroup takes a contiguous range of chunks, finds its first one by
-// bisection and steps through the table from there.
+// bisection and steps through the table from there, reading what lies in one
+// tensor without gaps as one run.
 //
 // Sums are taken in fp64 (squares of fp32 values neither overflow nor vanish
-// there): per thread, over the workgroup by a fixed tree, and over the
-// workgroups' partials in a fixed order, so results do not depend on timing.
-// The scaling kernel's workgroups each add the partials themselves (at most
-// kGradMaxWGs doubles, from the L2), so no workgroup waits for another and
-// no counter has to be reset.
+// there, and the reads hide the arithmetic): per thread, over the workgroup by
+// a fixed tree, and over the workgroups' partials in a fixed order, so results
+// do not depend on timing. The scaling kernel's workgroups each add the
+// partials themselves (at most kGradMaxWGs doubles, from the L2), so no
+// workgroup waits for another and no counter has to be reset. Few elements are
+// done by one workgroup in one launch.
 #include "common.hpp"
 #include "launch.hpp"
 
 namespace logra {
 
 constexpr int kGradThreads = 256;
+constexpr int kGradSmallThreads = 1024;
+constexpr int64_t kGradSmallChunks = 32;      // chunks (of one or several tensors) that one workgroup takes alone
+constexpr int64_t kGradSmallElements = 32768;
+// Elements above which the reads are marked as not to be kept in the caches.
+constexpr int64_t kGradStream = 1ll << 26;
 
 // Tensors need only their element's alignment (global memory takes 16-byte
 // accesses at any address). The table holds their addresses as numbers, so
@@ -49,12 +56,13 @@ __device__ __forceinline__ void grad_put(gbytes *p, int64_t i, float v) {
 }
 
 // V consecutive elements from index i (V * element size a multiple of 16).
-template <int BF16, int V>
+template <int BF16, int V, int NT = 0>
 __device__ __forceinline__ void grad_load(const gbytes *p, int64_t i, float (&v)[V]) {
     if (BF16) {
 #pragma unroll
         for (int q = 0; q < V / 8; ++q) {
-            const u32x4_t w = *(const LOGRA_GLOBAL u32x4_u2_t *)(p + 2 * (i + 8 * q));
+            const LOGRA_GLOBAL u32x4_u2_t *src = (const LOGRA_GLOBAL u32x4_u2_t *)(p + 2 * (i + 8 * q));
+            const u32x4_t w = NT ? __builtin_nontemporal_load(src) : *src;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[8 * q + 2 * e] = bf16_lo(w[e]);
@@ -64,14 +72,15 @@ __device__ __forceinline__ void grad_load(const gbytes *p, int64_t i, float (&v)
     } else {
 #pragma unroll
         for (int q = 0; q < V / 4; ++q) {
-            const u32x4_t w = *(const LOGRA_GLOBAL u32x4_u4_t *)(p + 4 * (i + 4 * q));
+            const LOGRA_GLOBAL u32x4_u4_t *src = (const LOGRA_GLOBAL u32x4_u4_t *)(p + 4 * (i + 4 * q));
+            const u32x4_t w = NT ? __builtin_nontemporal_load(src) : *src;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * q + e] = __uint_as_float(w[e]);
         }
     }
 }
 
-template <int BF16, int V>
+template <int BF16, int V, int NT = 0>
 __device__ __forceinline__ void grad_store(gbytes *p, int64_t i, const float (&v)[V]) {
     if (BF16) {
 #pragma unroll
@@ -79,7 +88,9 @@ __device__ __forceinline__ void grad_store(gbytes *p, int64_t i, const float (&v
             u32x4_t w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-            *(LOGRA_GLOBAL u32x4_u2_t *)(p + 2 * (i + 8 * q)) = w;
+            LOGRA_GLOBAL u32x4_u2_t *dst = (LOGRA_GLOBAL u32x4_u2_t *)(p + 2 * (i + 8 * q));
+            if (NT) __builtin_nontemporal_store(w, dst);
+            else *dst = w;
         }
     } else {
 #pragma unroll
@@ -87,10 +98,18 @@ __device__ __forceinline__ void grad_store(gbytes *p, int64_t i, const float (&v
             u32x4_t w;
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * q + e]);
-            *(LOGRA_GLOBAL u32x4_u4_t *)(p + 4 * (i + 4 * q)) = w;
+            LOGRA_GLOBAL u32x4_u4_t *dst = (LOGRA_GLOBAL u32x4_u4_t *)(p + 4 * (i + 4 * q));
+            if (NT) __builtin_nontemporal_store(w, dst);
+            else *dst = w;
         }
     }
 }
+
+// The threads that go through a run or a chunk together: a workgroup, or one
+// of its waves.
+struct GradGroup {
+    int id, size;
+};
 
 // One chunk of a tensor: rows x cols elements from `at` (element index with
 // row stride ld). Rows of a tensor without gaps are one long row.
@@ -122,15 +141,15 @@ __device__ __forceinline__ GradChunk grad_chunk(const GradEntry &e, int64_t c) {
 // f(chunk-local unit) over the chunk's units of V elements: a whole unit
 // calls full(index), the rest of a row calls one(index) per element.
 template <int V, int U, class Full, class One>
-__device__ __forceinline__ void grad_units(int rows, int cols, Full full, One one) {
+__device__ __forceinline__ void grad_units(GradGroup g, int rows, int cols, Full full, One one) {
     const int upr = (cols + V - 1) / V;
     const int n = rows * upr;
-    for (int u0 = threadIdx.x; u0 < n; u0 += U * blockDim.x) {
+    for (int u0 = g.id; u0 < n; u0 += U * g.size) {
         int row[U], col[U];
         bool whole[U], some[U];
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-            const int u = u0 + q * blockDim.x;
+            const int u = u0 + q * g.size;
             row[q] = rows == 1 ? 0 : u / upr;
             col[q] = (u - row[q] * upr) * V;
             some[q] = u < n;
@@ -144,14 +163,82 @@ __device__ __forceinline__ void grad_units(int rows, int cols, Full full, One on
     }
 }
 
-constexpr int kGradUnroll = 4;
+// Units of gapped chunks, and fp32 bytes of runs, that a thread has in flight.
+constexpr int kGradUnroll = 4, kGradRunBytes = 128;
 
+// A run of n elements without gaps: whole(index) for every U units of V
+// elements of a thread at once while they last, then unit by unit, then
+// one(index) for the last elements.
+template <int V, int U, class Many, class Unit, class One>
+__device__ __forceinline__ void grad_run(GradGroup g, int64_t n, Many many, Unit unit, One one) {
+    const int64_t step = static_cast<int64_t>(g.size) * V;
+    int64_t i = static_cast<int64_t>(g.id) * V;
+    for (; i + (U - 1) * step + V <= n; i += U * step) many(i, step);
+    for (; i + V <= n; i += step) unit(i);
+    if (i < n)
+        for (int64_t e = i; e < n; ++e) one(e);
+}
+
+template <int BF16, int NT>
+__device__ __forceinline__ double grad_run_sumsq(GradGroup g, const gbytes *p, int64_t n, double sum) {
+    constexpr int V = grad_vec<BF16>(), U = kGradRunBytes / 16 / (BF16 ? 2 : 1);
+    auto add = [&](float x) {
+        const double d = x;
+        sum = fma(d, d, sum);
+    };
+    grad_run<V, U>(
+        g, n,
+        [&](int64_t i, int64_t step) {
+            float v[U][V];
+#pragma unroll
+            for (int q = 0; q < U; ++q) grad_load<BF16, V, NT>(p, i + q * step, v[q]);
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int e = 0; e < V; ++e) add(v[q][e]);
+        },
+        [&](int64_t i) {
+            float v[V];
+            grad_load<BF16, V>(p, i, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) add(v[e]);
+        },
+        [&](int64_t i) { add(grad_get<BF16>(p, i)); });
+    return sum;
+}
+
+template <int IN16, int OUT16, int NT>
+__device__ __forceinline__ void grad_run_scale(GradGroup g, const gbytes *p, gbytes *o, int64_t n, float coef) {
+    constexpr int V = (IN16 || OUT16) ? 8 : 4, U = kGradRunBytes / 4 / V;
+    grad_run<V, U>(
+        g, n,
+        [&](int64_t i, int64_t step) {
+            float v[U][V];
+#pragma unroll
+            for (int q = 0; q < U; ++q) grad_load<IN16, V, NT>(p, i + q * step, v[q]);
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[q][e] *= coef;
+                grad_store<OUT16, V, NT>(o, i + q * step, v[q]);
+            }
+        },
+        [&](int64_t i) {
+            float v[V];
+            grad_load<IN16, V>(p, i, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] *= coef;
+            grad_store<OUT16, V>(o, i, v);
+        },
+        [&](int64_t i) { grad_put<OUT16>(o, i, coef * grad_get<IN16>(p, i)); });
+}
+
+// Chunks of tensors with gaps between their rows.
 template <int BF16>
-__device__ __forceinline__ double grad_chunk_sumsq(GradChunk k, double sum) {
+__device__ __forceinline__ double grad_chunk_sumsq(GradGroup g, GradChunk k, double sum) {
     constexpr int V = grad_vec<BF16>(), U = kGradUnroll;
-    if (k.ld == k.cols) k.cols *= k.rows, k.rows = 1;
     grad_units<V, U>(
-        k.rows, k.cols,
+        g, k.rows, k.cols,
         [&](const int (&row)[U], const int (&col)[U], const bool (&whole)[U]) {
             float v[U][V];
 #pragma unroll
@@ -176,11 +263,10 @@ __device__ __forceinline__ double grad_chunk_sumsq(GradChunk k, double sum) {
 }
 
 template <int IN16, int OUT16>
-__device__ __forceinline__ void grad_chunk_scale(GradChunk k, GradChunk o, float coef) {
+__device__ __forceinline__ void grad_chunk_scale(GradGroup g, GradChunk k, GradChunk o, float coef) {
     constexpr int V = (IN16 || OUT16) ? 8 : 4, U = kGradUnroll;
-    if (k.ld == k.cols && o.ld == o.cols) k.cols *= k.rows, k.rows = 1;
     grad_units<V, U>(
-        k.rows, k.cols,
+        g, k.rows, k.cols,
         [&](const int (&row)[U], const int (&col)[U], const bool (&whole)[U]) {
             float v[U][V];
 #pragma unroll
@@ -223,35 +309,61 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
     return s;
 }
 
-__device__ __forceinline__ double grad_range_sumsq(const GradEntry *t, int n, int64_t c0, int64_t c1) {
-    double sum = 0.0;
-    if (c0 < c1) {
-        int i = grad_find(t, n, c0);
-        for (int64_t c = c0; c < c1; ++c) {
-            while (c >= t[i].first + t[i].chunks) ++i;
-            const GradEntry e = t[i];
-            const GradChunk k = grad_chunk(e, c - e.first);
-            sum = e.bf16 ? grad_chunk_sumsq<1>(k, sum) : grad_chunk_sumsq<0>(k, sum);
-        }
+// First element of an entry's chunk c, of a tensor without gaps.
+__device__ __forceinline__ int64_t grad_run_at(const GradEntry &e, int64_t c) {
+    if (e.rows_per_chunk > 0) return min(c * e.rows_per_chunk, e.rows) * e.cols;
+    const int64_t row = c / e.segs_per_row;
+    return row * e.cols + (c - row * e.segs_per_row) * e.seg_len;
+}
+
+// f(entry, its number, first chunk, last chunk + 1) for the part of every
+// entry that chunks c0 .. c1 - 1 of the list hold.
+template <class F>
+__device__ __forceinline__ void grad_entries(const GradEntry *t, int n, int64_t c0, int64_t c1, F f) {
+    if (c0 >= c1) return;
+    for (int i = grad_find(t, n, c0); c0 < c1; ++i) {
+        const GradEntry e = t[i];
+        const int64_t last = min(c1, e.first + e.chunks);
+        if (c0 < last) f(e, i, c0 - e.first, last - e.first);
+        c0 = max(c0, last);
+    }
+}
+
+template <int NT>
+__device__ __forceinline__ double grad_entry_sumsq(GradGroup g, const GradEntry &e, int64_t a, int64_t b, double sum) {
+    if (e.ld == e.cols) {
+        const int64_t from = grad_run_at(e, a), n = grad_run_at(e, b) - from;
+        const gbytes *p = (const gbytes *)e.addr + from * (e.bf16 ? 2 : 4);
+        return e.bf16 ? grad_run_sumsq<1, NT>(g, p, n, sum) : grad_run_sumsq<0, NT>(g, p, n, sum);
+    }
+    for (int64_t c = a; c < b; ++c) {
+        const GradChunk k = grad_chunk(e, c);
+        sum = e.bf16 ? grad_chunk_sumsq<1>(g, k, sum) : grad_chunk_sumsq<0>(g, k, sum);
     }
     return sum;
 }
 
-__device__ __forceinline__ void grad_range_scale(const GradEntry *t, const GradEntry *to, int n, int64_t c0,
-                                                 int64_t c1, float coef) {
-    if (c0 >= c1) return;
-    int i = grad_find(t, n, c1 - 1);
-    for (int64_t c = c1 - 1; c >= c0; --c) {
-        while (c < t[i].first || t[i].chunks == 0) --i;
-        const GradEntry e = t[i], o = to[i];
-        const GradChunk k = grad_chunk(e, c - e.first), d = grad_chunk(o, c - e.first);
-        if (e.bf16) {
-            if (o.bf16) grad_chunk_scale<1, 1>(k, d, coef);
-            else grad_chunk_scale<1, 0>(k, d, coef);
-        } else {
-            if (o.bf16) grad_chunk_scale<0, 1>(k, d, coef);
-            else grad_chunk_scale<0, 0>(k, d, coef);
-        }
+template <int IN16, int OUT16, int NT>
+__device__ __forceinline__ void grad_entry_scale(GradGroup g, const GradEntry &e, const GradEntry &o, int64_t a,
+                                                 int64_t b, float coef) {
+    if (e.ld == e.cols && o.ld == o.cols) {
+        const int64_t from = grad_run_at(e, a);
+        grad_run_scale<IN16, OUT16, NT>(g, (const gbytes *)e.addr + from * (IN16 ? 2 : 4),
+                                        (gbytes *)o.addr + from * (OUT16 ? 2 : 4), grad_run_at(e, b) - from, coef);
+        return;
+    }
+    for (int64_t c = a; c < b; ++c) grad_chunk_scale<IN16, OUT16>(g, grad_chunk(e, c), grad_chunk(o, c), coef);
+}
+
+template <int NT>
+__device__ __forceinline__ void grad_entry_scale_any(GradGroup g, const GradEntry &e, const GradEntry &o, int64_t a,
+                                                     int64_t b, float coef) {
+    if (e.bf16) {
+        if (o.bf16) grad_entry_scale<1, 1, NT>(g, e, o, a, b, coef);
+        else grad_entry_scale<1, 0, NT>(g, e, o, a, b, coef);
+    } else {
+        if (o.bf16) grad_entry_scale<0, 1, NT>(g, e, o, a, b, coef);
+        else grad_entry_scale<0, 0, NT>(g, e, o, a, b, coef);
     }
 }
 
@@ -261,11 +373,17 @@ __device__ __forceinline__ float clip_coef(double norm, float max_norm) {
     return (norm > max_norm && norm < __builtin_inf()) ? static_cast<float>(max_norm / norm) : 1.f;
 }
 
+template <int NT>
 __global__ __launch_bounds__(kGradThreads) void grad_sumsq_kernel(const GradEntry *__restrict__ t, int n,
                                                                   int64_t chunks, double *__restrict__ partials) {
     __shared__ double lds[kGradThreads / 64];
     const int64_t g = blockIdx.x, G = gridDim.x;
-    const double s = block_sum(grad_range_sumsq(t, n, chunks * g / G, chunks * (g + 1) / G), lds);
+    const GradGroup group{static_cast<int>(threadIdx.x), kGradThreads};
+    double sum = 0.0;
+    grad_entries(t, n, chunks * g / G, chunks * (g + 1) / G, [&](const GradEntry &e, int, int64_t a, int64_t b) {
+        sum = grad_entry_sumsq<NT>(group, e, a, b, sum);
+    });
+    const double s = block_sum(sum, lds);
     if (threadIdx.x == 0) partials[g] = s;
 }
 
@@ -282,6 +400,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_norm_kernel(const double *_
     if (threadIdx.x == 0) *norm = static_cast<float>(s);
 }
 
+template <int NT>
 __global__ __launch_bounds__(kGradThreads) void grad_scale_kernel(
     const GradEntry *__restrict__ t, const GradEntry *__restrict__ to, int n, int64_t chunks,
     const double *__restrict__ partials, int n_partials, float max_norm, int in_place, float *__restrict__ norm,
@@ -296,27 +415,84 @@ __global__ __launch_bounds__(kGradThreads) void grad_scale_kernel(
     }
     // a factor of one changes nothing in place
     if (in_place && coef == 1.f) return;
-    grad_range_scale(t, to, n, chunks * g / G, chunks * (g + 1) / G, coef);
+    const GradGroup group{static_cast<int>(threadIdx.x), kGradThreads};
+    grad_entries(t, n, chunks * g / G, chunks * (g + 1) / G, [&](const GradEntry &e, int i, int64_t a, int64_t b) {
+        grad_entry_scale_any<NT>(group, e, to[i], a, b, coef);
+    });
 }
 
+// All of it by one workgroup, a chunk per wave at a time (at most 64 tensors:
+// each lane looks at one entry to find the chunk's); to and coef_out null: the
+// norm alone.
+__global__ __launch_bounds__(kGradSmallThreads) void grad_small_kernel(const GradEntry *__restrict__ t,
+                                                                       const GradEntry *__restrict__ to, int n,
+                                                                       int chunks, float max_norm, int in_place,
+                                                                       float *__restrict__ norm,
+                                                                       float *__restrict__ coef_out) {
+    __shared__ double lds[kGradSmallThreads / 64];
+    const int lane = threadIdx.x & 63;
+    const GradGroup group{lane, 64};
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t end = lane < n ? t[lane].first + t[lane].chunks : chunks;
+    auto each = [&](auto f) {
+        for (int c = wave; c < chunks; c += kGradSmallThreads / 64) {
+            const int i = __builtin_ctzll(__ballot(end > c));
+            const GradEntry e = t[i];
+            f(e, i, c - e.first);
+        }
+    };
+    double sum = 0.0;
+    each([&](const GradEntry &e, int, int64_t c) { sum = grad_entry_sumsq<0>(group, e, c, c + 1, sum); });
+    const double s = sqrt(block_sum(sum, lds));
+    const float coef = clip_coef(s, max_norm);
+    if (threadIdx.x == 0) {
+        *norm = static_cast<float>(s);
+        if (coef_out) *coef_out = coef;
+    }
+    if (!to || (in_place && coef == 1.f)) return;
+    each([&](const GradEntry &e, int i, int64_t c) { grad_entry_scale_any<0>(group, e, to[i], c, c + 1, coef); });
+}
+
+// As many chunks for every workgroup, but for the last ones.
 int grad_workgroups(int64_t chunks) {
-    return static_cast<int>(chunks < 1 ? 1 : chunks < kGradMaxWGs ? chunks : kGradMaxWGs);
+    if (chunks < 1) return 1;
+    const int64_t each = (chunks + kGradMaxWGs - 1) / kGradMaxWGs;
+    return static_cast<int>((chunks + each - 1) / each);
 }
 
-hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, double *partials, float *norm,
-                            hipStream_t st) {
+static bool grad_small(int n, int64_t chunks, int64_t elements) {
+    return n <= 64 && chunks <= kGradSmallChunks && elements <= kGradSmallElements;
+}
+
+hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, int64_t elements, double *partials,
+                            float *norm, hipStream_t st) {
+    if (grad_small(n, chunks, elements)) {
+        hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(kGradSmallThreads), 0, st, t, nullptr, n,
+                           static_cast<int>(chunks), 0.f, 0,
+                           norm, nullptr);
+        return hipGetLastError();
+    }
     const int g = grad_workgroups(chunks);
-    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(g), dim3(kGradThreads), 0, st, t, n, chunks, partials);
+    hipLaunchKernelGGL(elements > kGradStream ? grad_sumsq_kernel<1> : grad_sumsq_kernel<0>, dim3(g),
+                       dim3(kGradThreads), 0, st, t, n, chunks, partials);
     hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kGradThreads), 0, st, partials, g, norm);
     return hipGetLastError();
 }
 
-hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, float max_norm,
-                            double *partials, float *norm, float *coef, hipStream_t st) {
+hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, int64_t elements,
+                            float max_norm, double *partials, float *norm, float *coef, hipStream_t st) {
+    const int in_place = t == to ? 1 : 0;
+    if (grad_small(n, chunks, elements)) {
+        hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(kGradSmallThreads), 0, st, t, to, n,
+                           static_cast<int>(chunks), max_norm, in_place, norm, coef);
+        return hipGetLastError();
+    }
     const int g = grad_workgroups(chunks);
-    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(g), dim3(kGradThreads), 0, st, t, n, chunks, partials);
-    hipLaunchKernelGGL(grad_scale_kernel, dim3(g), dim3(kGradThreads), 0, st, t, to, n, chunks, partials, g,
-                       max_norm, t == to ? 1 : 0, norm, coef);
+    const bool stream = elements > kGradStream;
+    hipLaunchKernelGGL(stream ? grad_sumsq_kernel<1> : grad_sumsq_kernel<0>, dim3(g), dim3(kGradThreads), 0, st, t, n,
+                       chunks, partials);
+    hipLaunchKernelGGL(stream ? grad_scale_kernel<1> : grad_scale_kernel<0>, dim3(stream ? 4 * g : g),
+                       dim3(kGradThreads), 0, st, t, to, n, chunks, partials, g, max_norm, in_place, norm, coef);
     return hipGetLastError();
 }
 

@@ -219,10 +219,10 @@ struct GradEntry {
     int32_t bf16 = 0;
 };
 int grad_workgroups(int64_t chunks);
-hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, double *partials, float *norm,
-                            hipStream_t st);
-hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, float max_norm,
-                            double *partials, float *norm, float *coef, hipStream_t st);
+hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, int64_t elements, double *partials,
+                            float *norm, hipStream_t st);
+hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, int64_t elements,
+                            float max_norm, double *partials, float *norm, float *coef, hipStream_t st);
 
 // Pairs (token, choice) sorted by expert and rows moved along. elem: bytes
 // of an element of the rows (2 = bf16, 4 = fp32).

@@ -62,62 +62,137 @@ __device__ __forceinline__ u32x4_t es_load(__amdgpu_buffer_rsrc_t v, uint32_t of
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(v, off, 0, 0));
 }
 
-// What every wave works out from the offsets: the expert that holds unit u
-// when expert e holds units(count_e) consecutive ones, and the sums before it.
-struct EsPlace {
-    int expert, index;      // expert -1: no expert holds u; index: the unit's number within it
-    int blocks, extras;     // blocks of P and partial sketches of the experts before
+// A unit of the projection: up to unit_rows rows of one expert. All lanes of
+// the wave work it out from the offsets: the full units of all experts come
+// first, then each expert's last, shorter one, so that long ones do not start
+// last.
+struct EsUnit {
+    int expert;             // -1: there are fewer units
+    int index;              // the unit's number within its expert
+    int blocks;             // 32-row blocks of P of the experts before
 };
+__device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, int u, int unit_rows) {
+    const int lane = threadIdx.x & 63;
+    EsUnit p{-1, 0, 0};
+    int before = 0;
+    for (int pass = 0; pass < 2 && p.expert < 0; ++pass) {
+        int blocks = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int count = e0 + lane < E ? es_range(offsets, e0 + lane, N).count : 0;
+            const int nb = (count + kEsTokens - 1) / kEsTokens, full = count / unit_rows;
+            const int nu = pass == 0 ? full : count % unit_rows ? 1 : 0;
+            int iu = nu, ib = nb;            // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int a = __shfl_up(iu, o), b = __shfl_up(ib, o);
+                if (lane >= o) {
+                    iu += a;
+                    ib += b;
+                }
+            }
+            const uint64_t past = __ballot(before + iu > u);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                p.expert = e0 + l;
+                p.index = pass == 0 ? u - before - __builtin_amdgcn_readlane(iu - nu, l)
+                                    : __builtin_amdgcn_readlane(full, l);
+                p.blocks = blocks + __builtin_amdgcn_readlane(ib - nb, l);
+                break;
+            }
+            before += __builtin_amdgcn_readlane(iu, 63);
+            blocks += __builtin_amdgcn_readlane(ib, 63);
+        }
+    }
+    // the same in all lanes: kept in scalar registers
+    return EsUnit{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.index),
+                  __builtin_amdgcn_readfirstlane(p.blocks)};
+}
+
+// The items of the second product, written by one workgroup of the
+// projection's launch: at most `chunk` rows of one expert each, at least one
+// per expert, in classes of falling length (the order within a class has no
+// part in the results). The first item of an expert goes to S, the others to
+// a partial sketch each.
+struct EsItem {
+    int expert;             // -1: there are fewer items
+    int begin, rows;        // sorted rows
+    int block;              // first block of P
+    int part;               // partial sketch, -1 for S
+    int pad[3];
+};
+struct EsParts {
+    int first, count;       // an expert's partial sketches
+};
+constexpr int kEsClasses = 16;
 
 __device__ __forceinline__ int es_items(int count, int chunk) { return count > chunk ? (count + chunk - 1) / chunk : 1; }
 
-// unit_rows > 0: units of that many rows; 0: units are items (es_items), and
-// those of experts with more than half an item's rows come first, then those
-// with more than an eighth, then the rest, so that long items do not start
-// last. All lanes of the wave call it.
-__device__ __forceinline__ EsPlace es_find(const int32_t *offsets, int E, int N, int chunk, int u, int unit_rows) {
-    const int lane = threadIdx.x & 63;
-    EsPlace p{-1, 0, 0, 0};
-    int before_u = 0;
-    for (int size = unit_rows ? 2 : 0; size < 3 && p.expert < 0; ++size) {
-    int before_b = 0, before_x = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        int nb = 0, nx = 0, nu = 0;
-        if (e < E) {
-            const int count = es_range(offsets, e, N).count;
-            nb = (count + kEsTokens - 1) / kEsTokens;
-            nx = es_items(count, chunk) - 1;
-            const int of = 2 * count > chunk ? 0 : 8 * count > chunk ? 1 : 2;
-            nu = unit_rows ? (count + unit_rows - 1) / unit_rows : of == size ? nx + 1 : 0;
-        }
-        int iu = nu, ib = nb, ix = nx;       // inclusive sums over the lanes
+__device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, int N, int chunk, int max_items,
+                                               EsItem *__restrict__ items, EsParts *__restrict__ experts, int *lds) {
+    int *sum_b = lds, *sum_x = lds + kMaxExperts, *slot = lds + 2 * kMaxExperts;
+    const int tid = threadIdx.x, lane = tid & 63, n_threads = blockDim.x;
+    for (int i = tid; i < max_items; i += n_threads) items[i].expert = -1;
+    if (tid < kEsClasses) slot[tid] = 0;
+    for (int e = tid; e < E; e += n_threads) {
+        const int count = es_range(offsets, e, N).count;
+        sum_b[e] = (count + kEsTokens - 1) / kEsTokens;
+        sum_x[e] = es_items(count, chunk) - 1;
+    }
+    __syncthreads();
+    if (tid < 64) {          // exclusive sums, by one wave
+        int before_b = 0, before_x = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + lane;
+            const int nb = e < E ? sum_b[e] : 0, nx = e < E ? sum_x[e] : 0;
+            int ib = nb, ix = nx;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int a = __shfl_up(iu, o), b = __shfl_up(ib, o), c = __shfl_up(ix, o);
-            if (lane >= o) {
-                iu += a;
-                ib += b;
-                ix += c;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int a = __shfl_up(ib, o), b = __shfl_up(ix, o);
+                if (lane >= o) {
+                    ib += a;
+                    ix += b;
+                }
             }
+            if (e < E) {
+                sum_b[e] = before_b + ib - nb;
+                sum_x[e] = before_x + ix - nx;
+            }
+            before_b += __builtin_amdgcn_readlane(ib, 63);
+            before_x += __builtin_amdgcn_readlane(ix, 63);
         }
-        const uint64_t past = __ballot(before_u + iu > u);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            p.expert = e0 + l;
-            p.index = u - before_u - __builtin_amdgcn_readlane(iu - nu, l);
-            p.blocks = before_b + __builtin_amdgcn_readlane(ib - nb, l);
-            p.extras = before_x + __builtin_amdgcn_readlane(ix - nx, l);
-            break;
+    }
+    __syncthreads();
+    // class 0: the longest
+    auto class_of = [&](int rows) {
+        return kEsClasses - 1 - static_cast<int>(static_cast<int64_t>(rows > 0 ? rows - 1 : 0) * kEsClasses / chunk);
+    };
+    for (int e = tid; e < E; e += n_threads) {
+        const int count = es_range(offsets, e, N).count, n = es_items(count, chunk);
+        if (n > 1) atomicAdd(&slot[class_of(chunk)], n - 1);
+        atomicAdd(&slot[class_of(count - (n - 1) * chunk)], 1);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int at = 0;
+        for (int c = 0; c < kEsClasses; ++c) {
+            const int n = slot[c];
+            slot[c] = at;
+            at += n;
         }
-        before_u += __builtin_amdgcn_readlane(iu, 63);
-        before_b += __builtin_amdgcn_readlane(ib, 63);
-        before_x += __builtin_amdgcn_readlane(ix, 63);
     }
+    __syncthreads();
+    for (int e = tid; e < E; e += n_threads) {
+        const EsRange r = es_range(offsets, e, N);
+        const int n = es_items(r.count, chunk);
+        for (int i = 0; i < n; ++i) {
+            const int rows = min(chunk, r.count - i * chunk);
+            const int at = atomicAdd(&slot[class_of(rows)], 1);
+            if (at < max_items)
+                items[at] = EsItem{e, r.begin + i * chunk, rows, sum_b[e] + i * (chunk / kEsTokens),
+                                   i == 0 ? -1 : sum_x[e] + i - 1, {0, 0, 0}};
+        }
+        experts[e] = EsParts{sum_x[e], n - 1};
     }
-    // the same in all lanes: kept in scalar registers
-    return EsPlace{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.index),
-                   __builtin_amdgcn_readfirstlane(p.blocks), __builtin_amdgcn_readfirstlane(p.extras)};
 }
 
 __device__ __forceinline__ uint64_t es_key(const ExpertSketchArgs &a, int e) {
@@ -142,7 +217,9 @@ __device__ __forceinline__ int64_t es_x_row(const ExpertSketchArgs &a, int i) {
 constexpr int kEsWaves = 8, kEsWords = 8;
 
 template <int R>
-__global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int chunk, int K,
+__global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int chunk, int K, int64_t p_blocks,
+                                                         int max_items,
+                                                         EsItem *__restrict__ items, EsParts *__restrict__ experts,
                                                          float *__restrict__ P) {
     constexpr int RT = R < 128 ? R : 128, NB = RT / 16, MB = 2;
     constexpr int kTileLd = kEsTokens + 4;
@@ -154,7 +231,13 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int l0 = blockIdx.y * RT;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, kEsTokens);
+    if (blockIdx.x == 0) {
+        if (blockIdx.y == 0)
+            es_build_items(a.offsets, a.E, static_cast<int>(a.N), chunk, max_items, items, experts,
+                           reinterpret_cast<int *>(smem));
+        return;
+    }
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x - 1, kEsTokens);
     if (at.expert < 0) return;
     const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int n = min(kEsTokens, rows.count - at.index * kEsTokens);       // rows of this block
@@ -224,12 +307,14 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
         for (int nb = 0; nb < NB; ++nb)
             *reinterpret_cast<f32x4_t *>(&tile[(wave * RT + 16 * nb + i16) * kTileLd + 16 * mb + 4 * g]) = acc[mb][nb];
     __syncthreads();
+    const int64_t block = static_cast<int64_t>(at.blocks) + at.index;
+    if (block >= p_blocks) return;
     for (int q = tid; q < RT * 8; q += 512) {      // four rows of one column
         const int col = q >> 3, t = 4 * (q & 7);
         f32x4_t v = zero_f32x4();
 #pragma unroll
         for (int w = 0; w < kEsWaves; ++w) v += *reinterpret_cast<const f32x4_t *>(&tile[(w * RT + col) * kTileLd + t]);
-        *reinterpret_cast<f32x4_t *>(P + (static_cast<int64_t>(blockIdx.x) * R + l0 + col) * kEsTokens + t) = a.c * v;
+        *reinterpret_cast<f32x4_t *>(P + (block * R + l0 + col) * kEsTokens + t) = a.c * v;
     }
 }
 
@@ -276,7 +361,10 @@ __device__ __forceinline__ u32x4_t es_signs(uint64_t word, uint32_t sel, uint32_
 
 template <int R>
 __global__ __launch_bounds__(256, 2) void es_project_wide_kernel(ExpertSketchArgs a, int chunk, int K,
-                                                                 int64_t p_blocks, float *__restrict__ P) {
+                                                                 int64_t p_blocks, int max_items,
+                                                                 EsItem *__restrict__ items,
+                                                                 EsParts *__restrict__ experts,
+                                                                 float *__restrict__ P) {
     constexpr int MB = kEsWideRows / 32, NB = 2;
     __shared__ __attribute__((aligned(16))) char smem[4 * kEsXBuf];
     __shared__ uint64_t words[4][64];
@@ -288,9 +376,15 @@ __global__ __launch_bounds__(256, 2) void es_project_wide_kernel(ExpertSketchArg
     // both column tiles of a unit on one XCD (workgroup ids are dealt
     // round-robin over the XCDs), whose L2 then serves the second one's X
     constexpr int CT = R / kEsWideCols;
-    const int j = blockIdx.x / kXcds;
+    if (blockIdx.x < kXcds) {
+        if (blockIdx.x == 0)
+            es_build_items(a.offsets, a.E, static_cast<int>(a.N), chunk, max_items, items, experts,
+                           reinterpret_cast<int *>(smem));
+        return;
+    }
+    const int j = blockIdx.x / kXcds - 1;
     const int unit = j / CT * kXcds + static_cast<int>(blockIdx.x % kXcds);
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, unit, kEsWideRows);
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), unit, kEsWideRows);
     if (at.expert < 0) return;
     const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int r0 = at.index * kEsWideRows;
@@ -444,8 +538,9 @@ __device__ __forceinline__ void es_split(u32x4_t lo, u32x4_t hi, u32x4_t (&p)[kE
 }
 
 template <int R>
-__global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int chunk, int D, int tiles,
-                                                         int items, int64_t p_blocks, int64_t max_extras,
+__global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int D, int tiles, int max_items,
+                                                         int64_t p_blocks, int64_t max_extras,
+                                                         const EsItem *__restrict__ items,
                                                          const float *__restrict__ P, float *__restrict__ parts) {
     constexpr int WN = R / 32 < 4 ? R / 32 : 4;         // waves across the columns
     constexpr int WM = 4 / WN;                          // waves across the rows
@@ -458,24 +553,19 @@ __global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int
     // workgroup ids are dealt round-robin over the XCDs: the tiles of an item
     // go to one XCD, whose L2 then holds its P
     const int j = blockIdx.x / kXcds;
-    const int item = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), d0 = j % tiles * kEsRows;
-    if (item >= items) return;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, item, 0);
-    if (at.expert < 0) return;
-    const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
-    const int r0 = at.index * chunk;
-    const int n = min(chunk, rows.count - r0);
-    const int64_t block0 = static_cast<int64_t>(at.blocks) + r0 / kEsTokens;
+    const int number = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), d0 = j % tiles * kEsRows;
+    if (number >= max_items) return;
+    const EsItem item = items[number];
+    if (item.expert < 0) return;
+    const int n = item.rows;
+    const int64_t block0 = item.block;
     const int steps = static_cast<int>(min(static_cast<int64_t>((n + kEsTokens - 1) / kEsTokens),
                                            max(static_cast<int64_t>(0), p_blocks - block0)));
-    // where the tile goes: the first item of an expert to S, the others to a
-    // partial sketch each, added to S by es_reduce_kernel
-    float *dst = a.S + static_cast<int64_t>(at.expert) * D * R;
+    float *dst = a.S + static_cast<int64_t>(item.expert) * D * R;
     bool add = a.accumulate != 0;
-    if (at.index > 0) {
-        const int64_t x = static_cast<int64_t>(at.extras) + at.index - 1;
-        if (x >= max_extras) return;
-        dst = parts + x * D * R;
+    if (item.part >= 0) {       // added to S by es_reduce_kernel
+        if (item.part >= max_extras) return;
+        dst = parts + static_cast<int64_t>(item.part) * D * R;
         add = false;
     } else if (n <= 0 && add) {
         return;
@@ -492,7 +582,7 @@ __global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int
         // A dY tile in LDS: row t, 16-column block b at block b ^ swizzle(t)
         // of the row, so that the rows a transposed read touches at once lie
         // in different banks.
-        const uint16_t *dy = static_cast<const uint16_t *>(a.dY) + (static_cast<int64_t>(rows.begin) + r0) * a.lddy;
+        const uint16_t *dy = static_cast<const uint16_t *>(a.dY) + static_cast<int64_t>(item.begin) * a.lddy;
         const uint32_t ld_bytes = static_cast<uint32_t>(a.lddy * 2);
         const int lt = tid >> 4, lc = tid & 15;         // this thread's rows (lt, lt + 16) and 8-column piece
         auto swizzle = [](int t) { return (t & 3) | ((t >> 1) & 4); };
@@ -580,21 +670,14 @@ __global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int
 }
 
 // S_e += the partial sketches of expert e, in their order.
-__global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int chunk, int64_t size,
-                                                        int64_t max_extras, const float *__restrict__ parts) {
-    // expert e's partial sketches follow those of the experts before it
-    const int e = blockIdx.y;
-    const int own = es_items(es_range(a.offsets, e, static_cast<int>(a.N)).count, chunk) - 1;
-    if (own == 0) return;
-    const int lane = threadIdx.x & 63;
-    int before = 0;
-    for (int e0 = 0; e0 < e; e0 += 64)
-        if (e0 + lane < e) before += es_items(es_range(a.offsets, e0 + lane, static_cast<int>(a.N)).count, chunk) - 1;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
-    float *S = a.S + static_cast<int64_t>(e) * size;
-    const float *p = parts + static_cast<int64_t>(before) * size;
-    const int n = static_cast<int>(min(static_cast<int64_t>(own), max(static_cast<int64_t>(0), max_extras - before)));
+__global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int64_t size, int64_t max_extras,
+                                                        const EsParts *__restrict__ experts,
+                                                        const float *__restrict__ parts) {
+    const EsParts own = experts[blockIdx.y];
+    if (own.count == 0) return;
+    float *S = a.S + static_cast<int64_t>(blockIdx.y) * size;
+    const float *p = parts + static_cast<int64_t>(own.first) * size;
+    const int n = static_cast<int>(min(static_cast<int64_t>(own.count), max(static_cast<int64_t>(0), max_extras - own.first)));
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
          i += static_cast<int64_t>(gridDim.x) * 1024) {
         f32x4_t v = *reinterpret_cast<const f32x4_t *>(S + i);
@@ -606,12 +689,12 @@ __global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int 
 // ------------------------------------------------------------------- fp32 --
 // As sketch_f32.hip: fp32 FMAs over LDS tiles of 32 x 32, sums in index
 // order. P is N x r, row i of the sorted rows in row i.
-__global__ __launch_bounds__(256) void es_project_f32_kernel(ExpertSketchArgs a, int chunk, int K, float *__restrict__ P) {
+__global__ __launch_bounds__(256) void es_project_f32_kernel(ExpertSketchArgs a, int K, float *__restrict__ P) {
     __shared__ float xs[32][65];
     __shared__ uint64_t words[32];
     __shared__ int64_t row_of[32];
     const int R = a.R, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const EsPlace at = es_find(a.offsets, a.E, static_cast<int>(a.N), chunk, blockIdx.x, kEsTokens);
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x, kEsTokens);
     if (at.expert < 0) return;
     const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
     const int i0 = rows.begin + at.index * 32, n = min(32, rows.count - at.index * 32);
@@ -705,38 +788,40 @@ ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int 
     p.extras = N / p.chunk;
     p.items = E + p.extras;
     p.p_bytes = static_cast<size_t>(p.p_blocks) * R * kEsTokens * 4;
-    p.total = p.p_bytes + static_cast<size_t>(p.extras) * d * R * 4;
+    p.table_bytes = (static_cast<size_t>(p.items) * sizeof(EsItem) + E * sizeof(EsParts) + 255) / 256 * 256;
+    p.total = p.table_bytes + p.p_bytes + static_cast<size_t>(p.extras) * d * R * 4;
     return p;
 }
 
 template <int R>
 static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st) {
     const ExpertSketchPlan p = plan_expert_sketch(a.N, a.E, a.d, a.k, R, 1);
-    float *P = static_cast<float *>(a.ws);
-    float *parts = reinterpret_cast<float *>(static_cast<char *>(a.ws) + p.p_bytes);
-    const int D = static_cast<int>(a.d), K = static_cast<int>(a.k);
-    const int64_t wide = a.N / kEsWideRows + (a.N < a.E ? a.N : a.E);      // kEsWideRows-row units at most
-    if (p.p_blocks > 0) {
-        bool done = false;
-        if constexpr (R >= 128) {
-            done = a.N >= kEsWideFrom;
-            if (done)
-                hipLaunchKernelGGL(es_project_wide_kernel<R>, dim3((wide + kXcds - 1) / kXcds * kXcds * (R / kEsWideCols)),
-                                   dim3(256), 0, st, a, p.chunk,
-                                   K, p.p_blocks, P);
+    char *ws = static_cast<char *>(a.ws);
+    EsItem *items = reinterpret_cast<EsItem *>(ws);
+    EsParts *experts = reinterpret_cast<EsParts *>(items + p.items);
+    float *P = reinterpret_cast<float *>(ws + p.table_bytes);
+    float *parts = reinterpret_cast<float *>(ws + p.table_bytes + p.p_bytes);
+    const int D = static_cast<int>(a.d), K = static_cast<int>(a.k), n_items = static_cast<int>(p.items);
+    bool done = false;
+    if constexpr (R >= 128) {
+        done = a.N >= kEsWideFrom;
+        if (done) {
+            const int64_t units = a.N / kEsWideRows + (a.N < a.E ? a.N : a.E);      // at most
+            const int64_t wgs = ((units + kXcds - 1) / kXcds * (R / kEsWideCols) + 1) * kXcds;
+            hipLaunchKernelGGL(es_project_wide_kernel<R>, dim3(wgs), dim3(256), 0, st, a, p.chunk, K, p.p_blocks,
+                               n_items, items, experts, P);
         }
-        if (!done)
-            hipLaunchKernelGGL(es_project_kernel<R>, dim3(p.p_blocks, R < 128 ? 1 : R / 128), dim3(512), 0, st, a,
-                               p.chunk, K, P);
     }
+    if (!done)
+        hipLaunchKernelGGL(es_project_kernel<R>, dim3(p.p_blocks + 1, R < 128 ? 1 : R / 128), dim3(512), 0, st, a,
+                           p.chunk, K, p.p_blocks, n_items, items, experts, P);
     const int tiles = (D + kEsRows - 1) / kEsRows;
-    const int64_t wgs = (p.items + kXcds - 1) / kXcds * kXcds * tiles;
-    hipLaunchKernelGGL(es_fold_kernel<R>, dim3(wgs), dim3(256), 0, st, a, p.chunk, D, tiles,
-                       static_cast<int>(p.items), p.p_blocks, p.extras, P, parts);
+    hipLaunchKernelGGL(es_fold_kernel<R>, dim3((p.items + kXcds - 1) / kXcds * kXcds * tiles), dim3(256), 0, st, a, D,
+                       tiles, n_items, p.p_blocks, p.extras, items, P, parts);
     if (p.extras > 0) {
         const int64_t size = a.d * R;
-        const int64_t n = (size + 4095) / 4096;
-        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 32 ? n : 32, a.E), dim3(256), 0, st, a, p.chunk, size, p.extras,
+        const int64_t n = (size + 1023) / 1024;
+        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 64 ? n : 64, a.E), dim3(256), 0, st, a, size, p.extras, experts,
                            parts);
     }
     return hipGetLastError();
@@ -748,7 +833,7 @@ hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t
         float *P = static_cast<float *>(a.ws);
         const unsigned lt = (a.R + 31) / 32;
         if (p.p_blocks > 0)
-            hipLaunchKernelGGL(es_project_f32_kernel, dim3(p.p_blocks, lt), dim3(256), 0, st, a, p.chunk,
+            hipLaunchKernelGGL(es_project_f32_kernel, dim3(p.p_blocks, lt), dim3(256), 0, st, a,
                                static_cast<int>(a.k), P);
         hipLaunchKernelGGL(es_fold_f32_kernel, dim3((a.d + 31) / 32, lt, a.E), dim3(256), 0, st, a,
                            static_cast<int>(a.d), P);
