@@ -24,7 +24,10 @@ namespace logra {
 
 // ------------------------------------------------------------------- sort --
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortSingle = 8192;     // pairs one workgroup sorts alone
+// Up to kSortSelf pairs the sort is one launch: every workgroup counts all
+// pairs itself and places its own kSortChunk of them. Above that a launch of
+// counts goes first, whose sums the workgroups then add up.
+constexpr int kSortSelf = 4096, kSortChunk = 1024;
 constexpr int kSortMaxBlocks = 256;
 
 struct SortPlan {
@@ -34,13 +37,9 @@ struct SortPlan {
 
 static SortPlan plan_sort(int64_t n) {
     SortPlan p;
-    if (n <= kSortSingle) {
-        p.chunk = static_cast<int>((n + 1023) / 1024 * 1024);
-        return p;
-    }
-    const int64_t c = (n + kSortMaxBlocks - 1) / kSortMaxBlocks;
-    p.chunk = static_cast<int>((c < 2048 ? 2048 : c) + 1023) / 1024 * 1024;
-    p.blocks = static_cast<int>((n + p.chunk - 1) / p.chunk);
+    const int64_t c = n <= kSortSelf ? 1 : (n + kSortMaxBlocks - 1) / kSortMaxBlocks;
+    p.chunk = static_cast<int>((c + kSortChunk - 1) / kSortChunk * kSortChunk);
+    if (n > p.chunk) p.blocks = static_cast<int>((n + p.chunk - 1) / p.chunk);
     return p;
 }
 
@@ -50,8 +49,11 @@ struct SortIds {
     int K, E, wide;
     // expert of pair p, E for a dropped one
     __device__ __forceinline__ int operator()(int64_t p) const {
-        const uint32_t t = static_cast<uint32_t>(p) / static_cast<uint32_t>(K);
-        const int64_t at = t * ld + (static_cast<uint32_t>(p) - t * static_cast<uint32_t>(K));
+        int64_t at = p;
+        if (ld != K) {
+            const uint32_t t = static_cast<uint32_t>(p) / static_cast<uint32_t>(K);
+            at = t * ld + (static_cast<uint32_t>(p) - t * static_cast<uint32_t>(K));
+        }
         const int64_t id = wide ? reinterpret_cast<const int64_t *>(ids)[at]
                                 : static_cast<int64_t>(reinterpret_cast<const int32_t *>(ids)[at]);
         return id >= 0 && id < E ? static_cast<int>(id) : E;
@@ -129,8 +131,21 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids,
                 atomicAdd(&before[e], b);
             }
     } else {
+        // the other chunks' pairs, eight at a time per thread
+        for (int64_t q0 = tid; q0 < n; q0 += 8 * kSortThreads) {
+            int e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t p = q0 + i * kSortThreads;
+                e[i] = p < n && (p < p0 || p >= p0 + chunk) ? ids(p) : E;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e[i] < E) atomicAdd(&(q0 + i * kSortThreads < p0 ? before : total)[e[i]], 1);
+        }
+        __syncthreads();
         for (int e = tid; e < E; e += kSortThreads) {
-            int t = 0;
+            int t = total[e] + before[e];
             for (int w = 0; w < kSortWaves; ++w) t += cnt[w * E + e];
             total[e] = t;
         }
@@ -191,7 +206,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids,
 
 size_t expert_sort_workspace(int64_t n, int E) {
     const SortPlan p = plan_sort(n);
-    return p.blocks > 1 ? static_cast<size_t>(p.blocks) * E * 4 : 0;
+    return n > kSortSelf ? static_cast<size_t>(p.blocks) * E * 4 : 0;
 }
 
 hipError_t launch_expert_sort(int64_t T, int K, int E, const void *ids, int id_bytes, int64_t ld_ids,
@@ -201,7 +216,7 @@ hipError_t launch_expert_sort(int64_t T, int K, int E, const void *ids, int id_b
     const SortIds s{ids, ld_ids, K, E, id_bytes == 8 ? 1 : 0};
     int bits = 1;
     while ((1 << bits) <= E) ++bits;      // values 0 .. E
-    int32_t *hist = p.blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
+    int32_t *hist = n > kSortSelf ? static_cast<int32_t *>(ws) : nullptr;
     if (hist) hipLaunchKernelGGL(sort_hist_kernel, dim3(p.blocks), dim3(kSortThreads), 0, st, s, n, p.chunk, hist);
     hipLaunchKernelGGL(sort_scatter_kernel, dim3(p.blocks), dim3(kSortThreads), (kSortWaves + 2) * E * 4, st, s, n,
                        p.chunk, bits, hist, offsets, order, slots);

@@ -42,7 +42,8 @@ def _same_sort(got, ids, E):
 
 @pytest.mark.parametrize("T,K,E", [(0, 2, 4), (1, 1, 1), (1, 8, 128), (16, 8, 128), (63, 1, 7), (65, 64, 3),
                                    (1000, 3, 60), (1024, 8, 8), (1025, 8, 256), (5000, 4, 1024), (300, 5, 1000),
-                                   (30001, 2, 17), (70001, 8, 129)])
+                                   (30001, 2, 17), (512, 8, 64),
+                                   (1366, 3, 1024), (70001, 8, 129)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_sort(T, K, E, dtype):
     dev = device()
