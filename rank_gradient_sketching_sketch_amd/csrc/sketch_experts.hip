@@ -687,86 +687,152 @@ __global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int6
 }
 
 // ------------------------------------------------------------------- fp32 --
-// As sketch_f32.hip: fp32 FMAs over LDS tiles of 32 x 32, sums in index
-// order. P is N x r, row i of the sorted rows in row i.
-__global__ __launch_bounds__(256) void es_project_f32_kernel(ExpertSketchArgs a, int K, float *__restrict__ P) {
-    __shared__ float xs[32][65];
-    __shared__ uint64_t words[32];
-    __shared__ int64_t row_of[32];
-    const int R = a.R, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+// Both products on the fp32 matrix instructions (fp32 products and sums), any
+// shape. P is N x r, row i of the sorted rows in row i. A workgroup owns a
+// tile of the result and its waves split the contraction, adding their tiles
+// through LDS in wave order. Operands come straight from memory: the calls
+// this path is for are short, and what bounds them is the latency of a few
+// loads, which more waves over fewer steps hide best.
+constexpr int kEsF32Waves = 8;
+
+// D = A(16x4) * B(4x16) + C. Lane L holds A[L%16][L/16], B[L/16][L%16] and
+// D[4*(L/16) .. +3][L%16].
+__device__ __forceinline__ f32x4_t mfma_f32(float a, float b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+typedef f32x4_t f32x4_a4_t __attribute__((aligned(4)));     // rows need only their element's alignment
+
+// Adds the waves' tiles of MT x NT blocks in wave order and calls
+// store(row, column, value) for every element (row and column in the tile).
+template <int MT, int NT, class Store>
+__device__ __forceinline__ void es_f32_join(f32x4_t (&acc)[MT][NT], float *lds, Store store) {
+    constexpr int kLd = 16 * MT + 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<f32x4_t *>(&lds[(wave * 16 * NT + 16 * n + i16) * kLd + 16 * m + 4 * g]) = acc[m][n];
+    __syncthreads();
+    for (int q = tid; q < 16 * MT * 16 * NT; q += 64 * kEsF32Waves) {
+        const int row = q / (16 * NT), col = q - row * 16 * NT;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEsF32Waves; ++w) v += lds[(w * 16 * NT + col) * kLd + row];
+        store(row, col, v);
+    }
+}
+
+__global__ __launch_bounds__(64 * kEsF32Waves) void es_project_f32_kernel(ExpertSketchArgs a, int K,
+                                                                          float *__restrict__ P) {
+    constexpr int MT = kEsTokens / 16, NT = 2;
+    __shared__ __attribute__((aligned(16))) float lds[kEsF32Waves * 16 * NT * (16 * MT + 4)];
+    const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x, kEsTokens);
     if (at.expert < 0) return;
     const EsRange rows = es_range_uniform(a.offsets, at.expert, static_cast<int>(a.N));
-    const int i0 = rows.begin + at.index * 32, n = min(32, rows.count - at.index * 32);
-    const int l0 = blockIdx.y * 32, l = l0 + tx;
+    const int i0 = rows.begin + at.index * kEsTokens, n = min(kEsTokens, rows.count - at.index * kEsTokens);
+    const int l0 = blockIdx.y * 16 * NT;
     const uint64_t key = es_key(a, at.expert);
-    if (threadIdx.x < 32)
-        row_of[threadIdx.x] = static_cast<int>(threadIdx.x) < n ? es_x_row(a, i0 + threadIdx.x) : -1;
-    __syncthreads();
-    const float *X = static_cast<const float *>(a.X);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < K; j0 += 64) {
-        for (int e = 0; e < 8; ++e) {
-            const int idx = threadIdx.x + 256 * e, t = idx >> 6, j = idx & 63;
-            const int64_t row = row_of[t];
-            xs[t][j] = row >= 0 && j0 + j < K ? X[row * a.ldx + j0 + j] : 0.f;
-        }
-        if (threadIdx.x < 32)
-            words[threadIdx.x] = sign_word(key, static_cast<uint32_t>(l0 + threadIdx.x), static_cast<uint32_t>(j0 >> 6));
-        __syncthreads();
-        const uint64_t w = words[tx];
-        const int jn = min(64, K - j0);
-        for (int j = 0; j < jn; ++j) {
-            const float sg = ((w >> j) & 1ull) ? -1.f : 1.f;
+    const float *xrow[MT];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = fmaf(sg, xs[ty + 8 * q][j], acc[q]);
-        }
-        __syncthreads();
+    for (int m = 0; m < MT; ++m) {
+        const int64_t row = 16 * m + i16 < n ? es_x_row(a, i0 + 16 * m + i16) : -1;
+        xrow[m] = row < 0 ? nullptr : static_cast<const float *>(a.X) + row * a.ldx;
     }
-    if (l < R)
+    f32x4_t acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[m][q] = zero_f32x4();
+    // 64 columns of k per step; piece q of a lane is columns 16 q + 4 g .. +3, so
+    // that the lane's four loads are one row's and its four products' k agree
+    // between X and the signs
+    for (int b = wave; b < (K + 63) / 64; b += kEsF32Waves) {
+        f32x4_t x[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = 64 * b + 16 * q + 4 * g;
+                x[m][q] = zero_f32x4();
+                if (xrow[m] && k + 4 <= K) x[m][q] = *reinterpret_cast<const f32x4_a4_t *>(xrow[m] + k);
+                else if (xrow[m])
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (k + e < K) x[m][q][e] = xrow[m][k + e];
+            }
+        uint64_t w[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            w[t] = sign_word(key, static_cast<uint32_t>(l0 + 16 * t + i16), static_cast<uint32_t>(b)) >> (4 * g);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            if (ty + 8 * q < n) P[static_cast<int64_t>(i0 + ty + 8 * q) * R + l] = a.c * acc[q];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t bit = static_cast<uint32_t>(w[t] >> (16 * q)) << (31 - e);
+                    const float sign = __uint_as_float((bit & 0x80000000u) | 0x3F800000u);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[m][t] = mfma_f32(x[m][q][e], sign, acc[m][t]);
+                }
+    }
+    const int R = a.R;
+    es_f32_join(acc, lds, [&](int row, int col, float v) {
+        if (row < n && l0 + col < R) P[static_cast<int64_t>(i0 + row) * R + l0 + col] = a.c * v;
+    });
 }
 
-__global__ __launch_bounds__(256) void es_fold_f32_kernel(ExpertSketchArgs a, int D, const float *__restrict__ P) {
-    __shared__ float ds[32][33];
-    __shared__ float ps[32][33];
-    const int R = a.R, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const EsRange rows = es_range(a.offsets, blockIdx.z, static_cast<int>(a.N));
-    const int d0 = blockIdx.x * 32, l0 = blockIdx.y * 32;
+template <int T>
+__global__ __launch_bounds__(64 * kEsF32Waves) void es_fold_f32_kernel(ExpertSketchArgs a, int D,
+                                                                       const float *__restrict__ P) {
+    __shared__ __attribute__((aligned(16))) float lds[kEsF32Waves * 16 * T * (16 * T + 4)];
+    const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const EsRange rows = es_range_uniform(a.offsets, blockIdx.z, static_cast<int>(a.N));
+    if (rows.count == 0 && a.accumulate) return;
+    const int R = a.R, d0 = blockIdx.x * 16 * T, l0 = blockIdx.y * 16 * T;
     const float *dY = static_cast<const float *>(a.dY);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t0 = 0; t0 < rows.count; t0 += 32) {
-        for (int e = 0; e < 4; ++e) {
-            const int idx = threadIdx.x + 256 * e, t = idx >> 5, c = idx & 31;
-            const int64_t i = static_cast<int64_t>(rows.begin) + t0 + t;
-            const bool in = t0 + t < rows.count;
-            ds[t][c] = in && d0 + c < D ? dY[i * a.lddy + d0 + c] : 0.f;
-            ps[t][c] = in && l0 + c < R ? P[i * R + l0 + c] : 0.f;
-        }
-        __syncthreads();
-        const int tn = min(32, rows.count - t0);
-        for (int t = 0; t < tn; ++t) {
-            const float p = ps[t][tx];
+    f32x4_t acc[T][T];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = fmaf(ds[t][ty + 8 * q], p, acc[q]);
-        }
-        __syncthreads();
-    }
-    float *S = a.S + static_cast<int64_t>(blockIdx.z) * D * R;
-    if (l0 + tx < R)
+    for (int m = 0; m < T; ++m)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = d0 + ty + 8 * q;
-            if (i < D) {
-                float *dst = S + static_cast<int64_t>(i) * R + l0 + tx;
-                *dst = (a.accumulate ? *dst : 0.f) + acc[q];
+        for (int n = 0; n < T; ++n) acc[m][n] = zero_f32x4();
+    constexpr int U = T > 2 ? 2 : 4;       // steps of four rows in flight
+    for (int t0 = 4 * U * wave; t0 < rows.count; t0 += 4 * U * kEsF32Waves) {
+        float av[U][T], bv[U][T];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 4 * u + g;
+            const int64_t i = static_cast<int64_t>(rows.begin) + t;
+            const bool in = t < rows.count;
+#pragma unroll
+            for (int q = 0; q < T; ++q) {
+                const int d = d0 + 16 * q + i16, l = l0 + 16 * q + i16;
+                av[u][q] = in && d < D ? dY[i * a.lddy + d] : 0.f;
+                bv[u][q] = in && l < R ? P[i * R + l] : 0.f;
             }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < T; ++n)
+#pragma unroll
+                for (int m = 0; m < T; ++m) acc[m][n] = mfma_f32(av[u][m], bv[u][n], acc[m][n]);
+    }
+    float *S = a.S + static_cast<int64_t>(blockIdx.z) * D * R;
+    es_f32_join(acc, lds, [&](int row, int col, float v) {
+        if (d0 + row >= D || l0 + col >= R) return;
+        float *p = S + static_cast<int64_t>(d0 + row) * R + l0 + col;
+        *p = a.accumulate ? *p + v : v;
+    });
 }
 
 // ------------------------------------------------------------------ plans --
+constexpr int64_t kEsF32WideFrom = 256;
 constexpr int64_t kEsMaxChunk = 1 << 20;   // an item's part of P stays within a view (r <= 256)
 constexpr int64_t kEsWideFrom = 4096;   // rows from which the wide projection is used
 
@@ -831,12 +897,17 @@ hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t
     if (!bf16) {
         const ExpertSketchPlan p = plan_expert_sketch(a.N, a.E, a.d, a.k, a.R, 0);
         float *P = static_cast<float *>(a.ws);
-        const unsigned lt = (a.R + 31) / 32;
+        const int D = static_cast<int>(a.d), K = static_cast<int>(a.k);
         if (p.p_blocks > 0)
-            hipLaunchKernelGGL(es_project_f32_kernel, dim3(p.p_blocks, lt), dim3(256), 0, st, a,
-                               static_cast<int>(a.k), P);
-        hipLaunchKernelGGL(es_fold_f32_kernel, dim3((a.d + 31) / 32, lt, a.E), dim3(256), 0, st, a,
-                           static_cast<int>(a.d), P);
+            hipLaunchKernelGGL(es_project_f32_kernel, dim3(p.p_blocks, (a.R + 31) / 32), dim3(64 * kEsF32Waves), 0, st,
+                               a, K, P);
+        // tiles of 64 x 64 where they still give each compute unit one, which
+        // reads a quarter of what tiles of 32 x 32 read per product
+        const bool wide = static_cast<int64_t>((a.R + 63) / 64) * ((D + 63) / 64) * a.E >= kEsF32WideFrom;
+        const int tile = wide ? 64 : 32;
+        hipLaunchKernelGGL(wide ? es_fold_f32_kernel<4> : es_fold_f32_kernel<2>,
+                           dim3((D + tile - 1) / tile, (a.R + tile - 1) / tile, a.E), dim3(64 * kEsF32Waves), 0, st, a,
+                           D, P);
         return hipGetLastError();
     }
     switch (a.R) {

@@ -17,13 +17,18 @@ A step, in the order the host drives it:
      sharing a tile of S never wait for each other; otherwise
      logra_sketch_fold (accumulate = 0 for the first microbatch). Matrix i
      runs on sketch lane i mod n_sketch; each lane is a stream with its own
-     workspace.
-  2. pass 1: logra_update_sqnorm for every matrix (v -> v'), in batches of
+     workspace. An expert group (one projection of every expert of a layer)
+     is one call per microbatch, logra_sketch_experts, on a lane of its own
+     turn; its experts are matrices like the others from there on.
+  2. clipping, if the caller asks for it (`clip`): the global norm over every
+     sketch and the caller's dense gradients, and all of them scaled in place
+     (logra_grad_clip).
+  3. pass 1: logra_update_sqnorm for every matrix (v -> v'), in batches of
      up to 16 matrices per apply lane (logra_update_sqnorm_batch: two
      launches per batch), matrix i on apply lane i mod n_apply.
-  3. one device-to-host read of every sqnorm (the host step controller's
+  4. one device-to-host read of every sqnorm (the host step controller's
      input).
-  4. pass 2: logra_rowadam_apply for every matrix given a scale; a matrix
+  5. pass 2: logra_rowadam_apply for every matrix given a scale; a matrix
      that is given none (or whose sqnorm is not finite, when the caller asks
      to skip those) keeps W and v. Each applied matrix then swaps v and v'.
 Every lane forks from the caller's current stream at the start of a phase
@@ -68,6 +73,28 @@ class Matrix:
     alane: int = 0
 
 
+@dataclasses.dataclass
+class ExpertGroup:
+    """One projection of every expert of a layer: expert e's W[e] is d x k and
+    its matrix id matrix_id + e. W (experts x d x k) and v (experts x d) are
+    the caller's state (W updated in place; v read at the first step, then
+    members[e].v is expert e's, as for a Matrix); topk choices of an expert per token make
+    tokens topk rows of dY per microbatch."""
+    n_experts: int
+    d: int
+    k: int
+    matrix_id: int
+    topk: int
+    W: torch.Tensor
+    v: torch.Tensor
+    name: str = ""
+    # allocated by Step
+    S: Optional[torch.Tensor] = None
+    ws: Optional[torch.Tensor] = None
+    members: Optional[List[Matrix]] = None
+    lane: int = 0
+
+
 def _event(stream):
     # timing only: no system-scope fence, which would add its cost to the
     # probed kernel's time and to the step
@@ -78,6 +105,10 @@ class Step:
     """Streams, workspaces and per-phase calls for a fixed set of matrices.
 
     matrices  the Matrix records (W, v on the device).
+    groups    the ExpertGroup records; their experts follow the matrices in
+              `mats`, group by group (sqnorms, scales).
+    grads     dense gradients that `clip` takes along with the sketches
+              (device tensors written in place every step).
     r, tokens the sketch rank and the tokens of every microbatch.
     act_dtype B.LOGRA_BF16 or B.LOGRA_F32 (X, dY and the compute dtype).
     sketch_lanes / apply_lanes  stream counts (0: min(4, n) for the sketch;
@@ -94,21 +125,32 @@ class Step:
 
     def __init__(self, matrices: Sequence[Matrix], r: int, tokens: int, act_dtype: int,
                  device=None, sketch_lanes: int = 0, apply_lanes: int = 0,
-                 batch_pass1: bool = True, seed: int = 0, rowsq: bool = False, parts: str = "pair"):
-        if not matrices:
+                 batch_pass1: bool = True, seed: int = 0, rowsq: bool = False, parts: str = "pair",
+                 groups: Sequence[ExpertGroup] = (), grads: Sequence[torch.Tensor] = ()):
+        if not matrices and not groups:
             raise ValueError("a step needs at least one matrix")
+        self.dense: List[Matrix] = list(matrices)
+        self.groups: List[ExpertGroup] = list(groups)
+        self.grads = list(grads)
         self.mats: List[Matrix] = list(matrices)
+        for g in self.groups:
+            if tuple(g.W.shape) != (g.n_experts, g.d, g.k) or tuple(g.v.shape) != (g.n_experts, g.d):
+                raise ValueError("expert group %s: W experts x d x k and v experts x d expected" % g.name)
+            g.members = [Matrix(g.d, g.k, g.matrix_id + e, g.W[e], g.v[e], "%s.%d" % (g.name, e))
+                         for e in range(g.n_experts)]
+            self.mats.extend(g.members)
         self.r, self.tokens, self.code, self.seed = int(r), int(tokens), int(act_dtype), int(seed)
         dev = torch.device(device) if device is not None else self.mats[0].W.device
         self.device = dev
         n = len(self.mats)
-        self.n_sketch = max(1, min(sketch_lanes or min(MAX_SKETCH_LANES, n), n))
+        n_calls = len(self.dense) + len(self.groups)
+        self.n_sketch = max(1, min(sketch_lanes or min(MAX_SKETCH_LANES, n_calls), n_calls))
         self.n_apply = max(1, min(apply_lanes or (1 if n == 1 else DEFAULT_APPLY_LANES), n))
         self.timeouts = torch.zeros(1, dtype=torch.int32, device=dev)
         self.sketch_opts = B.LaunchOpts(sketch_concurrency=self.n_sketch, fold_timeouts=self.timeouts)
         self.apply_opts = B.LaunchOpts(apply_concurrency=self.n_apply)
-        ws_bytes = max(B.logra_sketch_workspace_bytes(B.MatrixDesc(m.d, m.k, r), tokens, act_dtype)
-                       for m in self.mats)
+        ws_bytes = max([0] + [B.logra_sketch_workspace_bytes(B.MatrixDesc(m.d, m.k, r), tokens, act_dtype)
+                              for m in self.dense])
         sq_ws_bytes = max(B.logra_sqnorm_workspace_bytes(B.MatrixDesc(m.d, m.k, r), act_dtype)
                           for m in self.mats)
         self.main = torch.cuda.current_stream(dev)
@@ -123,9 +165,20 @@ class Step:
         if parts not in ("pair", "all", "none"):
             raise ValueError("parts must be 'pair', 'all' or 'none'")
         self.parts_bytes = 0
+        self.expert_ws_bytes = 0
+        for i, g in enumerate(self.groups):
+            g.lane = (len(self.dense) + i) % self.n_sketch
+            g.S = torch.empty(g.n_experts, g.d, r, dtype=torch.float32, device=dev)
+            nb = max(16, B.logra_sketch_experts_workspace_bytes(B.MatrixDesc(g.d, g.k, r), g.n_experts,
+                                                                tokens * g.topk, act_dtype))
+            g.ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+            self.expert_ws_bytes += nb
+            for m, S in zip(g.members, g.S):
+                m.S = S
         for i, m in enumerate(self.mats):
-            m.S = torch.empty(m.d, r, dtype=torch.float32, device=dev)
-            pb = B.logra_sketch_parts_bytes(B.MatrixDesc(m.d, m.k, r), tokens, act_dtype)
+            if m.S is None or i < len(self.dense):
+                m.S = torch.empty(m.d, r, dtype=torch.float32, device=dev)
+            pb = 0 if i >= len(self.dense) else B.logra_sketch_parts_bytes(B.MatrixDesc(m.d, m.k, r), tokens, act_dtype)
             use = pb > 0 and (parts == "all" or (parts == "pair" and pb == 4 * m.d * r))
             m.parts = torch.empty(pb // 4, dtype=torch.float32, device=dev) if use else None
             self.parts_bytes += pb if use else 0
@@ -159,7 +212,11 @@ class Step:
                                                            act_dtype)
                 self.batch_ws_bytes += wsb
                 self.batches.append((li, chunk, sq, torch.empty(max(16, wsb), dtype=torch.uint8, device=dev)))
-        self.workspace_bytes = n_lanes * (max(16, ws_bytes) + max(16, sq_ws_bytes)) + self.batch_ws_bytes
+        self.workspace_bytes = (n_lanes * (max(16, ws_bytes) + max(16, sq_ws_bytes)) + self.batch_ws_bytes
+                                + self.expert_ws_bytes)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.coef = torch.ones(1, dtype=torch.float32, device=dev)
+        self._grad_list, self._grad_ws = None, None
 
     # ---- streams ---------------------------------------------------------
     def _fork(self):
@@ -182,10 +239,15 @@ class Step:
             m.desc = B.MatrixDesc(m.d, m.k, self.r, seed=self.seed, step=step, matrix_id=m.matrix_id)
 
     def sketch(self, step: int, microbatches: int,
-               inputs: Callable[[int, int], Tuple[torch.Tensor, torch.Tensor]],
-               probe: Optional[Tuple[int, int]] = None):
+               inputs: Optional[Callable[[int, int], Tuple[torch.Tensor, torch.Tensor]]] = None,
+               probe: Optional[Tuple[int, int]] = None,
+               expert_inputs: Optional[Callable[[int, int], Tuple]] = None):
         """Fold `microbatches` microbatches into every matrix's S, microbatch
-        by microbatch; inputs(i, mb) returns (X, dY) of matrix i.
+        by microbatch; inputs(i, mb) returns (X, dY) of matrix i, and
+        expert_inputs(g, mb) returns (X, dY, offsets, order) of group g: dY
+        (tokens topk rows) sorted by expert, offsets and order as
+        logra_expert_sort gives them, X the tokens' activations (or their
+        sorted copy, with order None).
 
         probe = (i, mb), mb >= 1: time matrix i's projection and fold
         without an event between the two (an event record delays the next
@@ -201,7 +263,7 @@ class Step:
         self._fork()
         events = None
         for mb in range(microbatches):
-            for i, m in enumerate(self.mats):
+            for i, m in enumerate(self.dense):
                 X, dY = inputs(i, mb)
                 ln = self.lanes[m.lane]
                 st = ln["stream"]
@@ -221,8 +283,26 @@ class Step:
                     B.logra_sketch_fold(m.desc, dY, m.S, mb > 0, ln["ws"], st, opts=self.sketch_opts)
                 if both:
                     events = (proj_pair, (start, _event(st)))
+            for i, g in enumerate(self.groups):
+                X, dY, offsets, order = expert_inputs(i, mb)
+                if dY.shape[0] != self.tokens * g.topk:
+                    raise ValueError("expert group %s: %d rows of dY expected" % (g.name, self.tokens * g.topk))
+                B.logra_sketch_experts(g.members[0].desc, offsets, X, dY, g.S, mb > 0, order=order, topk=g.topk,
+                                       ws=g.ws, stream=self.lanes[g.lane]["stream"])
         self._join()
         return events
+
+    def clip(self, max_norm: float):
+        """Clip the step's gradients by their global norm: every S (which
+        holds the whole step after `sketch`) and the dense gradients given to
+        Step, in place, before pass 1. Returns the device tensors (norm, coef)
+        without waiting for them; a norm that is not finite clips nothing."""
+        if self._grad_list is None:
+            sketches = [m.S for m in self.dense] + [g.S for g in self.groups]
+            self._grad_list = B.GradList(sketches + self.grads)
+            self._grad_ws = torch.empty(self._grad_list.workspace_bytes, dtype=torch.uint8, device=self.device)
+        B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)
+        return self.norm, self.coef
 
     def pass1(self, beta2: float, eps: float):
         """v' and sqnorm of every matrix (v unchanged)."""

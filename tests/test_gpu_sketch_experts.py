@@ -83,7 +83,8 @@ def test_bf16_matches_oracle(T, K, E, d, k, r, popular, pad):
 
 
 @pytest.mark.parametrize("T,K,E,d,k,r,popular,pad", [(1, 1, 1, 3, 5, 1, None, 0), (40, 2, 6, 45, 130, 20, None, 3),
-                                                     (384, 2, 8, 256, 512, 32, None, 0), (50, 4, 70, 33, 64, 40, 2, 0)])
+                                                     (384, 2, 8, 256, 512, 32, None, 0), (50, 4, 70, 33, 64, 40, 2, 0),
+                                                     (200, 2, 70, 260, 97, 100, None, 5)])
 def test_f32_matches_oracle(T, K, E, d, k, r, popular, pad):
     dev = device()
     say("sketch experts f32", T, K, E, d, k, r, popular, pad)
