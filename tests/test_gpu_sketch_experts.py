@@ -60,6 +60,12 @@ CASES = [
     (1500, 4, 16, 264, 40, 32, 15, 8),
     (31, 2, 70, 40, 2056, 256, None, 0),   # more experts than a wave has lanes
     (900, 2, 3, 1000, 200, 128, None, 0),
+    # enough rows for the wide projection: ragged k, padded rows, one popular expert, more experts than lanes
+    (1100, 4, 9, 136, 520, 256, None, 8),
+    (2100, 2, 5, 72, 200, 128, None, 0),
+    (1200, 4, 70, 40, 2056, 256, 3, 0),
+    (4100, 1, 3, 64, 72, 128, None, 16),
+    (600, 8, 130, 64, 128, 256, None, 0),
 ]
 
 
