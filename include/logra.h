@@ -788,13 +788,17 @@ logra_status logra_expert_combine_backward(int64_t T, int topk, int64_t h, int d
  *   S        n_experts x d x r fp32, contiguous. An expert without rows
  *            keeps its S (accumulate != 0) or gets zeros.
  *   act_dtype LOGRA_BF16: bf16 products with fp32 accumulation; the
- *            projection is kept as two bf16 terms (within 2^-16 of its
- *            fp32 value), so S is close to what fp32 products give. r in
+ *            projection is kept in fp32 and multiplied as three bf16 terms
+ *            (within 2^-24 of it), so S is what fp32 products give, closer
+ *            than logra_sketch_accumulate's, which rounds the projection to
+ *            bf16. r in
  *            {32, 64, 128, 256}; d, k, ldx, lddy multiples of 8; X, dY
  *            16-byte aligned. LOGRA_F32: fp32 throughout, r in [1, 1024].
  *   ws       device, 16-byte aligned, >= logra_sketch_experts_workspace_bytes
  *            bytes; scratch, one for every call in flight.
- * n_experts in [1, 1024], N <= 2^26.
+ * Limits: n_experts in [1, 1024], N <= 2^26, d and k <= 2^22 and
+ *   (n_experts + N / 256 + 8) (d / 128 + 1) < 2^24 (one launch covers all of
+ *   S); bf16 path: X (x_rows ldx elements) below 2^31 bytes, lddy <= 2^24.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE, HIP as there.
  */
 size_t logra_sketch_experts_workspace_bytes(const logra_matrix *m, int n_experts, int64_t N, int act_dtype);

@@ -752,7 +752,7 @@ logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list 
 
 namespace {
 
-constexpr int64_t kMaxPairs = 1ll << 26, kMaxExpertTokens = 1ll << 23;
+constexpr int64_t kMaxPairs = 1ll << 26, kMaxExpertTokens = 1ll << 23, kMaxExpertDim = 1ll << 22;
 
 logra_status check_pairs(int64_t T, int topk) {
     if (T < 0 || topk < 1) return LOGRA_ERR_INVALID_ARGUMENT;
@@ -843,8 +843,13 @@ static logra_status check_sketch_experts(const logra_matrix *m, int n_experts, i
     if (!matrix_ok(m) || n_experts < 1 || N < 0) return LOGRA_ERR_INVALID_ARGUMENT;
     if (act_dtype != LOGRA_F32 && act_dtype != LOGRA_BF16) return LOGRA_ERR_UNSUPPORTED;
     if (n_experts > kMaxExperts || N > kMaxPairs) return LOGRA_ERR_UNSUPPORTED;
+    if (m->d > kMaxExpertDim || m->k > kMaxExpertDim) return LOGRA_ERR_UNSUPPORTED;
     if (act_dtype == LOGRA_BF16 ? !bf16_rank_ok(m->r) || m->d % 8 || m->k % 8 : m->r > 1024)
         return LOGRA_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads in a dimension
+    const ExpertSketchPlan p =
+        plan_expert_sketch(N, n_experts, m->d, m->k, static_cast<int>(m->r), act_dtype == LOGRA_BF16);
+    if ((p.items + 8) * ((m->d + 127) / 128) >= (1ll << 24)) return LOGRA_ERR_UNSUPPORTED;
     return LOGRA_OK;
 }
 

@@ -17,6 +17,8 @@
 // workgroup, so that a token's own row crosses the memory bus once however
 // many experts it goes to. Rows of Xs and dYs that no pair maps to are not
 // written.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -233,6 +235,10 @@ typedef u32x4_t u32x4_e4_t __attribute__((aligned(4)));
 template <int BF16>
 struct RowOf {
     static constexpr int V = BF16 ? 8 : 4;
+    using Elem = std::conditional_t<BF16 != 0, uint16_t, uint32_t>;
+    using Vec = std::conditional_t<BF16 != 0, u32x4_e2_t, u32x4_e4_t>;
+    static __device__ __forceinline__ u32x4_t load_bits(const char *p) { return *reinterpret_cast<const Vec *>(p); }
+    static __device__ __forceinline__ void store_bits(char *p, u32x4_t v) { *reinterpret_cast<Vec *>(p) = v; }
     static __device__ __forceinline__ void load(const char *p, float (&v)[V]) {
         if (BF16) {
             const u32x4_t w = *reinterpret_cast<const u32x4_e2_t *>(p);
@@ -287,6 +293,7 @@ struct RowOf {
     }
 };
 
+// Without weights the rows' bits are copied.
 template <int BF16>
 __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h, const char *__restrict__ X,
                                                                     int64_t ldx, const int32_t *__restrict__ slots,
@@ -296,17 +303,33 @@ __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h
     using R = RowOf<BF16>;
     constexpr int V = R::V, B = BF16 ? 2 : 4;
     const int64_t t = blockIdx.x;
+    const int32_t *slot = slots + t * K;
     for (int c = threadIdx.x * V; c < h; c += kRowThreads * V) {
-        float x[V];
-        R::get(X + (t * ldx + c) * B, h - c, x);
-        for (int j = 0; j < K; ++j) {
-            const int64_t s = slots[t * K + j];
-            if (s < 0 || s >= n_rows) continue;
-            float y[V];
-            const float f = w ? w[t * K + j] : 1.f;
+        const char *src = X + (t * ldx + c) * B;
+        auto each = [&](auto f) {
+            for (int j = 0; j < K; ++j) {
+                const int64_t s = slot[j];
+                if (s >= 0 && s < n_rows) f(Xs + (s * ldxs + c) * B, j);
+            }
+        };
+        if (w) {
+            float x[V];
+            R::get(src, h - c, x);
+            each([&](char *dst, int j) {
+                const float f = w[t * K + j];
+                float y[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = w ? f * x[e] : x[e];
-            R::put(Xs + (s * ldxs + c) * B, h - c, y);
+                for (int e = 0; e < V; ++e) y[e] = f * x[e];
+                R::put(dst, h - c, y);
+            });
+        } else if (h - c >= V) {
+            const u32x4_t x = R::load_bits(src);
+            each([&](char *dst, int) { R::store_bits(dst, x); });
+        } else {
+            for (int e = 0; e < h - c; ++e) {
+                const typename R::Elem x = reinterpret_cast<const typename R::Elem *>(src)[e];
+                each([&](char *dst, int) { reinterpret_cast<typename R::Elem *>(dst)[e] = x; });
+            }
         }
     }
 }

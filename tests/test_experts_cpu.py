@@ -193,6 +193,12 @@ def test_sketch_experts_refusals(B):
     assert call(E=1025) == UNSUP and call(N=(1 << 26) + 1) == UNSUP and call(dt=5) == UNSUP
     assert call(m=B.MatrixDesc(64, 128, 48)) == UNSUP and call(m=B.MatrixDesc(60, 128, 32)) == UNSUP
     assert call(m=B.MatrixDesc(64, 128, 2000), dt=0) == UNSUP
+    assert call(m=B.MatrixDesc((1 << 22) + 8, 128, 32), ldd=1 << 23) == UNSUP
+    assert call(m=B.MatrixDesc(64, (1 << 22) + 8, 32), ldx=1 << 23) == UNSUP
+    assert call(E=1024, m=B.MatrixDesc(1 << 22, 128, 32), ldd=1 << 22) == UNSUP     # S past one launch
+    assert call(ldx=1 << 25, rows=32) == UNSUP                  # X past one buffer view (2^31 bytes)
+    assert call(ldx=(1 << 25) - 8, rows=32, wsb=0) == WS
+    assert call(ldd=(1 << 24) + 8) == UNSUP
     assert call(ws=None) == WS and call(wsb=need - 1) == WS and call(ws=ctypes.c_void_p(0x10008)) == WS
     assert call(N=0, acc=1, ws=None, wsb=0, X=None, dY=None) == OK
     assert B.logra_sketch_experts_workspace_bytes(B.MatrixDesc(64, 128, 48), 4, 100, 1) == 0

@@ -130,6 +130,19 @@ def test_rows_match_oracle(T, K, E, h, pad, off, dt):
     assert np.all(_f64(dw)[~kept] == 0)
 
 
+@pytest.mark.parametrize("dt,raw", [(torch.bfloat16, torch.int16), (torch.float32, torch.int32)])
+def test_gather_without_weights_copies_every_bit_pattern(dt, raw):
+    dev = device()
+    g = torch.Generator().manual_seed(0)
+    lo, hi = torch.iinfo(raw).min, torch.iinfo(raw).max
+    X = torch.randint(lo, hi, (33, 2003), generator=g, dtype=torch.int64).to(raw).to(dev)     # NaNs of every payload
+    offsets, order, slots = _sort(_ids(5, 33, 3, 7).to(dev), 7, dev)
+    Xs = torch.zeros(99, 2003, dtype=raw, device=dev)
+    L.logra_expert_gather(X.view(dt), slots, Xs.view(dt))
+    n = int(offsets[-1])
+    assert torch.equal(Xs[:n], X[order[:n].long() // 3]) and not Xs[n:].any()
+
+
 def test_gather_and_combine_are_each_others_gradient():
     """<combine(Ys, w), G> differentiated: by differences of the forward call
     (the function is linear in Ys and in w, so a difference over a step of 1/4

@@ -160,6 +160,33 @@ def test_rows_and_tokens_that_are_not_named_are_not_read(dt):
     assert torch.equal(S, S2)
 
 
+@pytest.mark.parametrize("T,r,dt", [(60, 64, torch.bfloat16), (2500, 256, torch.bfloat16), (60, 32, torch.float32)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_values_reach_their_own_expert_only(T, r, dt, bad):
+    """A token's non-finite activation or output gradient makes the sketches
+    of its experts non-finite and no other's (T = 2500: the wide projection)."""
+    dev = device()
+    K, E, d, k = 2, 6, 72, 136
+    offsets, order, X, dY = _inputs(3, T, K, E, d, k, dt, dev, drop=0.3)
+    m = L.MatrixDesc(d, k, r)
+    o = offsets.tolist()
+    S = torch.empty(E, d, r, device=dev)
+    first = o[2] + 1                                          # a row of expert 2
+    token = int(order[first]) // K
+    held = {e for e in range(E) if any(int(p) // K == token for p in order[o[e]:o[e + 1]])}
+    X2 = X.clone()
+    X2[token, 5] = bad
+    L.logra_sketch_experts(m, offsets, X2, dY, S, False, order=order, topk=K)
+    for e in range(E):
+        assert bool(torch.isfinite(S[e]).all()) == (e not in held)
+    dY2 = dY.clone()
+    dY2[first, 7] = bad
+    L.logra_sketch_experts(m, offsets, X, dY2, S, False, order=order, topk=K)
+    for e in range(E):
+        assert bool(torch.isfinite(S[e]).all()) == (e != 2)
+    assert not torch.isfinite(S[2, 7]).any() and torch.isfinite(S[2, :7]).all() and torch.isfinite(S[2, 8:]).all()
+
+
 def test_same_as_the_one_matrix_sketch():
     """One expert with every row: the one-matrix call's S to the bf16 path's
     tolerance (that call rounds P to one bf16 term)."""
