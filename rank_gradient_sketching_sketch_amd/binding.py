@@ -596,16 +596,21 @@ class GradList:
         self.device = self.tensors[0].device if self.tensors else torch.device(device or "cuda")
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        items = (_GradTensor * max(1, len(self.tensors)))()
-        for i, t in enumerate(self.tensors):
-            if t.device != self.device or self.device.type != "cuda":
+        if self.device.type != "cuda":
+            raise LograError(1, where + ": tensors on one GPU expected")
+        # logra_grad_tensor is five 64-bit words: data, rows, cols, ld, dtype
+        words, index = [], self.device.index
+        for t in self.tensors:
+            if t.get_device() != index:
                 raise LograError(1, where + ": tensors on one GPU expected")
-            items[i] = _GradTensor(t.data_ptr(), *self._rows_of(t), _dtype_code(t), 0)
+            rows, cols, ld = self._rows_of(t)
+            words += (t.data_ptr(), rows, cols, ld, _dtype_code(t))
+        items = (ctypes.c_int64 * max(1, len(words)))(*words)
         lib = load_library()
         host = torch.empty(max(8, int(lib.logra_grad_table_bytes(len(self.tensors)))), dtype=torch.uint8)
         self.desc = _GradListDesc()
-        _check(lib.logra_grad_list_pack(len(self.tensors), items, _ptr(host), _nbytes(host),
-                                        ctypes.byref(self.desc)), "logra_grad_list_pack")
+        _check(lib.logra_grad_list_pack(len(self.tensors), ctypes.cast(items, ctypes.POINTER(_GradTensor)), _ptr(host),
+                                        _nbytes(host), ctypes.byref(self.desc)), "logra_grad_list_pack")
         self.table = host.to(self.device)
         self.desc.table = self.table.data_ptr()
         self.ref = ctypes.byref(self.desc)
@@ -615,7 +620,7 @@ class GradList:
     @staticmethod
     def _rows_of(t):
         if t.is_contiguous():
-            cols = t.shape[-1] if t.dim() else 1
+            cols = t.size(-1) if t.dim() else 1
             return (t.numel() // cols if cols else 0), cols, cols
         if t.dim() == 2 and (t.stride(1) == 1 or t.size(1) == 1):
             return t.size(0), t.size(1), t.stride(0)

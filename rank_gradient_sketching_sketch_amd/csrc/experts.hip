@@ -16,7 +16,9 @@
 // All of them are bound by memory. The row kernels give each token a
 // workgroup, so that a token's own row crosses the memory bus once however
 // many experts it goes to. Rows of Xs and dYs that no pair maps to are not
-// written.
+// written. 4096 tokens, 8 of 128 experts, bf16 rows of 2048: gather 30 us
+// (147 MB, 4.8 TB/s), combine 33 us (151 MB, 4.6 TB/s), combine backward 59 us
+// (277 MB, 4.7 TB/s); a copy of 1 GiB reaches 5.2 TB/s on this card.
 #include <type_traits>
 
 #include "common.hpp"
@@ -28,7 +30,9 @@ namespace logra {
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 // Up to kSortSelf pairs the sort is one launch: every workgroup counts all
 // pairs itself and places its own kSortChunk of them. Above that a launch of
-// counts goes first, whose sums the workgroups then add up.
+// counts goes first, whose sums the workgroups then add up. (128 experts: 4096
+// pairs 6.1 us in one launch, 7.3 us and a launch more in two; 32768 pairs
+// 17.5 us in one, 10 us in two.)
 constexpr int kSortSelf = 4096, kSortChunk = 1024;
 constexpr int kSortMaxBlocks = 256;
 

@@ -17,6 +17,16 @@
 // partials themselves (at most kGradMaxWGs doubles, from the L2), so no
 // workgroup waits for another and no counter has to be reset. Few elements are
 // done by one workgroup in one launch.
+//
+// Bound by memory: the gradients are read twice (the factor is known only
+// when all have been read once) and written once. 196 fp32 sketches of 1.42 GB
+// in all, scaled into other tensors: 214 us for the sum (6.6 TB/s) and 532 us
+// for the scaling (5.4 TB/s); a copy of 1 GiB reaches 5.2 TB/s on this card.
+// What it took from a first version's 323 + 603 us: runs over whole tensors
+// instead of chunks with a table look-up each (223 + 579), then streaming
+// loads and stores and four times the workgroups for the scaling. Reading
+// the second time from the back, to meet what the last-level cache kept,
+// changed nothing.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -24,9 +34,11 @@ namespace logra {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradSmallThreads = 1024;
-constexpr int64_t kGradSmallChunks = 32;      // chunks (of one or several tensors) that one workgroup takes alone
-constexpr int64_t kGradSmallElements = 32768;
-// Elements above which the reads are marked as not to be kept in the caches.
+// What one workgroup takes alone, in one launch: nine tensors of 1536 elements
+// take it 5.0 us, two launches of the others 9.1 us.
+constexpr int64_t kGradSmallChunks = 32, kGradSmallElements = 32768;
+// Elements above which loads and stores are marked as not to be kept in the
+// caches (fp32: the last-level cache's 256 MB).
 constexpr int64_t kGradStream = 1ll << 26;
 
 // Tensors need only their element's alignment (global memory takes 16-byte
