@@ -144,9 +144,9 @@ __device__ __forceinline__ int es_items(int count, int chunk) { return count > c
 
 __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, int N, int chunk, int max_items,
                                                EsItem *__restrict__ items, EsParts *__restrict__ experts, int *lds) {
+    // lds: kMaxExperts sums of blocks and of partial sketches, a counter per class and their total
     int *sum_b = lds, *sum_x = lds + kMaxExperts, *slot = lds + 2 * kMaxExperts;
     const int tid = threadIdx.x, lane = tid & 63, n_threads = blockDim.x;
-    for (int i = tid; i < max_items; i += n_threads) items[i].expert = -1;
     if (tid < kEsClasses) slot[tid] = 0;
     for (int e = tid; e < E; e += n_threads) {
         const int count = es_range(offsets, e, N).count;
@@ -194,8 +194,10 @@ __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, in
             slot[c] = at;
             at += n;
         }
+        slot[kEsClasses] = at;
     }
     __syncthreads();
+    for (int i = slot[kEsClasses] + tid; i < max_items; i += n_threads) items[i].expert = -1;
     for (int e = tid; e < E; e += n_threads) {
         const EsRange r = es_range(offsets, e, N);
         const int n = es_items(r.count, chunk);
@@ -338,8 +340,8 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
 // 32x32x16 matrix instructions. Each of the eight waves holds all 64 rows of
 // 64 columns; they split the columns and k, and the k parts are added through
 // LDS in order. X goes through LDS in steps of 64 columns of k per part, two
-// buffers, requested two steps ahead; each lane hashes the one sign word of
-// its column and step, a step ahead. Row blocks without rows are skipped.
+// buffers, requested a step ahead; each lane hashes the one sign word of its
+// column and step, a step ahead. Row blocks without rows are skipped.
 constexpr int kEsWideRows = 64;
 constexpr int kEsXRow = 72;            // bf16 per LDS row of 64 (16 bytes of padding against bank conflicts)
 constexpr int kEsTileLd = kEsWideRows + 4;
@@ -432,10 +434,10 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
     // the loop over k with M row blocks
     auto run = [&](auto m_blocks) {
         constexpr int M = decltype(m_blocks)::value;
-        u32x4_t x0[WK];
-        xload(0, x0);
+        u32x4_t x[WK];
+        xload(0, x);
         uint64_t word = word_at(0);
-        auto step = [&](int i, u32x4_t (&x)[WK]) {
+        auto step = [&](int i) {
             uint16_t *buf = xs + (i & 1) * Sh::X_BUF;
 #pragma unroll
             for (int p = 0; p < WK; ++p)
@@ -463,14 +465,13 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
                 }
             }
         };
-        for (int i = 0; i < steps; ++i) step(i, x0);
+        for (int i = 0; i < steps; ++i) step(i);
     };
     if (blocks == 1) run(std::integral_constant<int, 1>());
     else run(std::integral_constant<int, 2>());
-    // The k parts are added in order. Each of a wave's row blocks of 32 is
-    // brought together by one of the WK waves that hold a part of it: lane
-    // (i32, h) of block (mb, nb) holds rows 32 mb + 8 q + 4 h .. +3 of column
-    // i32, q = 0 .. 3.
+    // The k parts are added in order, each 32 x 32 block (mb, nb) by one of the
+    // WK waves that hold a part of it: lane (i32, h) holds rows
+    // 32 mb + 8 q + 4 h .. +3 of its column i32, q = 0 .. 3.
     float *tile = reinterpret_cast<float *>(smem);
     auto at_tile = [&](int part, int mb, int nb, int q) {
         return reinterpret_cast<f32x4_t *>(
