@@ -6,8 +6,8 @@
 // The gradients of a step are many tensors (one sketch per projection,
 // plus the dense gradients of what is not sketched), so the kernels walk a
 // device table of them, cut into chunks of at most kGradChunk elements; each
-// workgroup takes a contiguous range of chunks, finds its first one by
-// bisection and steps through the table from there, reading what lies in one
+// workgroup takes a contiguous range of chunks, finds the first one's tensor
+// and steps through the table from there, reading what lies in one
 // tensor without gaps as one run.
 //
 // Sums are taken in fp64 (squares of fp32 values neither overflow nor vanish
@@ -297,15 +297,19 @@ __device__ __forceinline__ void grad_chunk_scale(GradGroup g, GradChunk k, GradC
         });
 }
 
-// The entry that holds chunk c (entries without elements hold none).
+// The entry that holds chunk c (entries without elements hold none), found by
+// whole waves: each lane looks at the last of one of 64 parts of the range.
 __device__ __forceinline__ int grad_find(const GradEntry *t, int n, int64_t c) {
-    int lo = 0, hi = n;                  // first entry whose chunks end behind c
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (t[mid].first + t[mid].chunks <= c) lo = mid + 1;
-        else hi = mid;
+    const int lane = threadIdx.x & 63;
+    int lo = 0;
+    while (n > 1) {                      // the entry is among n from lo
+        const int part = (n + 63) / 64, i = min((lane + 1) * part, n) - 1;
+        const uint64_t past = __ballot(t[lo + i].first + t[lo + i].chunks > c);
+        const int at = __builtin_ctzll(past) * part;
+        lo += at;
+        n = min(part, n - at);
     }
-    return lo;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // Sum over the workgroup by a fixed tree; every thread gets it.
