@@ -575,7 +575,7 @@ def _rows(where, t, h=None, dtype=None):
                 raise LograError(1, "%s: rows of %d elements expected" % (where, h))
             if dtype is not None and t.dtype is not dtype:
                 raise LograError(1, where + ": one dtype for all rows expected")
-            return n, cols, ld if n > 1 else max(ld, cols)
+            return n, cols, ld if n > 1 else cols      # one row: its stride has no meaning
     raise LograError(1, where + ": 2-D tensor with unit column stride expected")
 
 
@@ -583,7 +583,8 @@ class GradList:
     """The gradients of a step, described to the library once: logra_grad_norm
     and logra_grad_clip read them through a device table that holds their
     addresses. The list keeps the tensors; they must stay where they are
-    (gradients written in place every step, as Step's sketches are).
+    (gradients written in place every step, as Step's sketches are). Making
+    one copies the table to the GPU, so make it before a graph capture.
 
     tensors  float32 or bfloat16, on one GPU, contiguous of any shape or 2-D
              with unit column stride and a longer row stride; none may overlap

@@ -216,7 +216,7 @@ class Step:
                                 + self.expert_ws_bytes)
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.coef = torch.ones(1, dtype=torch.float32, device=dev)
-        self._grad_list, self._grad_ws = None, None
+        self._list_gradients()      # copies a table to the device, which a captured `clip` could not
 
     # ---- streams ---------------------------------------------------------
     def _fork(self):
@@ -292,15 +292,21 @@ class Step:
         self._join()
         return events
 
+    def _gradients(self):
+        return [m.S for m in self.dense] + [g.S for g in self.groups] + self.grads
+
+    def _list_gradients(self):
+        self._grad_list = B.GradList(self._gradients())
+        self._grad_ws = torch.empty(self._grad_list.workspace_bytes, dtype=torch.uint8, device=self.device)
+
     def clip(self, max_norm: float):
         """Clip the step's gradients by their global norm: every S (which
         holds the whole step after `sketch`) and the dense gradients given to
         Step, in place, before pass 1. Returns the device tensors (norm, coef)
         without waiting for them; a norm that is not finite clips nothing."""
-        if self._grad_list is None:
-            sketches = [m.S for m in self.dense] + [g.S for g in self.groups]
-            self._grad_list = B.GradList(sketches + self.grads)
-            self._grad_ws = torch.empty(self._grad_list.workspace_bytes, dtype=torch.uint8, device=self.device)
+        listed, now = self._grad_list.tensors, self._gradients()
+        if len(listed) != len(now) or any(a is not b for a, b in zip(listed, now)):
+            self._list_gradients()      # a sketch or gradient was replaced since
         B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)
         return self.norm, self.coef
 

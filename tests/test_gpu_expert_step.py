@@ -142,3 +142,36 @@ def test_step_refuses_what_does_not_fit():
     offsets, order = torch.zeros(E + 1, dtype=torch.int32, device=dev), torch.zeros(T * K - 1, dtype=torch.int32, device=dev)
     with pytest.raises(ValueError):
         st.sketch(0, 1, expert_inputs=lambda i, mb: (X, dY, offsets, order))
+
+
+def test_clip_captured_at_once_and_with_a_replaced_gradient():
+    """The first clip of a step may be a captured one, and a gradient that the
+    caller puts in another's place is the one clipped from then on."""
+    dev = device()
+    side = torch.cuda.Stream(device=dev)
+    g = torch.Generator().manual_seed(31)
+    mat = Matrix(40, H, 7, torch.zeros(40, H, device=dev), torch.zeros(40, device=dev))
+    first, second = torch.zeros(H + 1, device=dev), torch.randn(2 * H, generator=g).to(dev)
+    with torch.cuda.stream(side):
+        st = Step([mat], R, T, B.LOGRA_BF16, grads=[first])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        norm, coef = st.clip(0.5)
+    for scale in (1.0, 1e-4, 3.0):
+        S, d = torch.randn(40, R, generator=g) * scale, torch.randn(H + 1, generator=g) * scale
+        mat.S.copy_(S)
+        first.copy_(d)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        n_ref, c_ref, out = ox.clip([to_f64(S), to_f64(d)], 0.5)
+        assert abs(norm.item() - n_ref) <= 2.0 ** -23 * n_ref and abs(coef.item() - c_ref) <= 2.0 ** -22 * c_ref
+        for got, want in zip((mat.S, first), out):
+            assert np.all(np.abs(to_f64(got) - want) <= 2.0 ** -22 * np.abs(want))
+    kept, st.grads[0] = first.clone(), second
+    n_ref, c_ref, out = ox.clip([to_f64(mat.S), to_f64(second)], 0.5)
+    norm, coef = st.clip(0.5)
+    torch.cuda.synchronize()
+    assert abs(norm.item() - n_ref) <= 2.0 ** -23 * n_ref and torch.equal(first, kept)
+    for got, want in zip((mat.S, second), out):
+        assert np.all(np.abs(to_f64(got) - want) <= 2.0 ** -22 * np.abs(want))

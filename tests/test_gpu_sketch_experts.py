@@ -250,3 +250,16 @@ def test_repeats_graph_and_side_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(S, ref)
+
+
+def test_one_row_of_any_stride():
+    """The row stride of a single row has no meaning: none is refused."""
+    dev = device()
+    offsets, order, X, dY = _inputs(12, 1, 1, 3, 40, 64, torch.bfloat16, dev)
+    m = L.MatrixDesc(40, 64, 32, seed=1, step=0, matrix_id=0)
+    want, got = torch.empty(3, 40, 32, device=dev), torch.empty(3, 40, 32, device=dev)
+    L.logra_sketch_experts(m, offsets, X, dY, want, False, order=order, topk=1)
+    for ld in (1, 67, 1 << 25):
+        L.logra_sketch_experts(m, offsets, X.as_strided((1, 64), (ld, 1)), dY.as_strided((1, 40), (ld, 1)), got, False,
+                               order=order, topk=1)
+        assert torch.equal(want, got)
