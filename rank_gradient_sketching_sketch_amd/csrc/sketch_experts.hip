@@ -228,17 +228,18 @@ __device__ __forceinline__ int64_t es_x_row(const ExpertSketchArgs &a, int i) {
 }
 
 // ---------------------------------------------------------- bf16, stage 1 --
-// A workgroup owns one 32-row block of P and 128 (or r) columns over the
+// A workgroup owns one 32-row block of P and RT of its columns over the
 // whole of k; its eight waves split the k range and add their tiles through
 // LDS in wave order, as stage 1 of the one-matrix sketch does.
 constexpr int kEsWaves = 8, kEsWords = 8;
+constexpr int kEsAhead = 3;         // sign words' columns of X in flight
 
-template <int R>
+template <int RT>
 __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int chunk, int K, int64_t p_blocks,
                                                          int max_items,
                                                          EsItem *__restrict__ items, EsParts *__restrict__ experts,
                                                          float *__restrict__ P) {
-    constexpr int RT = R < 128 ? R : 128, NB = RT / 16, MB = 2;
+    constexpr int NB = RT / 16, MB = 2;
     constexpr int kTileLd = kEsTokens + 4;
     constexpr int kTable = kEsWaves * kEsWords * RT * 8, kTiles = kEsWaves * RT * kTileLd * 4;
     __shared__ __attribute__((aligned(16))) char smem[kTable > kTiles ? kTable : kTiles];
@@ -247,33 +248,42 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i16 = lane & 15, g = lane >> 4;
-    const int l0 = blockIdx.y * RT;
-    if (blockIdx.x == 0) {
-        if (blockIdx.y == 0)
+    // workgroup ids are dealt round-robin over the XCDs: the column tiles of a
+    // block go to one XCD, whose L2 then holds its rows of X
+    const int j = blockIdx.x / kXcds, tiles = a.R / RT;
+    const int number = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), l0 = j % tiles * RT;
+    if (number == 0) {
+        if (l0 == 0)
             es_build_items(a.offsets, a.E, static_cast<int>(a.N), chunk, max_items, items, experts,
                            reinterpret_cast<int *>(smem));
         return;
     }
-    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x - 1, kEsTokens);
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number - 1, kEsTokens);
     if (at.expert < 0) return;
     const EsRange rows = at.rows;
     const int n = min(kEsTokens, rows.count - at.index * kEsTokens);       // rows of this block
     const uint64_t key = es_key(a, at.expert);
 
-    const uint16_t *xrow[MB];
+    const __amdgpu_buffer_rsrc_t xv = es_view(a.X, static_cast<uint32_t>(a.x_rows * a.ldx * 2));
+    uint32_t xoff[MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
         const int i = 16 * mb + i16;
         const int64_t r = i < n ? es_x_row(a, rows.begin + at.index * kEsTokens + i) : -1;
-        xrow[mb] = r < 0 ? nullptr : static_cast<const uint16_t *>(a.X) + r * a.ldx;
+        xoff[mb] = r < 0 ? kEsOob : static_cast<uint32_t>((r * a.ldx + 8 * g) * 2);
     }
     const int nkb = (K + 63) >> 6;
     const int bpw = (nkb + kEsWaves - 1) / kEsWaves;
     const int kb0 = min(nkb, wave * bpw), kb1 = min(nkb, kb0 + bpw);
-    const int s_begin = 2 * kb0, s_end = min((K + 31) >> 5, 2 * kb1);
-    auto xload = [&](int s, int mb) -> u32x4_t {
-        const int k = 32 * s + 8 * g;
-        return xrow[mb] && s < s_end && k < K ? load_u32x4(xrow[mb] + k) : zero_u32x4();
+    // the columns of sign word b, 32 each half
+    auto xload = [&](int b, u32x4_t (&x)[2][MB]) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const int k = 64 * b + 32 * half;
+                x[half][mb] = es_load(xv, (xoff[mb] + 2u * k) | (b < kb1 && k + 8 * g < K ? 0u : kEsOob));
+            }
     };
     uint64_t *wt = table + wave * (kEsWords * RT);
     auto refill = [&](int first) {
@@ -292,30 +302,35 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = zero_f32x4();
     const uint32_t one_pair = opaque_u32(0x3F803F80u);
-    u32x4_t xa[MB], xn[MB];
+    u32x4_t x[kEsAhead][2][MB];
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) xa[mb] = xload(s_begin, mb);
+    for (int q = 0; q < kEsAhead; ++q) xload(kb0 + q, x[q]);
     int first = kb0;
-    if (s_begin < s_end) refill(first);
-    for (int s = s_begin; s < s_end; ++s) {
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) xn[mb] = xload(s + 1, mb);
-        const int b = s >> 1;
+    if (kb0 < kb1) refill(first);
+    auto word_step = [&](int b, u32x4_t (&xb)[2][MB]) {
         if (b >= first + kEsWords) {
             first += kEsWords;
             refill(first);
         }
         const uint64_t *wrow = wt + (b - first) * RT + i16;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const uint64_t w = wrow[16 * nb];
-            const uint32_t dw = (s & 1) ? static_cast<uint32_t>(w >> 32) : static_cast<uint32_t>(w);
-            const u32x4_t bf = signs8_to_bf16(__builtin_amdgcn_ubfe(dw, 8 * g, 8), one_pair);
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) acc[mb][nb] = mfma_bf16(xa[mb], bf, acc[mb][nb]);
+            for (int nb = 0; nb < NB; ++nb) {
+                const uint64_t w = wrow[16 * nb];
+                const uint32_t dw = half ? static_cast<uint32_t>(w >> 32) : static_cast<uint32_t>(w);
+                const u32x4_t bf = signs8_to_bf16(__builtin_amdgcn_ubfe(dw, 8 * g, 8), one_pair);
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) acc[mb][nb] = mfma_bf16(xb[half][mb], bf, acc[mb][nb]);
+            }
         }
+    };
+    for (int b0 = kb0; b0 < kb1; b0 += kEsAhead) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) xa[mb] = xn[mb];
+        for (int q = 0; q < kEsAhead; ++q) {
+            if (b0 + q < kb1) word_step(b0 + q, x[q]);
+            xload(b0 + q + kEsAhead, x[q]);
+        }
     }
     __syncthreads();      // every wave is done with its word table
 #pragma unroll
@@ -331,7 +346,7 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
         f32x4_t v = zero_f32x4();
 #pragma unroll
         for (int w = 0; w < kEsWaves; ++w) v += *reinterpret_cast<const f32x4_t *>(&tile[(w * RT + col) * kTileLd + t]);
-        *reinterpret_cast<f32x4_t *>(P + (block * R + l0 + col) * kEsTokens + t) = a.c * v;
+        *reinterpret_cast<f32x4_t *>(P + (block * a.R + l0 + col) * kEsTokens + t) = a.c * v;
     }
 }
 
@@ -731,17 +746,20 @@ __device__ __forceinline__ void es_f32_join(f32x4_t (&acc)[MT][NT], float *lds, 
     }
 }
 
+template <int T>
 __global__ __launch_bounds__(64 * kEsF32Waves) void es_project_f32_kernel(ExpertSketchArgs a, int K,
                                                                           float *__restrict__ P) {
-    constexpr int MT = kEsTokens / 16, NT = 2;
+    constexpr int MT = T, NT = T, kRows = 16 * T;
     __shared__ __attribute__((aligned(16))) float lds[kEsF32Waves * 16 * NT * (16 * MT + 4)];
     const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x, kEsTokens);
+    // the column tiles of a block of rows go to one XCD, as in the bf16 kernel
+    const int j = blockIdx.x / kXcds, tiles = (a.R + 16 * NT - 1) / (16 * NT);
+    const int number = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), l0 = j % tiles * 16 * NT;
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number, kRows);
     if (at.expert < 0) return;
     const EsRange rows = at.rows;
-    const int i0 = rows.begin + at.index * kEsTokens, n = min(kEsTokens, rows.count - at.index * kEsTokens);
-    const int l0 = blockIdx.y * 16 * NT;
+    const int i0 = rows.begin + at.index * kRows, n = min(kRows, rows.count - at.index * kRows);
     const uint64_t key = es_key(a, at.expert);
     const float *xrow[MT];
 #pragma unroll
@@ -840,12 +858,24 @@ __global__ __launch_bounds__(64 * kEsF32Waves) void es_fold_f32_kernel(ExpertSke
 
 // ------------------------------------------------------------------ plans --
 constexpr int64_t kEsF32WideFrom = 256;
+// The fp32 projection's tiles are 32 x 32, and 16 x 16 where that would make no
+// more than kEsF32SmallWGs workgroups (8 experts: 768 rows, k = 512, r = 32 5.1 us
+// against 7.8 with 32 x 32, r = 256 8.2 against 8.5; 2048 rows, k = 2048, r = 256
+// 38 against 31).
+constexpr int64_t kEsF32SmallWGs = 256;
 constexpr int64_t kEsMaxChunk = 1 << 20;   // an item's part of P stays within a view (r <= 256)
 // The wide projection is used from kEsWideFrom rows or where the other one
 // would take more than kEsWideWGs workgroups (whole call, k = 2048, r = 256:
 // 8 experts, 2048 rows 35 us against 41 wide, 4096 rows 61 against 56; 128
 // experts, 1024 rows 40 against 40, 2048 rows 49 against 44).
 constexpr int64_t kEsWideFrom = 4096, kEsWideWGs = 320;
+
+// The other projection takes 128 columns, or all r, per workgroup; 64 or 32
+// where it would have no more than kEsNarrowWGs workgroups (8 experts, k =
+// 2048, r = 256: 512 rows 9.1 us with 32 columns, 10.7 with 64, 12.6 with 128;
+// 2048 rows 15.2, 11.8, 14.1; 16 experts, 128 rows, k = 1536, r = 64: 6.7 with
+// 32 columns, 8.0 with 64).
+constexpr int64_t kEsNarrowWGs = 160;
 
 ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int R, int bf16) {
     ExpertSketchPlan p;
@@ -893,9 +923,13 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
                                n_items, items, experts, P);
         }
     }
-    if (!done)
-        hipLaunchKernelGGL(es_project_kernel<R>, dim3(p.p_blocks + 1, R < 128 ? 1 : R / 128), dim3(512), 0, st, a,
-                           p.chunk, K, p.p_blocks, n_items, items, experts, P);
+    if (!done) {
+        int rt = R < 128 ? R : 128;
+        while (rt > 32 && p.p_blocks * (R / rt) <= kEsNarrowWGs) rt /= 2;
+        hipLaunchKernelGGL(rt == 32 ? es_project_kernel<32> : rt == 64 ? es_project_kernel<64> : es_project_kernel<128>,
+                           dim3((p.p_blocks / kXcds + 1) * kXcds * (R / rt)), dim3(512), 0, st, a, p.chunk, K, p.p_blocks, n_items, items,
+                           experts, P);
+    }
     const int tiles = (D + kEsRows - 1) / kEsRows;
     hipLaunchKernelGGL(es_fold_kernel<R>, dim3((p.items + kXcds - 1) / kXcds * kXcds * tiles), dim3(256), 0, st, a, D,
                        tiles, n_items, p.p_blocks, p.extras, items, P, parts);
@@ -913,9 +947,13 @@ hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t
         const ExpertSketchPlan p = plan_expert_sketch(a.N, a.E, a.d, a.k, a.R, 0);
         float *P = static_cast<float *>(a.ws);
         const int D = static_cast<int>(a.d), K = static_cast<int>(a.k);
-        if (p.p_blocks > 0)
-            hipLaunchKernelGGL(es_project_f32_kernel, dim3(p.p_blocks, (a.R + 31) / 32), dim3(64 * kEsF32Waves), 0, st,
-                               a, K, P);
+        if (p.p_blocks > 0) {
+            const int T = p.p_blocks * ((a.R + 31) / 32) <= kEsF32SmallWGs ? 1 : 2;
+            const int64_t units = a.N / (16 * T) + (a.N < a.E ? a.N : a.E);
+            hipLaunchKernelGGL(T == 1 ? es_project_f32_kernel<1> : es_project_f32_kernel<2>,
+                               dim3((units + kXcds - 1) / kXcds * kXcds * ((a.R + 16 * T - 1) / (16 * T))),
+                               dim3(64 * kEsF32Waves), 0, st, a, K, P);
+        }
         // tiles of 64 x 64 where they still give each compute unit one, which
         // reads a quarter of what tiles of 32 x 32 read per product
         const bool wide = static_cast<int64_t>((a.R + 63) / 64) * ((D + 63) / 64) * a.E >= kEsF32WideFrom;

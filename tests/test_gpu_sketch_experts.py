@@ -66,6 +66,9 @@ CASES = [
     (1200, 4, 70, 40, 2056, 256, 3, 0),
     (4100, 1, 3, 64, 72, 128, None, 16),
     (600, 8, 130, 64, 128, 256, None, 0),
+    # 64 columns per workgroup of the other projection, of 256 and of 64
+    (900, 2, 4, 72, 712, 256, 2, 8),
+    (3001, 2, 6, 64, 72, 64, None, 0),
 ]
 
 
