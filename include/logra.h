@@ -704,8 +704,9 @@ logra_status logra_grad_list_pack(int64_t n, const logra_grad_tensor *tensors, v
  *   In place nothing is written where coef is 1. max_norm >= 0 (infinity:
  *   only the norm, and copies). The tensors of out must not overlap those of
  *   the list.
- *   ws: device, 16-byte aligned, >= logra_grad_workspace_bytes(list) bytes;
- *   scratch, one for every call in flight.
+ *   ws: device, 16-byte aligned, >= logra_grad_workspace_bytes(list) bytes
+ *   (0 for few elements: ws is not used then); scratch, one for every call in
+ *   flight.
  * Errors: INVALID_ARGUMENT (nulls, table NULL or misaligned with n > 0,
  *   lists of different shapes, max_norm negative or NaN), WORKSPACE, HIP.
  */

@@ -9,6 +9,7 @@ unloadable library raises LograError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -503,27 +504,32 @@ def logra_ts_apply(m: MatrixDesc, ws: torch.Tensor, W: torch.Tensor, lr: float, 
 # short tensors), so the checks read each property of a tensor once and pass
 # plain integers.
 
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+@functools.lru_cache(maxsize=None)
+def _gpu(dev):
+    return torch.device("cuda", dev)
+
+
 def _enter(where, stream, tensors):
-    """(device index, raw stream) of one call: its tensors must all be on one
-    GPU; without a stream it runs on that GPU's current one."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or d != dev:
-                if d < 0 or dev >= 0:
-                    raise LograError(1, where + ": tensors on one GPU expected")
-                dev = d
+    """(device index, raw stream) of one call: its tensors (the first one not
+    None) must all be on one GPU; without a stream it runs on that GPU's current one."""
+    dev = tensors[0].get_device()
     if dev < 0:
-        raise LograError(1, where + ": a tensor on a GPU expected")
+        raise LograError(1, where + ": tensors on one GPU expected")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise LograError(1, where + ": tensors on one GPU expected")
     if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
+        return dev, _current_stream(dev)
     return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _call(where, dev, fn, *args):
     """The C call with its GPU current."""
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -539,7 +545,7 @@ def _workspace(where, dev, stream, handle, ws, nbytes):
     if ws is None:
         if nbytes == 0:
             return None, None, 0
-        device = torch.device("cuda", dev)
+        device = _gpu(dev)
         if stream is None:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
@@ -566,17 +572,18 @@ def _one_float(where, t):
 def _rows(where, t, h=None, dtype=None):
     """(rows, columns, row stride) of a 2-D tensor of rows (unit column
     stride), of h columns and of dtype if those are given."""
-    shape = t.shape
-    if len(shape) == 2:
-        n, cols = shape
-        ld, unit = t.stride()
-        if unit == 1 or cols <= 1 or n == 0:
-            if h is not None and cols != h:
-                raise LograError(1, "%s: rows of %d elements expected" % (where, h))
-            if dtype is not None and t.dtype is not dtype:
-                raise LograError(1, where + ": one dtype for all rows expected")
-            return n, cols, ld if n > 1 else cols      # one row: its stride has no meaning
-    raise LograError(1, where + ": 2-D tensor with unit column stride expected")
+    stride = t.stride()
+    if len(stride) != 2:
+        raise LograError(1, where + ": 2-D tensor with unit column stride expected")
+    n, cols = t.shape
+    ld, unit = stride
+    if unit != 1 and cols > 1 and n > 0:
+        raise LograError(1, where + ": 2-D tensor with unit column stride expected")
+    if h is not None and cols != h:
+        raise LograError(1, "%s: rows of %d elements expected" % (where, h))
+    if dtype is not None and t.dtype is not dtype:
+        raise LograError(1, where + ": one dtype for all rows expected")
+    return n, cols, ld if n > 1 else cols      # one row: its stride has no meaning
 
 
 class GradList:
@@ -655,6 +662,7 @@ def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: 
           norm.data_ptr(), coef.data_ptr(), p, nb, handle)
 
 
+@functools.lru_cache(maxsize=None)
 def logra_expert_sort_workspace_bytes(T: int, topk: int, n_experts: int) -> int:
     return int(load_library().logra_expert_sort_workspace_bytes(T, topk, n_experts))
 
@@ -683,8 +691,9 @@ def _slots_of(where, slots, weights, T):
     shape = slots.shape
     if len(shape) != 2 or shape[0] != T or slots.dtype is not torch.int32 or not slots.is_contiguous():
         raise LograError(1, "%s: contiguous int32 slots of %d tokens expected" % (where, T))
-    if weights is not None:
-        _want(where, weights, torch.float32, shape)
+    if weights is not None and (weights.shape != shape or weights.dtype is not torch.float32
+                                or not weights.is_contiguous()):
+        raise LograError(1, "%s: contiguous float32 weights of the slots' shape expected" % where)
     return shape[1]
 
 

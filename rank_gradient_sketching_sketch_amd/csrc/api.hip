@@ -650,6 +650,11 @@ bool grad_list_ok(const logra_grad_list *g) {
     return g && g->n >= 0 && g->chunks >= 0 && (g->n == 0 || (g->table && aligned16(g->table)));
 }
 
+bool grad_ws_ok(const logra_grad_list *g, const void *ws, size_t ws_bytes) {
+    const size_t need = logra_grad_workspace_bytes(g);
+    return need == 0 || (ws && ws_bytes >= need && aligned16(ws));
+}
+
 struct GradSpan {
     uint64_t begin, end;
     bool operator<(const GradSpan &o) const { return begin < o.begin; }
@@ -725,12 +730,12 @@ logra_status logra_grad_list_pack(int64_t n, const logra_grad_tensor *tensors, v
 }
 
 size_t logra_grad_workspace_bytes(const logra_grad_list *list) {
-    return list && list->chunks >= 0 ? static_cast<size_t>(grad_workgroups(list->chunks)) * sizeof(double) : 0;
+    return list && list->chunks >= 0 ? grad_workspace(list->n, list->chunks, list->elements) : 0;
 }
 
 logra_status logra_grad_norm(const logra_grad_list *list, float *norm, void *ws, size_t ws_bytes, void *stream) {
     if (!grad_list_ok(list) || !norm || !aligned_to(norm, 4)) return LOGRA_ERR_INVALID_ARGUMENT;
-    if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
+    if (!grad_ws_ok(list, ws, ws_bytes)) return LOGRA_ERR_WORKSPACE;
     return from_hip(launch_grad_norm(static_cast<const GradEntry *>(list->table), list->n, list->chunks,
                                      list->elements, static_cast<double *>(ws), norm, static_cast<hipStream_t>(stream)));
 }
@@ -742,7 +747,7 @@ logra_status logra_grad_clip(const logra_grad_list *list, const logra_grad_list 
     if (!out) out = list;
     if (!grad_list_ok(out) || out->n != list->n || out->chunks != list->chunks || out->shapes != list->shapes)
         return LOGRA_ERR_INVALID_ARGUMENT;
-    if (!ws || ws_bytes < logra_grad_workspace_bytes(list) || !aligned16(ws)) return LOGRA_ERR_WORKSPACE;
+    if (!grad_ws_ok(list, ws, ws_bytes)) return LOGRA_ERR_WORKSPACE;
     return from_hip(launch_grad_clip(static_cast<const GradEntry *>(list->table),
                                      static_cast<const GradEntry *>(out->table), list->n, list->chunks,
                                      list->elements, max_norm, static_cast<double *>(ws), norm, coef, static_cast<hipStream_t>(stream)));

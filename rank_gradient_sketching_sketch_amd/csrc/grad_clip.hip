@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kGradSmallThreads) void grad_small_kernel(const Gra
 }
 
 // As many chunks for every workgroup, but for the last ones.
-int grad_workgroups(int64_t chunks) {
+static int grad_workgroups(int64_t chunks) {
     if (chunks < 1) return 1;
     const int64_t each = (chunks + kGradMaxWGs - 1) / kGradMaxWGs;
     return static_cast<int>((chunks + each - 1) / each);
@@ -478,6 +478,10 @@ int grad_workgroups(int64_t chunks) {
 
 static bool grad_small(int n, int64_t chunks, int64_t elements) {
     return n <= 64 && chunks <= kGradSmallChunks && elements <= kGradSmallElements;
+}
+
+size_t grad_workspace(int n, int64_t chunks, int64_t elements) {
+    return grad_small(n, chunks, elements) ? 0 : static_cast<size_t>(grad_workgroups(chunks)) * sizeof(double);
 }
 
 hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, int64_t elements, double *partials,

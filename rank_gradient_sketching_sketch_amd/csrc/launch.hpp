@@ -218,7 +218,7 @@ struct GradEntry {
     int32_t rows_per_chunk = 0, segs_per_row = 0, seg_len = 0;
     int32_t bf16 = 0;
 };
-int grad_workgroups(int64_t chunks);
+size_t grad_workspace(int n, int64_t chunks, int64_t elements);
 hipError_t launch_grad_norm(const GradEntry *t, int n, int64_t chunks, int64_t elements, double *partials,
                             float *norm, hipStream_t st);
 hipError_t launch_grad_clip(const GradEntry *t, const GradEntry *to, int n, int64_t chunks, int64_t elements,

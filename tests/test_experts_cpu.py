@@ -134,6 +134,10 @@ def test_clip_refusals(B):
     assert lib.logra_grad_norm(r(d), FAKE2, FAKE, 0, None) == WS
     assert lib.logra_grad_norm(None, FAKE2, FAKE, need, None) == BAD
     assert lib.logra_grad_workspace_bytes(None) == 0
+    # few elements in few tensors are done by one workgroup, without a workspace
+    for shapes, few in (([(1, 32768)], True), ([(1, 32769)], False), ([(1, 8)] * 32, True), ([(1, 8)] * 33, False)):
+        _, s, _ = _pack(B, [(0x100000 * (i + 1), n, c, c, 0) for i, (n, c) in enumerate(shapes)])
+        assert (lib.logra_grad_workspace_bytes(r(s)) == 0) == few
 
 
 def test_expert_refusals(B):
