@@ -81,11 +81,12 @@ struct EsUnit {
     int expert;             // -1: there are fewer units
     int index;              // the unit's number within its expert
     int blocks;             // 32-row blocks of P of the experts before
+    int part;               // of a short unit: which of the `split` parts of its columns
     EsRange rows;           // the expert's sorted rows
 };
-__device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, int u, int unit_rows) {
+__device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, int u, int unit_rows, int split) {
     const int lane = threadIdx.x & 63;
-    EsUnit p{-1, 0, 0, {0, 0}};
+    EsUnit p{-1, 0, 0, 0, {0, 0}};
     int before = 0;
     for (int pass = 0; pass < 2 && p.expert < 0; ++pass) {
         int blocks = 0;
@@ -93,7 +94,7 @@ __device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, 
             const EsRange r = e0 + lane < E ? es_range(offsets, e0 + lane, N) : EsRange{0, 0};
             const int count = r.count;
             const int nb = (count + kEsTokens - 1) / kEsTokens, full = count / unit_rows;
-            const int nu = pass == 0 ? full : count % unit_rows ? 1 : 0;
+            const int nu = pass == 0 ? full : count % unit_rows ? split : 0;
             int iu = nu, ib = nb;            // inclusive sums over the lanes
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -107,8 +108,9 @@ __device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, 
             if (past) {
                 const int l = __builtin_ctzll(past);
                 p.expert = e0 + l;
-                p.index = pass == 0 ? u - before - __builtin_amdgcn_readlane(iu - nu, l)
-                                    : __builtin_amdgcn_readlane(full, l);
+                const int q = u - before - __builtin_amdgcn_readlane(iu - nu, l);
+                p.index = pass == 0 ? q : __builtin_amdgcn_readlane(full, l);
+                p.part = pass == 0 ? -1 : q;
                 p.blocks = blocks + __builtin_amdgcn_readlane(ib - nb, l);
                 p.rows = EsRange{__builtin_amdgcn_readlane(r.begin, l), __builtin_amdgcn_readlane(count, l)};
                 break;
@@ -119,7 +121,7 @@ __device__ __forceinline__ EsUnit es_unit(const int32_t *offsets, int E, int N, 
     }
     // the same in all lanes: kept in scalar registers
     return EsUnit{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.index),
-                  __builtin_amdgcn_readfirstlane(p.blocks),
+                  __builtin_amdgcn_readfirstlane(p.blocks), __builtin_amdgcn_readfirstlane(p.part),
                   {__builtin_amdgcn_readfirstlane(p.rows.begin), __builtin_amdgcn_readfirstlane(p.rows.count)}};
 }
 
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
                            reinterpret_cast<int *>(smem));
         return;
     }
-    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number - 1, kEsTokens);
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number - 1, kEsTokens, 1);
     if (at.expert < 0) return;
     const EsRange rows = at.rows;
     const int n = min(kEsTokens, rows.count - at.index * kEsTokens);       // rows of this block
@@ -352,9 +354,9 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
 
 // The same product for calls with many rows and r >= 128: up to 64 rows of
 // one expert and all r columns per workgroup, so that X is read once, on
-// 32x32x16 matrix instructions. Each of the eight waves holds all 64 rows of
-// 64 columns; they split the columns and k, and the k parts are added through
-// LDS in order. X goes through LDS in steps of 64 columns of k per part, two
+// 32x32x16 matrix instructions (short units may take half the columns, NB =
+// 1). Each of the eight waves holds all 64 rows of 32 NB columns; they split
+// the columns and k, and the k parts are added through LDS in order. X goes through LDS in steps of 64 columns of k per part, two
 // buffers, requested a step ahead; each lane hashes the one sign word of its
 // column and step, a step ahead. Row blocks without rows are skipped.
 constexpr int kEsWideRows = 64;
@@ -394,33 +396,22 @@ __device__ __forceinline__ u32x4_t es_signs(uint64_t word, uint32_t sel, uint32_
     return r;
 }
 
-template <int R>
-__global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(ExpertSketchArgs a, int chunk, int K,
-                                                                 int64_t p_blocks, int max_items,
-                                                                 EsItem *__restrict__ items,
-                                                                 EsParts *__restrict__ experts,
-                                                                 float *__restrict__ P) {
+template <int R, int NB>
+__device__ __forceinline__ void es_project_unit(const ExpertSketchArgs &a, const EsUnit &at, int col0, int K,
+                                                int64_t p_blocks, float *__restrict__ P, char *smem,
+                                                uint64_t (*words)[64]) {
     using Sh = EsWide<R>;
-    constexpr int WN = Sh::WN, WK = Sh::WK, MB = kEsWideRows / 32, NB = 2;
-    __shared__ __attribute__((aligned(16))) char smem[Sh::LDS_BYTES];
-    __shared__ uint64_t words[8][64];
+    constexpr int WN = Sh::WN, WK = Sh::WK, MB = kEsWideRows / 32;
     uint16_t *xs = reinterpret_cast<uint16_t *>(smem);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % WN, wk = wave / WN;
     const int i32 = lane & 31, h = lane >> 5;
-    if (blockIdx.x == 0) {
-        es_build_items(a.offsets, a.E, static_cast<int>(a.N), chunk, max_items, items, experts,
-                       reinterpret_cast<int *>(smem));
-        return;
-    }
-    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x - 1, kEsWideRows);
-    if (at.expert < 0) return;
     const EsRange rows = at.rows;
     const int r0 = at.index * kEsWideRows;
     const int n = min(kEsWideRows, rows.count - r0);
     const int blocks = __builtin_amdgcn_readfirstlane((n + 31) >> 5);
-    const int l0 = 64 * wn;
+    const int l0 = col0 + 32 * NB * wn;
 
     // the row of X whose 16-byte pieces this thread moves
     const int xr = tid >> 3, xc = 8 * (tid & 7);
@@ -435,7 +426,7 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
         }
     };
     // columns of k past K are zeros in X, so their signs do not matter
-    const uint64_t first_word = es_key(a, at.expert) + ((static_cast<uint64_t>(l0 + lane) << 32) + 1ull) * kGolden;
+    const uint64_t first_word = es_key(a, at.expert) + ((static_cast<uint64_t>(l0 + lane % (32 * NB)) << 32) + 1ull) * kGolden;
     auto word_at = [&](int i) { return splitmix_finalize(first_word + static_cast<uint64_t>(WK * i + wk) * kGolden); };
     f32x16_t acc[MB][NB];
 #pragma unroll
@@ -490,19 +481,19 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
     float *tile = reinterpret_cast<float *>(smem);
     auto at_tile = [&](int part, int mb, int nb, int q) {
         return reinterpret_cast<f32x4_t *>(
-            &tile[(part * R + l0 + 32 * nb + i32) * kEsTileLd + 32 * mb + 8 * q + 4 * h]);
+            &tile[(part * R + 32 * NB * wn + 32 * nb + i32) * kEsTileLd + 32 * mb + 8 * q + 4 * h]);
     };
     auto piece = [&](int mb, int nb, int q) {
         return f32x4_t{acc[mb][nb][4 * q], acc[mb][nb][4 * q + 1], acc[mb][nb][4 * q + 2], acc[mb][nb][4 * q + 3]};
     };
-    // wave wk finishes the blocks (mb, nb) with (2 mb + nb) % WK == wk; of the
+    // wave wk finishes the blocks (mb, nb) with (NB mb + nb) % WK == wk; of the
     // others' parts, part p lies in slot (p - wk - 1) mod WK
     __syncthreads();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int owner = (2 * mb + nb) % WK;
+            const int owner = (NB * mb + nb) % WK;
             if (owner == wk) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) *at_tile((wk + WK - owner - 1) % WK, mb, nb, q) = piece(mb, nb, q);
@@ -514,7 +505,7 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
         if (mb >= blocks || block0 + mb >= p_blocks) break;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            if ((2 * mb + nb) % WK != wk) continue;
+            if ((NB * mb + nb) % WK != wk) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 f32x4_t v = zero_f32x4();
@@ -526,6 +517,25 @@ __global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(
             }
         }
     }
+}
+
+template <int R>
+__global__ __launch_bounds__(512, R == 256 ? 4 : 2) void es_project_wide_kernel(ExpertSketchArgs a, int chunk, int K,
+                                                                 int64_t p_blocks, int max_items, int split,
+                                                                 EsItem *__restrict__ items,
+                                                                 EsParts *__restrict__ experts,
+                                                                 float *__restrict__ P) {
+    __shared__ __attribute__((aligned(16))) char smem[EsWide<R>::LDS_BYTES];
+    __shared__ uint64_t words[8][64];
+    if (blockIdx.x == 0) {
+        es_build_items(a.offsets, a.E, static_cast<int>(a.N), chunk, max_items, items, experts,
+                       reinterpret_cast<int *>(smem));
+        return;
+    }
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), blockIdx.x - 1, kEsWideRows, split);
+    if (at.expert < 0) return;
+    if (at.part < 0 || split == 1) es_project_unit<R, 2>(a, at, 0, K, p_blocks, P, smem, words);
+    else es_project_unit<R, 1>(a, at, at.part * (R / 2), K, p_blocks, P, smem, words);
 }
 
 // ---------------------------------------------------------- bf16, stage 2 --
@@ -757,7 +767,7 @@ __global__ __launch_bounds__(64 * kEsF32Waves) void es_project_f32_kernel(Expert
     // the column tiles of a block of rows go to one XCD, as in the bf16 kernel
     const int j = blockIdx.x / kXcds, tiles = (a.R + 16 * NT - 1) / (16 * NT);
     const int number = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), l0 = j % tiles * 16 * NT;
-    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number, kRows);
+    const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number, kRows, 1);
     if (at.expert < 0) return;
     const EsRange rows = at.rows;
     const int i0 = rows.begin + at.index * kRows, n = min(kRows, rows.count - at.index * kRows);
@@ -878,6 +888,12 @@ constexpr int64_t kEsWideFrom = 4096, kEsWideWGs = 320;
 // 32 columns, 8.0 with 64).
 constexpr int64_t kEsNarrowWGs = 160;
 
+// Where the experts' last, shorter units are few, two workgroups take half the
+// columns of each: they fill what the long ones leave (k = 2048, r = 256, kernel
+// alone: 128 uneven experts, 32768 rows 48.7 us against 52.7, 4096 rows 15.8
+// against 18.6; 256 experts, 8192 rows 26.1 against 23.5; with r = 128, one
+// workgroup per compute unit, 128 experts, 33568 rows 42.3 against 40.8).
+constexpr int64_t kEsSplitShorts = 128;
 // From this many elements of S on (the 32 MB of all L2 caches) what the second
 // product finishes is written past them, so that P stays there: 67 -> 62.5 us
 // for the 100 MB of the call above.
@@ -924,9 +940,11 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
     if constexpr (R >= 128) {
         done = a.N >= kEsWideFrom || p.p_blocks * (R / 128) > kEsWideWGs;
         if (done) {
-            const int64_t units = a.N / kEsWideRows + (a.N < a.E ? a.N : a.E);      // at most
+            const int64_t shorts = a.N < a.E ? a.N : a.E;        // units of fewer rows, at most
+            const int split = R == 256 && shorts <= kEsSplitShorts ? 2 : 1;
+            const int64_t units = a.N / kEsWideRows + split * shorts;
             hipLaunchKernelGGL(es_project_wide_kernel<R>, dim3(units + 1), dim3(512), 0, st, a, p.chunk, K, p.p_blocks,
-                               n_items, items, experts, P);
+                               n_items, split, items, experts, P);
         }
     }
     if (!done) {
