@@ -137,8 +137,9 @@ struct EsItem {
     int part;               // partial sketch, -1 for S, -2 for S of an expert without partial ones
     int pad[3];
 };
-struct EsParts {
-    int first, count;       // an expert's partial sketches
+struct EsParts {            // the partial sketches of an expert that has some
+    int expert;
+    int first, count;       // count 0: there are fewer such experts
 };
 constexpr int kEsClasses = 16;
 
@@ -146,8 +147,9 @@ __device__ __forceinline__ int es_items(int count, int chunk) { return count > c
 
 __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, int N, int chunk, int max_items,
                                                EsItem *__restrict__ items, EsParts *__restrict__ experts, int *lds) {
-    // lds: kMaxExperts sums of blocks and of partial sketches, a counter per class and their total
-    int *sum_b = lds, *sum_x = lds + kMaxExperts, *slot = lds + 2 * kMaxExperts;
+    // lds: kMaxExperts sums of blocks, of partial sketches and of experts that
+    // have some (and the sum of these), a counter per class and their total
+    int *sum_b = lds, *sum_x = lds + kMaxExperts, *sum_m = lds + 2 * kMaxExperts, *slot = sum_m + kMaxExperts + 1;
     const int tid = threadIdx.x, lane = tid & 63, n_threads = blockDim.x;
     if (tid < kEsClasses) slot[tid] = 0;
     for (int e = tid; e < E; e += n_threads) {
@@ -157,10 +159,11 @@ __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, in
     }
     __syncthreads();
     if (tid < 64) {          // exclusive sums, by one wave
-        int before_b = 0, before_x = 0;
+        int before_b = 0, before_x = 0, before_m = 0;
         for (int e0 = 0; e0 < E; e0 += 64) {
             const int e = e0 + lane;
             const int nb = e < E ? sum_b[e] : 0, nx = e < E ? sum_x[e] : 0;
+            const uint64_t multi = __ballot(nx > 0);
             int ib = nb, ix = nx;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -173,10 +176,13 @@ __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, in
             if (e < E) {
                 sum_b[e] = before_b + ib - nb;
                 sum_x[e] = before_x + ix - nx;
+                sum_m[e] = before_m + __popcll(multi & ((1ull << lane) - 1ull));
             }
+            before_m += __popcll(multi);
             before_b += __builtin_amdgcn_readlane(ib, 63);
             before_x += __builtin_amdgcn_readlane(ix, 63);
         }
+        if (lane == 0) sum_m[E] = before_m;
     }
     __syncthreads();
     // class 0: the longest
@@ -199,6 +205,7 @@ __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, in
         slot[kEsClasses] = at;
     }
     __syncthreads();
+    const int max_parts = min(E, max_items - E);      // experts with partial sketches, at most
     for (int i = slot[kEsClasses] + tid; i < max_items; i += n_threads) items[i].expert = -1;
     for (int e = tid; e < E; e += n_threads) {
         const EsRange r = es_range(offsets, e, N);
@@ -210,8 +217,9 @@ __device__ __forceinline__ void es_build_items(const int32_t *offsets, int E, in
                 items[at] = EsItem{e, r.begin + i * chunk, rows, sum_b[e] + i * (chunk / kEsTokens),
                                    i > 0 ? sum_x[e] + i - 1 : n > 1 ? -1 : -2, {0, 0, 0}};
         }
-        experts[e] = EsParts{sum_x[e], n - 1};
+        if (n > 1 && sum_m[e] < max_parts) experts[sum_m[e]] = EsParts{e, sum_x[e], n - 1};
     }
+    for (int i = sum_m[E] + tid; i < max_parts; i += n_threads) experts[i].count = 0;
 }
 
 __device__ __forceinline__ uint64_t es_key(const ExpertSketchArgs &a, int e) {
@@ -702,13 +710,14 @@ __global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int
     else each([](float *p, float v) { *p = v; });
 }
 
-// S_e += the partial sketches of expert e, in their order.
+// S_e += the partial sketches of expert e, in their order; a row of workgroups
+// per expert that has some.
 __global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int64_t size, int64_t max_extras,
                                                         const EsParts *__restrict__ experts,
                                                         const float *__restrict__ parts) {
     const EsParts own = experts[blockIdx.y];
     if (own.count == 0) return;
-    float *S = a.S + static_cast<int64_t>(blockIdx.y) * size;
+    float *S = a.S + static_cast<int64_t>(own.expert) * size;
     const float *p = parts + static_cast<int64_t>(own.first) * size;
     const int n = static_cast<int>(min(static_cast<int64_t>(own.count), max(static_cast<int64_t>(0), max_extras - own.first)));
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
@@ -960,7 +969,7 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
     if (p.extras > 0) {
         const int64_t size = a.d * R;
         const int64_t n = (size + 1023) / 1024;
-        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 64 ? n : 64, a.E), dim3(256), 0, st, a, size, p.extras, experts,
+        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 64 ? n : 64, p.extras < a.E ? p.extras : a.E), dim3(256), 0, st, a, size, p.extras, experts,
                            parts);
     }
     return hipGetLastError();
