@@ -238,6 +238,15 @@ __device__ __forceinline__ int64_t es_x_row(const ExpertSketchArgs &a, int i) {
 }
 
 // ---------------------------------------------------------- bf16, stage 1 --
+// A block of P is 32 rows x r, stored as the second product's operand: per 32
+// columns four runs of 1 KB, one for each load of a wave there. Lane (i, h)
+// of it takes rows 16 kb + 8 h + 4 q .. +3 of column i, kb and q the run's
+// number. Returns where four rows from 4 rows4 of a column are.
+__device__ __forceinline__ int es_p_at(int col, int rows4) {
+    const int kb = rows4 >> 2, h = (rows4 >> 1) & 1, q = rows4 & 1;
+    return ((((col >> 5) * 2 + kb) * 2 + q) * 64 + h * 32 + (col & 31)) * 4;
+}
+
 // A workgroup owns one 32-row block of P and RT of its columns over the
 // whole of k; its eight waves split the k range and add their tiles through
 // LDS in wave order, as stage 1 of the one-matrix sketch does.
@@ -352,11 +361,11 @@ __global__ __launch_bounds__(512) void es_project_kernel(ExpertSketchArgs a, int
     const int64_t block = static_cast<int64_t>(at.blocks) + at.index;
     if (block >= p_blocks) return;
     for (int q = tid; q < RT * 8; q += 512) {      // four rows of one column
-        const int col = q >> 3, t = 4 * (q & 7);
+        const int col = q % RT, t = 4 * (q / RT);
         f32x4_t v = zero_f32x4();
 #pragma unroll
         for (int w = 0; w < kEsWaves; ++w) v += *reinterpret_cast<const f32x4_t *>(&tile[(w * RT + col) * kTileLd + t]);
-        *reinterpret_cast<f32x4_t *>(P + (block * a.R + l0 + col) * kEsTokens + t) = a.c * v;
+        *reinterpret_cast<f32x4_t *>(P + block * a.R * kEsTokens + es_p_at(l0 + col, t / 4)) = a.c * v;
     }
 }
 
@@ -520,7 +529,7 @@ __device__ __forceinline__ void es_project_unit(const ExpertSketchArgs &a, const
 #pragma unroll
                 for (int part = 0; part < WK; ++part)
                     v += part == wk ? piece(mb, nb, q) : *at_tile((part + WK - wk - 1) % WK, mb, nb, q);
-                *reinterpret_cast<f32x4_t *>(P + ((block0 + mb) * R + l0 + 32 * nb + i32) * kEsTokens + 8 * q + 4 * h) =
+                *reinterpret_cast<f32x4_t *>(P + (block0 + mb) * R * kEsTokens + es_p_at(l0 + 32 * nb + i32, 2 * q + h)) =
                     a.c * v;
             }
         }
@@ -636,11 +645,11 @@ __global__ __launch_bounds__(256, 2) void es_fold_kernel(ExpertSketchArgs a, int
         };
         constexpr uint32_t kStep = R * kEsTokens * 4;   // bytes of P per step
         const __amdgpu_buffer_rsrc_t pview = es_view(P + block0 * R * kEsTokens, static_cast<uint32_t>(steps) * kStep);
-        const uint32_t poff = ((32 * wn * NB + i32) * kEsTokens + 8 * h) * 4;
+        const uint32_t poff = wn * NB * 4096 + lane * 16;
         auto pload = [&](uint32_t at_step, int nb, int kb, u32x4_t (&v)[2]) {
-            const uint32_t off = poff + at_step + (32 * nb * kEsTokens + 16 * kb) * 4;
+            const uint32_t off = poff + at_step + 4096 * nb + 2048 * kb;
             v[0] = es_load(pview, off);
-            v[1] = es_load(pview, off + 16);
+            v[1] = es_load(pview, off + 1024);
         };
         u32x4_t next0[2], next1[2], pv[2][NB][2];
         gload(0, next0);
