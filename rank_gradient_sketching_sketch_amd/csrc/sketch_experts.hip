@@ -732,7 +732,15 @@ __global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int6
     for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < size;
          i += static_cast<int64_t>(gridDim.x) * 1024) {
         f32x4_t v = *reinterpret_cast<const f32x4_t *>(S + i);
-        for (int q = 0; q < n; ++q) v += *reinterpret_cast<const f32x4_t *>(p + q * size + i);
+        int q = 0;
+        for (; q + 4 <= n; q += 4) {        // four requests at once
+            f32x4_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const f32x4_t *>(p + (q + j) * size + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v += w[j];
+        }
+        for (; q < n; ++q) v += *reinterpret_cast<const f32x4_t *>(p + q * size + i);
         *reinterpret_cast<f32x4_t *>(S + i) = v;
     }
 }
@@ -906,6 +914,7 @@ constexpr int64_t kEsWideFrom = 4096, kEsWideWGs = 320;
 // 32 columns, 8.0 with 64).
 constexpr int64_t kEsNarrowWGs = 160;
 
+constexpr int64_t kEsReduceWGs = 256;      // per expert, at most
 // Where the experts' last, shorter units are few, two workgroups take half the
 // columns of each: they fill what the long ones leave (k = 2048, r = 256, kernel
 // alone: 128 uneven experts, 32768 rows 48.7 us against 52.7, 4096 rows 15.8
@@ -928,12 +937,13 @@ ExpertSketchPlan plan_expert_sketch(int64_t N, int E, int64_t d, int64_t k, int 
         p.total = p.p_bytes;
         return p;
     }
-    // Rows of an item: each 32 of them take an item about 1.2 us, and every
-    // item beyond an expert's first costs d r 4 bytes written and read again,
-    // which is d r 1.6e-6 us of the whole chip; with N / chunk such items the
-    // sum of the two is least at sqrt(N d r) / 152. (8 experts, 8192 rows,
-    // d = 768, r = 256: 288 rows, 46 us, against 86 us with unsplit experts.)
-    int64_t chunk = static_cast<int64_t>(sqrt(static_cast<double>(N) * static_cast<double>(d) * R) / 152.0);
+    // Rows of an item: the longest one's time grows with them, and every item
+    // beyond an expert's first costs d r 4 bytes written and read again. With
+    // N / chunk such items the sum of the two is least at sqrt(N d r) times a
+    // constant. Whole call in us with 1 / 152, 1 / 110, 1 / 90 of it, uneven
+    // experts, d = 768, k = 2048, r = 256: 128 experts, 32768 rows 106, 97, 97;
+    // 32 experts, 16384 rows 66, 63, 62; 8 experts, 8192 rows 45, 47, 48.
+    int64_t chunk = static_cast<int64_t>(sqrt(static_cast<double>(N) * static_cast<double>(d) * R) / 110.0);
     chunk = (chunk < 256 ? 256 : chunk + 31) / 32 * 32;
     if (chunk > kEsMaxChunk) chunk = kEsMaxChunk;
     p.chunk = static_cast<int>(chunk);
@@ -978,7 +988,7 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
     if (p.extras > 0) {
         const int64_t size = a.d * R;
         const int64_t n = (size + 1023) / 1024;
-        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < 64 ? n : 64, p.extras < a.E ? p.extras : a.E), dim3(256), 0, st, a, size, p.extras, experts,
+        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < kEsReduceWGs ? n : kEsReduceWGs, p.extras < a.E ? p.extras : a.E), dim3(256), 0, st, a, size, p.extras, experts,
                            parts);
     }
     return hipGetLastError();
