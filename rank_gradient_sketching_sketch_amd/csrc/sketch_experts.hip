@@ -21,13 +21,15 @@
 // would cost half as many bytes again on the path that bounds that product.
 //
 // 4096 tokens, 8 of 128 experts (uneven: 1 to 1300 rows each), d = 768,
-// k = 2048, r = 256: projection 56 us, second product 66 us, partial sketches
-// 7 us, 120 us in all. The bytes that cannot be left out (X, dY, S) take 32 us
+// k = 2048, r = 256: projection 43 us, second product 55 us, partial sketches
+// 6 us, 98 us in all. The bytes that cannot be left out (X, dY, S) take 32 us
 // at the rate of a copy, the 73 GFLOP of the matrix instructions 61 us at the
-// rate of a large library product. Of the projection, 22 us are the loop over
-// k (14 to 19 of them matrix instructions), 8 us the way to its first row and
-// 8 us P's 33 MB written; with even experts it takes 37 us, the rest is the
-// last units' latency. Of the second product 17 us are S's 100 MB written.
+// rate of a large library product. Of the projection, some 22 us are the loop
+// over k (14 to 19 of them matrix instructions), 7 us the way to its first row
+// and 2 us P's 33 MB written; with even experts it takes 35 us, the rest is
+// the last units' latency. The second product takes 42 us with even experts:
+// 20 us are S's 100 MB written, which comes on top of 22 us of matrix
+// instructions because workgroups that start together finish together.
 #include <math.h>
 
 #include <type_traits>
