@@ -755,6 +755,7 @@ __global__ __launch_bounds__(256) void es_reduce_kernel(ExpertSketchArgs a, int6
 // this path is for are short, and what bounds them is the latency of a few
 // loads, which more waves over fewer steps hide best.
 constexpr int kEsF32Waves = 8;
+constexpr int kEsUnitsAtOnce = 1 << 16;     // units of a grid's row: a launch has fewer than 2^32 threads in x
 
 // D = A(16x4) * B(4x16) + C. Lane L holds A[L%16][L/16], B[L/16][L%16] and
 // D[4*(L/16) .. +3][L%16].
@@ -794,7 +795,8 @@ __global__ __launch_bounds__(64 * kEsF32Waves) void es_project_f32_kernel(Expert
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the column tiles of a block of rows go to one XCD, as in the bf16 kernel
     const int j = blockIdx.x / kXcds, tiles = (a.R + 16 * NT - 1) / (16 * NT);
-    const int number = j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds), l0 = j % tiles * 16 * NT;
+    const int number = blockIdx.z * kEsUnitsAtOnce + j / tiles * kXcds + static_cast<int>(blockIdx.x % kXcds);
+    const int l0 = j % tiles * 16 * NT;
     const EsUnit at = es_unit(a.offsets, a.E, static_cast<int>(a.N), number, kRows, 1);
     if (at.expert < 0) return;
     const EsRange rows = at.rows;
@@ -905,8 +907,8 @@ constexpr int64_t kEsF32SmallWGs = 256;
 constexpr int64_t kEsMaxChunk = 1 << 20;   // an item's part of P stays within a view (r <= 256)
 // The wide projection is used from kEsWideFrom rows or where the other one
 // would take more than kEsWideWGs workgroups (whole call, k = 2048, r = 256:
-// 8 experts, 2048 rows 35 us against 41 wide, 4096 rows 61 against 56; 128
-// experts, 1024 rows 40 against 40, 2048 rows 49 against 44).
+// 8 experts, 2048 rows 34 us against 37 wide, 4096 rows 45 against 40; 128
+// experts, 1024 rows 42 against 41, 2048 rows 51 against 42).
 constexpr int64_t kEsWideFrom = 4096, kEsWideWGs = 320;
 
 // The other projection takes 128 columns, or all r, per workgroup; 64 or 32
@@ -1005,7 +1007,9 @@ hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t
             const int T = p.p_blocks * ((a.R + 31) / 32) <= kEsF32SmallWGs ? 1 : 2;
             const int64_t units = a.N / (16 * T) + (a.N < a.E ? a.N : a.E);
             hipLaunchKernelGGL(T == 1 ? es_project_f32_kernel<1> : es_project_f32_kernel<2>,
-                               dim3((units + kXcds - 1) / kXcds * kXcds * ((a.R + 16 * T - 1) / (16 * T))),
+                               dim3(((units < kEsUnitsAtOnce ? units : kEsUnitsAtOnce) + kXcds - 1) / kXcds * kXcds *
+                                        ((a.R + 16 * T - 1) / (16 * T)), 1,
+                                    (units + kEsUnitsAtOnce - 1) / kEsUnitsAtOnce),
                                dim3(64 * kEsF32Waves), 0, st, a, K, P);
         }
         // tiles of 64 x 64 where they still give each compute unit one, which

@@ -1,17 +1,18 @@
 """The sketch over experts against the plain fp64 oracle.
 
-Tolerances. bf16: per entry, P's two-term form is off by at most 2^-16 |P|
+Tolerances. bf16: per entry, P's three-term form is off by at most 2^-24 |P|
 (each bf16 rounding is 2^-8 of what it rounds), its fp32 accumulation by
-(k + 16) 2^-23 of c sum |X| and that of S by (2 n + 16) 2^-23 of
+(k + 16) 2^-23 of c sum |X| and that of S by (3 n + 16) 2^-23 of
 sum |dY| |P| (2^-23: the matrix cores' additions are not taken to round to
-nearest). Over all entries those errors are independent: the split's root
-mean square is below (0.45 2^-8)^2 < 2^-18, the accumulations' below
-sqrt(k + n) 2^-23, so the relative Frobenius error stays below 1e-5. fp32:
+nearest). Over all entries those errors are independent: the accumulations'
+root mean square is below sqrt(k + 3 n) 2^-23, so the relative Frobenius error
+stays below 1e-5. fp32:
 (k + n + 8) 2^-23 of the magnitudes, and 1e-5 likewise."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 import rank_gradient_sketching_sketch_amd as L
 from rank_gradient_sketching_sketch_amd import binding as B
 from oracle import experts as ox
@@ -39,7 +40,7 @@ def _check(S, ref, mag_p, mag_x, k, n, bf16):
     S = _f64(S)
     u = 2.0 ** -23
     if bf16:
-        bound = (2.0 ** -16 + (2 * n + 16) * u) * mag_p + (k + 16) * u * (1 + 2.0 ** -8) * mag_x
+        bound = (2.0 ** -24 + (3 * n + 16) * u) * mag_p + (k + 16) * u * (1 + 2.0 ** -8) * mag_x
     else:
         bound = (k + n + 8) * u * (mag_x + mag_p)
     assert np.all(np.abs(S - ref) <= bound + 1e-30)
@@ -266,3 +267,22 @@ def test_one_row_of_any_stride():
         L.logra_sketch_experts(m, offsets, X.as_strided((1, 64), (ld, 1)), dY.as_strided((1, 40), (ld, 1)), got, False,
                                order=order, topk=1)
         assert torch.equal(want, got)
+
+
+def test_f32_more_rows_than_one_row_of_the_grid():
+    """2.24 million rows (70000 units of 32): whole numbers and halves, so
+    that every sum is exact in fp32."""
+    dev = device()
+    N, E, d, r = 70000 * 32, 3, 2, 4
+    g = torch.Generator().manual_seed(4)
+    dY = torch.randint(0, 2, (N, d), generator=g).float().to(dev)
+    X = torch.ones(N, 1, device=dev)
+    bounds = [0, 1000003, 1000003, N - 5]
+    offsets = torch.tensor(bounds, dtype=torch.int32, device=dev)
+    S = torch.empty(E, d, r, device=dev)
+    m = L.MatrixDesc(d, 1, r, seed=3, step=1, matrix_id=9)
+    L.logra_sketch_experts(m, offsets, X, dY, S, False)
+    for e in range(E):
+        A = oracle.sign_matrix(3, 1, 9 + e, r, 1)
+        sums = _f64(dY[bounds[e]:bounds[e + 1]]).sum(0)
+        assert np.array_equal(_f64(S[e]), sums[:, None] * A[:, 0][None, :])
