@@ -16,9 +16,9 @@
 // All of them are bound by memory. The row kernels give each token a
 // workgroup, so that a token's own row crosses the memory bus once however
 // many experts it goes to. Rows of Xs and dYs that no pair maps to are not
-// written. 4096 tokens, 8 of 128 experts, bf16 rows of 2048: gather 30 us
-// (147 MB, 4.8 TB/s), combine 33 us (151 MB, 4.6 TB/s), combine backward 59 us
-// (277 MB, 4.7 TB/s); a copy of 1 GiB reaches 5.2 TB/s on this card.
+// written. 4096 tokens, 8 of 128 experts, bf16 rows of 2048: gather 27 us
+// (147 MB, 5.4 TB/s), combine 25.5 us (151 MB, 5.9 TB/s), combine backward 55 us
+// (277 MB, 5.0 TB/s); a copy of 1 GiB reaches 5.2 TB/s on this card.
 #include <type_traits>
 
 #include "common.hpp"
@@ -241,33 +241,42 @@ struct RowOf {
     static constexpr int V = BF16 ? 8 : 4;
     using Elem = std::conditional_t<BF16 != 0, uint16_t, uint32_t>;
     using Vec = std::conditional_t<BF16 != 0, u32x4_e2_t, u32x4_e4_t>;
-    static __device__ __forceinline__ u32x4_t load_bits(const char *p) { return *reinterpret_cast<const Vec *>(p); }
-    static __device__ __forceinline__ void store_bits(char *p, u32x4_t v) { *reinterpret_cast<Vec *>(p) = v; }
+    template <int NT = 0>
+    static __device__ __forceinline__ u32x4_t load_bits(const char *p) {
+        const Vec *src = reinterpret_cast<const Vec *>(p);
+        return NT ? __builtin_nontemporal_load(src) : *src;
+    }
+    template <int NT>
+    static __device__ __forceinline__ void store_bits(char *p, u32x4_t v) {
+        Vec *dst = reinterpret_cast<Vec *>(p);
+        if (NT) __builtin_nontemporal_store(v, dst);
+        else *dst = v;
+    }
+    template <int NT>
     static __device__ __forceinline__ void load(const char *p, float (&v)[V]) {
+        const u32x4_t w = load_bits<NT>(p);
         if (BF16) {
-            const u32x4_t w = *reinterpret_cast<const u32x4_e2_t *>(p);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[2 * e] = bf16_lo(w[e]);
                 v[(2 * e + 1) % V] = bf16_hi(w[e]);
             }
         } else {
-            const u32x4_t w = *reinterpret_cast<const u32x4_e4_t *>(p);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
         }
     }
+    template <int NT>
     static __device__ __forceinline__ void store(char *p, const float (&v)[V]) {
         u32x4_t w;
         if (BF16) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[(2 * e) % V], v[(2 * e + 1) % V]);
-            *reinterpret_cast<u32x4_e2_t *>(p) = w;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
-            *reinterpret_cast<u32x4_e4_t *>(p) = w;
         }
+        store_bits<NT>(p, w);
     }
     // the first n < V elements, the rest zero
     static __device__ __forceinline__ void load_some(const char *p, int n, float (&v)[V]) {
@@ -287,18 +296,20 @@ struct RowOf {
                 else reinterpret_cast<float *>(p)[e] = v[e];
             }
     }
+    template <int NT = 0>
     static __device__ __forceinline__ void get(const char *p, int n, float (&v)[V]) {
-        if (n >= V) load(p, v);
+        if (n >= V) load<NT>(p, v);
         else load_some(p, n, v);
     }
+    template <int NT = 0>
     static __device__ __forceinline__ void put(char *p, int n, const float (&v)[V]) {
-        if (n >= V) store(p, v);
+        if (n >= V) store<NT>(p, v);
         else store_some(p, n, v);
     }
 };
 
 // Without weights the rows' bits are copied.
-template <int BF16>
+template <int BF16, int NT>
 __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h, const char *__restrict__ X,
                                                                     int64_t ldx, const int32_t *__restrict__ slots,
                                                                     const float *__restrict__ w,
@@ -324,11 +335,11 @@ __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h
                 float y[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) y[e] = f * x[e];
-                R::put(dst, h - c, y);
+                R::template put<NT>(dst, h - c, y);
             });
         } else if (h - c >= V) {
             const u32x4_t x = R::load_bits(src);
-            each([&](char *dst, int) { R::store_bits(dst, x); });
+            each([&](char *dst, int) { R::template store_bits<NT>(dst, x); });
         } else {
             for (int e = 0; e < h - c; ++e) {
                 const typename R::Elem x = reinterpret_cast<const typename R::Elem *>(src)[e];
@@ -338,7 +349,7 @@ __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(int K, int h
     }
 }
 
-template <int BF16>
+template <int BF16, int NT>
 __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(int K, int h, const char *__restrict__ Ys,
                                                                      int64_t ldys, int64_t n_rows,
                                                                      const int32_t *__restrict__ slots,
@@ -355,16 +366,16 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(int K, int 
             const int64_t s = slots[t * K + j];
             if (s < 0 || s >= n_rows) continue;
             float x[V];
-            R::get(Ys + (s * ldys + c) * B, h - c, x);
+            R::template get<NT>(Ys + (s * ldys + c) * B, h - c, x);
             const float f = w ? w[t * K + j] : 1.f;
 #pragma unroll
             for (int e = 0; e < V; ++e) y[e] = fmaf(f, x[e], y[e]);
         }
-        R::put(Y + (t * ldy + c) * B, h - c, y);
+        R::template put<NT>(Y + (t * ldy + c) * B, h - c, y);
     }
 }
 
-template <int BF16>
+template <int BF16, int NT>
 __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(
     int K, int h, const char *__restrict__ dY, int64_t lddy, const char *__restrict__ Ys, int64_t ldys,
     const int32_t *__restrict__ slots, const float *__restrict__ w, char *__restrict__ dYs, int64_t lddys,
@@ -383,13 +394,13 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(
             for (int c = threadIdx.x * V; c < h; c += kRowThreads * V) {
                 float g[V], y[V];
                 R::get(dY + (t * lddy + c) * B, h - c, g);
-                R::get(Ys + (s * ldys + c) * B, h - c, y);
+                R::template get<NT>(Ys + (s * ldys + c) * B, h - c, y);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     dot = fmaf(g[e], y[e], dot);
                     g[e] *= f;
                 }
-                R::put(dYs + (s * lddys + c) * B, h - c, g);
+                R::template put<NT>(dYs + (s * lddys + c) * B, h - c, g);
             }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
@@ -404,10 +415,24 @@ __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(
     }
 }
 
+// Above this many bytes of sorted rows the kernels read and write them past
+// the caches (the last-level one holds 256 MB, and what a step does between
+// two uses of the same rows is more than that). bf16 rows of 2048, 8 pairs per
+// token, us without / with: rows not in the caches, 4096 tokens (134 MB)
+// gather 30.4 / 25.8, combine 33.5 / 25.9, its gradient 59.0 / 55.7; 2500
+// tokens (82 MB) 16.6 / 16.9, 20.5 / 18.9, 43.0 / 41.5; the same buffers again
+// and again, 4096 tokens 23.4 / 25.1, 23.4 / 24.7, 50.2 / 54.3, 2500 tokens 15.5
+// / 16.0, 16.2 / 18.6, 31.9 / 40.0. A token's own row in the backward kernel is
+// read topk times and stays cached.
+constexpr int64_t kRowStreamBytes = 96ll << 20;
+static bool stream_rows(int64_t pairs, int64_t h, int elem) { return pairs * h * elem > kRowStreamBytes; }
+
 hipError_t launch_expert_gather(int64_t T, int K, int64_t h, int elem, const void *X, int64_t ldx,
                                 const int32_t *slots, const float *w, void *Xs, int64_t ldxs, int64_t n_rows,
                                 hipStream_t st) {
-    auto kernel = elem == 2 ? expert_gather_kernel<1> : expert_gather_kernel<0>;
+    const bool nt = stream_rows(T * K, h, elem);
+    auto kernel = elem == 2 ? (nt ? expert_gather_kernel<1, 1> : expert_gather_kernel<1, 0>)
+                            : (nt ? expert_gather_kernel<0, 1> : expert_gather_kernel<0, 0>);
     hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
                        static_cast<const char *>(X), ldx, slots, w, static_cast<char *>(Xs), ldxs, n_rows);
     return hipGetLastError();
@@ -416,7 +441,9 @@ hipError_t launch_expert_gather(int64_t T, int K, int64_t h, int elem, const voi
 hipError_t launch_expert_combine(int64_t T, int K, int64_t h, int elem, const void *Ys, int64_t ldys,
                                  int64_t n_rows, const int32_t *slots, const float *w, void *Y, int64_t ldy,
                                  hipStream_t st) {
-    auto kernel = elem == 2 ? expert_combine_kernel<1> : expert_combine_kernel<0>;
+    const bool nt = stream_rows(T * K, h, elem);
+    auto kernel = elem == 2 ? (nt ? expert_combine_kernel<1, 1> : expert_combine_kernel<1, 0>)
+                            : (nt ? expert_combine_kernel<0, 1> : expert_combine_kernel<0, 0>);
     hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
                        static_cast<const char *>(Ys), ldys, n_rows, slots, w, static_cast<char *>(Y), ldy);
     return hipGetLastError();
@@ -425,7 +452,9 @@ hipError_t launch_expert_combine(int64_t T, int K, int64_t h, int elem, const vo
 hipError_t launch_expert_combine_backward(int64_t T, int K, int64_t h, int elem, const void *dY, int64_t lddy,
                                           const void *Ys, int64_t ldys, const int32_t *slots, const float *w,
                                           void *dYs, int64_t lddys, int64_t n_rows, float *dw, hipStream_t st) {
-    auto kernel = elem == 2 ? expert_combine_backward_kernel<1> : expert_combine_backward_kernel<0>;
+    const bool nt = stream_rows(T * K, h, elem);
+    auto kernel = elem == 2 ? (nt ? expert_combine_backward_kernel<1, 1> : expert_combine_backward_kernel<1, 0>)
+                            : (nt ? expert_combine_backward_kernel<0, 1> : expert_combine_backward_kernel<0, 0>);
     hipLaunchKernelGGL(kernel, dim3(T), dim3(kRowThreads), 0, st, K, static_cast<int>(h),
                        static_cast<const char *>(dY), lddy, static_cast<const char *>(Ys), ldys, slots, w,
                        static_cast<char *>(dYs), lddys, n_rows, dw);

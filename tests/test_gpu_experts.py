@@ -91,7 +91,7 @@ def _f64(t):
 
 ROWS = [(1, 1, 1, 1, 0, 0), (1, 8, 128, 2048, 0, 0), (5, 3, 4, 7, 3, 1), (33, 8, 16, 256, 8, 0), (40, 2, 8, 1499, 0, 0),
         (9, 6, 60, 1000, 5, 3), (17, 1, 3, 4100, 4, 4), (3, 64, 8, 520, 0, 0), (200, 4, 8, 64, 0, 0),
-        (64, 9, 5, 9000, 2, 1)]
+        (64, 9, 5, 9000, 2, 1), (1200, 3, 5, 14001, 3, 1)]      # the last: more than 96 MB of rows
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
