@@ -31,8 +31,8 @@ constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 // Up to kSortSelf pairs the sort is one launch: every workgroup counts all
 // pairs itself and places its own kSortChunk of them. Above that a launch of
 // counts goes first, whose sums the workgroups then add up. (128 experts: 4096
-// pairs 6.1 us in one launch, 7.3 us and a launch more in two; 32768 pairs
-// 17.5 us in one, 10 us in two.)
+// pairs 5.6 us in one launch, 4160 pairs 4.7 us and 2.4 us for the counts in
+// two; 32768 pairs 17.5 us in one, 6.0 us and 2.7 to 4 us in two.)
 constexpr int kSortSelf = 4096, kSortChunk = 1024;
 constexpr int kSortMaxBlocks = 256;
 
@@ -109,51 +109,52 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids,
     int *before = total + E;                     // [E] pairs of the expert in the chunks before this one
     __shared__ int wave_sum[kSortWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < (kSortWaves + 2) * E; i += kSortThreads) lds[i] = 0;
-    __syncthreads();
-
     const int64_t p0 = static_cast<int64_t>(blockIdx.x) * chunk;
     const int per_wave = chunk / kSortWaves;     // a multiple of 64
     const int64_t w0 = p0 + static_cast<int64_t>(wave) * per_wave;
     int *mine = cnt + wave * E;
-    for (int64_t g = w0; g < w0 + per_wave && g < n; g += 64) {
-        const int e = g + lane < n ? ids(g + lane) : E;
-        if (e < E) atomicAdd(&mine[e], 1);
-    }
-    __syncthreads();
 
+    // what the counts need is requested before the counters are cleared: the
+    // first group's experts (kept for the second pass over them), and the
+    // pairs of the other chunks, as counts or, kOther at most, one by one
+    constexpr int kOther = kSortSelf / kSortThreads;
+    const int e_first = w0 + lane < n ? ids(w0 + lane) : E;
+    const int parts = max(1, kSortThreads / E), part = tid / E, e_part = tid - part * E;
+    int t = 0, b = 0, other[kOther];
     if (hist) {
-        const int parts = max(1, kSortThreads / E);
-        const int part = tid / E;
         if (part < parts)
-            for (int e = tid - part * E; e < E; e += kSortThreads) {
-                int t = 0, b = 0;
-                for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
-                    const int h = hist[static_cast<int64_t>(q) * E + e];
-                    t += h;
-                    b += q < static_cast<int>(blockIdx.x) ? h : 0;
-                }
-                atomicAdd(&total[e], t);
-                atomicAdd(&before[e], b);
+            for (int q = part; q < static_cast<int>(gridDim.x); q += parts) {
+                const int h = hist[static_cast<int64_t>(q) * E + e_part];
+                t += h;
+                b += q < static_cast<int>(blockIdx.x) ? h : 0;
             }
     } else {
-        // the other chunks' pairs, eight at a time per thread
-        for (int64_t q0 = tid; q0 < n; q0 += 8 * kSortThreads) {
-            int e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t p = q0 + i * kSortThreads;
-                e[i] = p < n && (p < p0 || p >= p0 + chunk) ? ids(p) : E;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e[i] < E) atomicAdd(&(q0 + i * kSortThreads < p0 ? before : total)[e[i]], 1);
+        for (int i = 0; i < kOther; ++i) {
+            const int64_t p = tid + i * kSortThreads;
+            other[i] = p < n && (p < p0 || p >= p0 + chunk) ? ids(p) : E;
         }
+    }
+    for (int i = tid; i < (kSortWaves + 2) * E; i += kSortThreads) lds[i] = 0;
+    __syncthreads();
+    for (int64_t g = w0; g < w0 + per_wave && g < n; g += 64) {
+        const int e = g == w0 ? e_first : g + lane < n ? ids(g + lane) : E;
+        if (e < E) atomicAdd(&mine[e], 1);
+    }
+    if (hist) {
+        if (part < parts) {
+            atomicAdd(&total[e_part], t);
+            atomicAdd(&before[e_part], b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kOther; ++i)
+            if (other[i] < E) atomicAdd(&(tid + i * kSortThreads < p0 ? before : total)[other[i]], 1);
         __syncthreads();
         for (int e = tid; e < E; e += kSortThreads) {
-            int t = total[e] + before[e];
-            for (int w = 0; w < kSortWaves; ++w) t += cnt[w * E + e];
-            total[e] = t;
+            int sum = total[e] + before[e];
+            for (int w = 0; w < kSortWaves; ++w) sum += cnt[w * E + e];
+            total[e] = sum;
         }
     }
     __syncthreads();
@@ -177,10 +178,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids,
     if (tid < E) {
         const int first = carry + incl - own;
         int at = first + before[tid];
+        int c[kSortWaves];
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) c[w] = cnt[w * E + tid];
+#pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            const int c = cnt[w * E + tid];
             cnt[w * E + tid] = at;
-            at += c;
+            at += c[w];
         }
         if (blockIdx.x == 0) offsets[tid] = first;
     }
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(SortIds ids,
 
     for (int64_t g = w0; g < w0 + per_wave && g < n; g += 64) {
         const int64_t p = g + lane;
-        const int e = p < n ? ids(p) : E;
+        const int e = g == w0 ? e_first : p < n ? ids(p) : E;
         const uint64_t same = match_lanes(e, bits);
         const int rank = __popcll(same & ((1ull << lane) - 1ull));
         int at = 0;
