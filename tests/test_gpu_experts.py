@@ -91,7 +91,7 @@ def _f64(t):
 
 ROWS = [(1, 1, 1, 1, 0, 0), (1, 8, 128, 2048, 0, 0), (5, 3, 4, 7, 3, 1), (33, 8, 16, 256, 8, 0), (40, 2, 8, 1499, 0, 0),
         (9, 6, 60, 1000, 5, 3), (17, 1, 3, 4100, 4, 4), (3, 64, 8, 520, 0, 0), (200, 4, 8, 64, 0, 0),
-        (64, 9, 5, 9000, 2, 1), (1200, 3, 5, 14001, 3, 1)]      # the last: more than 96 MB of rows
+        (64, 9, 5, 9000, 2, 1), (6, 3, 4, 9, 2, 1), (12, 5, 6, 2049, 0, 0), (1200, 3, 5, 14001, 3, 1)]      # the last: more than 96 MB of rows
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
@@ -277,3 +277,27 @@ def test_repeats_graph_and_side_stream():
         torch.cuda.synchronize()
         graph.replay()
         same()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("h", [9, 1499, 2047])
+def test_infinities_near_a_row_end_off_the_vector_width(h, dt):
+    """An infinity counts once wherever it stands: <dY, Ys> stays infinite, and
+    no other element of the row is touched by it."""
+    dev = device()
+    T, K, E = 4, 3, 5
+    offsets, order, slots = _sort(_ids(2, T, K, E).to(dev), E, dev)
+    w = torch.full((T, K), 2.0, device=dev)
+    for at in sorted({max(0, h - 1 - i) for i in range(10)}):
+        dY = torch.ones(T, h, device=dev).to(dt)
+        Ys = torch.ones(T * K, h, device=dev).to(dt)
+        Ys[:, at] = float("inf")
+        Y, dYs, dw = torch.empty_like(dY), torch.zeros_like(Ys), torch.empty(T, K, device=dev)
+        L.logra_expert_combine(Ys, slots, Y, weights=w)
+        L.logra_expert_combine_backward(dY, Ys, slots, w, dYs, dw)
+        kept = slots >= 0
+        assert torch.equal(dw.isinf(), kept) and not dw.isnan().any()
+        some = kept.any(1)
+        assert torch.equal(Y[some][:, at].float(), torch.full((int(some.sum()),), float("inf"), device=dev))
+        rest = torch.arange(h, device=dev) != at
+        assert torch.equal(Y[:, rest].float(), (2 * kept.sum(1, keepdim=True)).float().expand(T, h - 1))
