@@ -92,6 +92,16 @@ __device__ __forceinline__ void grad_load(const gbytes *p, int64_t i, float (&v)
     }
 }
 
+// The first n < V of them, zeros behind: the requests go out together.
+template <int BF16, int V>
+__device__ __forceinline__ void grad_load_some(const gbytes *p, int64_t i, int n, float (&v)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        v[e] = 0.f;
+        if (e < n) v[e] = grad_get<BF16>(p, i + e);
+    }
+}
+
 template <int BF16, int V, int NT = 0>
 __device__ __forceinline__ void grad_store(gbytes *p, int64_t i, const float (&v)[V]) {
     if (BF16) {
@@ -150,10 +160,10 @@ __device__ __forceinline__ GradChunk grad_chunk(const GradEntry &e, int64_t c) {
     return k;
 }
 
-// f(chunk-local unit) over the chunk's units of V elements: a whole unit
-// calls full(index), the rest of a row calls one(index) per element.
-template <int V, int U, class Full, class One>
-__device__ __forceinline__ void grad_units(GradGroup g, int rows, int cols, Full full, One one) {
+// f(chunk-local unit) over the chunk's units of V elements: whole units go to
+// full(rows, columns, which), the rest of a row to rest(row, column).
+template <int V, int U, class Full, class Some>
+__device__ __forceinline__ void grad_units(GradGroup g, int rows, int cols, Full full, Some rest) {
     const int upr = (cols + V - 1) / V;
     const int n = rows * upr;
     for (int u0 = g.id; u0 < n; u0 += U * g.size) {
@@ -170,8 +180,7 @@ __device__ __forceinline__ void grad_units(GradGroup g, int rows, int cols, Full
         full(row, col, whole);
 #pragma unroll
         for (int q = 0; q < U; ++q)
-            if (some[q] && !whole[q])
-                for (int e = col[q]; e < cols; ++e) one(row[q], e);
+            if (some[q] && !whole[q]) rest(row[q], col[q]);
     }
 }
 
@@ -180,15 +189,15 @@ constexpr int kGradUnroll = 4, kGradRunBytes = 128;
 
 // A run of n elements without gaps: whole(index) for every U units of V
 // elements of a thread at once while they last, then unit by unit, then
-// one(index) for the last elements.
+// one(index) for the last elements (fewer than V).
 template <int V, int U, class Many, class Unit, class One>
 __device__ __forceinline__ void grad_run(GradGroup g, int64_t n, Many many, Unit unit, One one) {
     const int64_t step = static_cast<int64_t>(g.size) * V;
     int64_t i = static_cast<int64_t>(g.id) * V;
     for (; i + (U - 1) * step + V <= n; i += U * step) many(i, step);
     for (; i + V <= n; i += step) unit(i);
-    if (i < n)
-        for (int64_t e = i; e < n; ++e) one(e);
+    const int64_t e = n / V * V + g.id;      // the last elements: one for each of the first threads
+    if (e < n) one(e);
 }
 
 template <int BF16, int NT>
@@ -268,8 +277,13 @@ __device__ __forceinline__ double grad_chunk_sumsq(GradGroup g, GradChunk k, dou
                 }
         },
         [&](int row, int col) {
-            const double d = grad_get<BF16>(k.p, k.at + row * k.ld + col);
-            sum = fma(d, d, sum);
+            float v[V];
+            grad_load_some<BF16, V>(k.p, k.at + row * k.ld + col, k.cols - col, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const double d = v[e];
+                sum = fma(d, d, sum);
+            }
         });
     return sum;
 }
@@ -293,7 +307,11 @@ __device__ __forceinline__ void grad_chunk_scale(GradGroup g, GradChunk k, GradC
             }
         },
         [&](int row, int col) {
-            grad_put<OUT16>(o.p, o.at + row * o.ld + col, coef * grad_get<IN16>(k.p, k.at + row * k.ld + col));
+            float v[V];
+            grad_load_some<IN16, V>(k.p, k.at + row * k.ld + col, k.cols - col, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (e < k.cols - col) grad_put<OUT16>(o.p, o.at + row * o.ld + col + e, coef * v[e]);
         });
 }
 
