@@ -21,8 +21,8 @@
 // would cost half as many bytes again on the path that bounds that product.
 //
 // 4096 tokens, 8 of 128 experts (uneven: 1 to 1300 rows each), d = 768,
-// k = 2048, r = 256: projection 43 us, second product 55 us, partial sketches
-// 6 us, 98 us in all. The bytes that cannot be left out (X, dY, S) take 32 us
+// k = 2048, r = 256: projection 44 us, second product 55 us, partial sketches
+// 6 us, 100 us in all. The bytes that cannot be left out (X, dY, S) take 32 us
 // at the rate of a copy, the 73 GFLOP of the matrix instructions 61 us at the
 // rate of a large library product. Of the projection, some 22 us are the loop
 // over k (14 to 19 of them matrix instructions), 7 us the way to its first row
