@@ -70,6 +70,10 @@ CASES = [
     # 64 columns per workgroup of the other projection, of 256 and of 64
     (900, 2, 4, 72, 712, 256, 2, 8),
     (3001, 2, 6, 64, 72, 64, None, 0),
+    # the most experts
+    (1500, 2, 1024, 16, 72, 256, None, 0),
+    (700, 1, 1024, 8, 64, 32, None, 0),
+    (6000, 1, 1024, 8, 64, 128, 1023, 0),
 ]
 
 
