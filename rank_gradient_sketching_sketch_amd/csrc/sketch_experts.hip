@@ -983,8 +983,8 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
         int rt = R < 128 ? R : 128;
         while (rt > 32 && p.p_blocks * (R / rt) <= kEsNarrowWGs) rt /= 2;
         hipLaunchKernelGGL(rt == 32 ? es_project_kernel<32> : rt == 64 ? es_project_kernel<64> : es_project_kernel<128>,
-                           dim3((p.p_blocks / kXcds + 1) * kXcds * (R / rt)), dim3(512), 0, st, a, p.chunk, K, p.p_blocks, n_items, items,
-                           experts, P);
+                           dim3((p.p_blocks / kXcds + 1) * kXcds * (R / rt)), dim3(512), 0, st, a, p.chunk, K,
+                           p.p_blocks, n_items, items, experts, P);
     }
     const int tiles = (D + kEsRows - 1) / kEsRows;
     hipLaunchKernelGGL(es_fold_kernel<R>, dim3((p.items + kXcds - 1) / kXcds * kXcds * tiles), dim3(256), 0, st, a, D,
@@ -992,8 +992,9 @@ static hipError_t expert_sketch_bf16_r(const ExpertSketchArgs &a, hipStream_t st
     if (p.extras > 0) {
         const int64_t size = a.d * R;
         const int64_t n = (size + 1023) / 1024;
-        hipLaunchKernelGGL(es_reduce_kernel, dim3(n < kEsReduceWGs ? n : kEsReduceWGs, p.extras < a.E ? p.extras : a.E), dim3(256), 0, st, a, size, p.extras, experts,
-                           parts);
+        hipLaunchKernelGGL(es_reduce_kernel,
+                           dim3(n < kEsReduceWGs ? n : kEsReduceWGs, p.extras < a.E ? p.extras : a.E), dim3(256), 0,
+                           st, a, size, p.extras, experts, parts);
     }
     return hipGetLastError();
 }
