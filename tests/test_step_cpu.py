@@ -1,0 +1,149 @@
+"""The step scheduler's ordering, on the CPU: streams, events and the library's
+calls are stand-ins that record which work each stream has waited for."""
+import os
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from rank_gradient_sketching_sketch_amd import binding as B
+from rank_gradient_sketching_sketch_amd import step as step_module
+from rank_gradient_sketching_sketch_amd.step import ExpertGroup, Matrix, Step
+
+T, K, E, D, H, R = 16, 2, 3, 32, 64, 32
+
+
+class FakeStream:
+    """`seen`: the pieces of work that are over before the stream's next one starts."""
+    count = 0
+
+    def __init__(self, device=None, **kw):
+        FakeStream.count += 1
+        self.cuda_stream, self.device_index = FakeStream.count, 0
+        self.seen, self.idle = set(), True
+
+    def work(self, name):
+        self.seen.add(name)
+        self.idle = False
+        return name
+
+    def wait_event(self, e):
+        self.seen |= e.seen
+
+    def wait_stream(self, s):
+        self.seen |= s.seen
+
+    def query(self):
+        return self.idle
+
+
+class FakeEvent:
+    def __init__(self, *a, **kw):
+        self.seen = set()
+
+    def record(self, stream):
+        self.seen = set(stream.seen)
+
+
+class FakeTensor:
+    """A tensor that work `made` on `stream` writes; `kept` are the streams it was recorded on."""
+
+    def __init__(self, shape, stream, made=None):
+        self.shape, self.stream, self.made, self.kept = shape, stream, made, set()
+
+    def record_stream(self, s):
+        self.kept.add(s)
+
+
+@pytest.fixture
+def sim(monkeypatch):
+    if not os.path.exists(B.LIB_PATH):
+        from rank_gradient_sketching_sketch_amd import build_lib
+        build_lib.build()
+    s = SimpleNamespace(current=[FakeStream()], calls=[], seen=[], capturing=False)
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            s.current.append(self.stream)
+
+        def __exit__(self, *exc):
+            s.current.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: s.current[-1])
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "Event", FakeEvent)
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: s.capturing)
+    monkeypatch.setattr(B, "GradList", lambda tensors, device=None: SimpleNamespace(tensors=list(tensors), workspace_bytes=0))
+
+    def reads(name, st, *tensors):
+        for t in tensors:
+            if t.made is not None and st is not t.stream:
+                assert t.made in st.seen, "%s reads %s before it is there" % (name, t.made)
+                assert st in t.kept, "%s is not kept from other use" % t.made
+        s.calls.append((name, st))
+        s.seen.append(set(st.seen))
+        st.work("%s %d" % (name, len(s.calls)))
+
+    monkeypatch.setattr(B, "logra_sketch_project", lambda m, X, ws, st, opts: reads("project", st, X))
+    monkeypatch.setattr(B, "logra_sketch_fold", lambda m, dY, S, acc, ws, st, opts: reads("fold", st, dY))
+    monkeypatch.setattr(B, "logra_sketch_fold_parts", lambda m, dY, S, parts, phase, ws, st, opts: reads("fold", st, dY))
+    monkeypatch.setattr(B, "logra_sketch_experts", lambda m, offsets, X, dY, S, acc, order, topk, ws, stream: reads(
+        "experts", stream, *[t for t in (offsets, X, dY, order) if t is not None]))
+    return s
+
+
+def _step(n_dense, n_groups, **kw):
+    mats = [Matrix(D, H, i, torch.zeros(D, H), torch.zeros(D)) for i in range(n_dense)]
+    groups = [ExpertGroup(E, D, H, 100 + E * i, K, torch.zeros(E, D, H), torch.zeros(E, D)) for i in range(n_groups)]
+    return Step(mats, R, T, B.LOGRA_F32, groups=groups, **kw)
+
+
+def _run(st, sim, made, mbs=3, **kw):
+    """One step's sketches whose inputs the callbacks make on the current
+    stream (made) or had before."""
+    def new(what, shape):
+        cur = sim.current[-1]
+        return FakeTensor(shape, cur, cur.work(what) if made else None)
+
+    return st.sketch(1, mbs, lambda i, mb: (new("X %d %d" % (i, mb), (T, H)), new("dY %d %d" % (i, mb), (T, D))),
+                     expert_inputs=lambda g, mb: (new("Xe %d %d" % (g, mb), (T, H)), new("dYe %d %d" % (g, mb), (T * K, D)),
+                                                  new("offsets %d %d" % (g, mb), (E + 1,)),
+                                                  new("order %d %d" % (g, mb), (T * K,)) if g == 0 else None), **kw)
+
+
+@pytest.mark.parametrize("dense,groups,kw", [(1, 1, {}), (0, 2, {}), (3, 2, {}), (0, 1, {}), (1, 0, dict(late=True)),
+                                             (5, 0, dict(late=True))])
+@pytest.mark.parametrize("other", [False, True])
+@pytest.mark.parametrize("capturing", [False, True])
+def test_inputs_made_in_the_callbacks_are_waited_for(sim, dense, groups, kw, other, capturing):
+    """What a callback enqueues on the caller's stream is over before a lane
+    reads it, and its memory is kept; `other`: the caller's stream is not the
+    one that the step was made on."""
+    st = _step(dense, groups)
+    if other:
+        sim.current.append(FakeStream())
+    sim.capturing = capturing
+    _run(st, sim, True, **kw)
+    for name, lane in sim.calls:
+        assert any(lane is ln["stream"] for ln in st.lanes)
+    lanes = {id(ln["stream"]): ln["stream"] for ln in st.lanes}.values()
+    for ln in lanes:
+        assert ln.seen <= st.main.seen              # joined
+    assert len(sim.calls) == 3 * (2 * dense + groups)
+
+
+@pytest.mark.parametrize("dense,groups,kw", [(3, 1, {}), (0, 3, {}), (3, 1, dict(late=False)), (4, 0, {})])
+def test_inputs_made_before_leave_the_lanes_apart(sim, dense, groups, kw):
+    """Callbacks that enqueue nothing make no lane wait for another."""
+    st = _step(dense, groups)
+    sim.current[-1].idle = True
+    _run(st, sim, False, **kw)
+    lanes = [lane for _, lane in sim.calls]
+    assert len({id(lane) for lane in lanes}) == st.n_sketch > 2
+    for i, (lane, seen) in enumerate(zip(lanes, sim.seen)):
+        for j, (name, other) in enumerate(sim.calls[:i]):
+            assert ("%s %d" % (name, j + 1) in seen) == (other is lane)
