@@ -248,9 +248,11 @@ class Step:
             self.callbacks = torch.cuda.Stream(device=self.device)
         self.callbacks.wait_stream(torch.cuda.current_stream(self.device))
         self.callbacks.wait_stream(self.main)
-        with torch.cuda.stream(self.callbacks):
-            yield
-        self.main.wait_stream(self.callbacks)
+        try:
+            with torch.cuda.stream(self.callbacks):
+                yield
+        finally:
+            self.main.wait_stream(self.callbacks)
 
     def _take(self, lane, tensors):
         """What a callback has just made, for a lane to read: the lane waits
@@ -316,10 +318,11 @@ class Step:
             late = bool(self.groups)
         self.set_step(step)
         self._fork()
-        with self._late_inputs() if late else contextlib.nullcontext():
-            events = self._sketch(microbatches, inputs, probe, expert_inputs, self._take if late else None)
-        self._join()
-        return events
+        try:                # a callback may fail: what is enqueued by then is joined all the same
+            with self._late_inputs() if late else contextlib.nullcontext():
+                return self._sketch(microbatches, inputs, probe, expert_inputs, self._take if late else None)
+        finally:
+            self._join()
 
     def _sketch(self, microbatches, inputs, probe, expert_inputs, take):
         events = None

@@ -147,3 +147,27 @@ def test_inputs_made_before_leave_the_lanes_apart(sim, dense, groups, kw):
     for i, (lane, seen) in enumerate(zip(lanes, sim.seen)):
         for j, (name, other) in enumerate(sim.calls[:i]):
             assert ("%s %d" % (name, j + 1) in seen) == (other is lane)
+
+
+@pytest.mark.parametrize("late", [False, True])
+def test_a_callback_that_fails_leaves_no_lane_unjoined(sim, late):
+    """Work that was enqueued before an exception is over before what the
+    caller does next."""
+    for wrong in ("raise", "rows"):
+        st = _step(3, 1)
+
+        def inputs(i, mb):
+            if wrong == "raise" and mb == 1 and i == 2:
+                raise RuntimeError("no more rows")
+            cur = sim.current[-1]
+            return FakeTensor((T, H), cur, cur.work("X") if late else None), FakeTensor((T, D), cur)
+
+        def experts(g, mb):
+            return tuple(FakeTensor((T * K - (mb == 1), D), sim.current[-1]) for _ in range(4))
+
+        with pytest.raises((RuntimeError, ValueError)):
+            st.sketch(1, 3, inputs, expert_inputs=experts, late=late)
+        for ln in st.lanes:
+            assert ln["stream"].seen <= st.main.seen
+        assert st.callbacks is None or st.callbacks.seen <= st.main.seen
+        assert sim.current == [st.main]
