@@ -665,7 +665,8 @@ logra_status logra_ts_apply(const logra_matrix *m, const void *ws, size_t ws_byt
  *   HOST memory (logra_grad_table_bytes(n) bytes, 8-byte aligned) and fills
  *   *list; the caller copies the table to the device, puts that address
  *   (16-byte aligned) into list->table, and keeps both while the tensors
- *   stay where they are.
+ *   stay where they are: until every call that was given the list is over,
+ *   and as long as a graph captured from one may be replayed.
  * logra_grad_tensor: rows x cols elements at `data` (device) with row stride
  *   ld >= cols (one row: any ld >= cols); LOGRA_F32 or LOGRA_BF16, mixed in
  *   one list as wished; rows or cols 0 for an empty tensor (data may then be

@@ -538,6 +538,13 @@ def _call(where, dev, fn, *args):
         raise LograError(status, where)
 
 
+def _stream_object(dev, stream, handle):
+    """The stream of a call as torch's object."""
+    if stream is None:
+        return torch.cuda.current_stream(_gpu(dev))
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=_gpu(dev))
+
+
 def _workspace(where, dev, stream, handle, ws, nbytes):
     """(tensor, address, bytes). One made here comes from the stream the call
     runs on, so that its memory is not handed to other work while the call
@@ -549,9 +556,7 @@ def _workspace(where, dev, stream, handle, ws, nbytes):
         if stream is None:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(handle, device=device)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(_stream_object(dev, stream, handle)):
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return ws, ws.data_ptr(), nbytes
     if ws.get_device() != dev or not ws.is_contiguous():
@@ -591,7 +596,8 @@ class GradList:
     and logra_grad_clip read them through a device table that holds their
     addresses. The list keeps the tensors; they must stay where they are
     (gradients written in place every step, as Step's sketches are). Making
-    one copies the table to the GPU, so make it before a graph capture.
+    one copies the table to the GPU, so make it before a graph capture, and
+    keep it as long as a graph that was captured from its calls.
 
     tensors  float32 or bfloat16, on one GPU, contiguous of any shape or 2-D
              with unit column stride and a longer row stride; none may overlap
@@ -620,10 +626,18 @@ class GradList:
         _check(lib.logra_grad_list_pack(len(self.tensors), ctypes.cast(items, ctypes.POINTER(_GradTensor)), _ptr(host),
                                         _nbytes(host), ctypes.byref(self.desc)), "logra_grad_list_pack")
         self.table = host.to(self.device)
+        self.streams = {_current_stream(index)}     # whose work the table's memory waits for
         self.desc.table = self.table.data_ptr()
         self.ref = ctypes.byref(self.desc)
         self.elements = int(self.desc.elements)
         self.workspace_bytes = int(lib.logra_grad_workspace_bytes(self.ref))
+
+    def _used_on(self, dev, stream, handle):
+        """The table's memory goes to no other use before this stream's work
+        is over, whichever stream it comes from."""
+        if handle not in self.streams:
+            self.table.record_stream(_stream_object(dev, stream, handle))
+            self.streams.add(handle)
 
     @staticmethod
     def _rows_of(t):
@@ -644,6 +658,7 @@ def logra_grad_norm(grads: GradList, norm: torch.Tensor, ws: Optional[torch.Tens
     where = "logra_grad_norm"
     _one_float(where, norm)
     dev, handle = _enter(where, stream, (grads.table, norm))
+    grads._used_on(dev, stream, handle)
     ws, p, nb = _workspace(where, dev, stream, handle, ws, grads.workspace_bytes)
     _call(where, dev, load_library().logra_grad_norm, grads.ref, norm.data_ptr(), p, nb, handle)
 
@@ -657,6 +672,9 @@ def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: 
     _one_float(where, norm)
     _one_float(where, coef)
     dev, handle = _enter(where, stream, (grads.table, norm, coef, None if out is None else out.table))
+    grads._used_on(dev, stream, handle)
+    if out is not None:
+        out._used_on(dev, stream, handle)
     ws, p, nb = _workspace(where, dev, stream, handle, ws, grads.workspace_bytes)
     _call(where, dev, load_library().logra_grad_clip, grads.ref, None if out is None else out.ref, max_norm,
           norm.data_ptr(), coef.data_ptr(), p, nb, handle)
