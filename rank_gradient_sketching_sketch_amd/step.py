@@ -220,6 +220,7 @@ class Step:
                                 + self.expert_ws_bytes)
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.coef = torch.ones(1, dtype=torch.float32, device=dev)
+        self._captured = []         # (list, workspace) that graphs captured from `clip` read
         self._list_gradients()      # copies a table to the device, which a captured `clip` could not
 
     # ---- streams ---------------------------------------------------------
@@ -364,17 +365,29 @@ class Step:
         return [m.S for m in self.dense] + [g.S for g in self.groups] + self.grads
 
     def _list_gradients(self):
-        self._grad_list = B.GradList(self._gradients())
-        self._grad_ws = torch.empty(self._grad_list.workspace_bytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(self.main):      # where `clip` reads the table and the workspace
+            self._grad_list = B.GradList(self._gradients())
+            self._grad_ws = torch.empty(self._grad_list.workspace_bytes, dtype=torch.uint8, device=self.device)
 
     def clip(self, max_norm: float):
         """Clip the step's gradients by their global norm: every S (which
         holds the whole step after `sketch`) and the dense gradients given to
         Step, in place, before pass 1. Returns the device tensors (norm, coef)
-        without waiting for them; a norm that is not finite clips nothing."""
+        without waiting for them; a norm that is not finite clips nothing.
+
+        Captured in a graph, it clips the gradients of the capture at every
+        replay, also after another one has taken a gradient's place; the step
+        keeps what such a graph reads. After a replacement the first clip
+        lists the gradients anew, which a capture cannot: ValueError there."""
         listed, now = self._grad_list.tensors, self._gradients()
+        with torch.cuda.stream(self.main):
+            capturing = torch.cuda.is_current_stream_capturing()
         if len(listed) != len(now) or any(a is not b for a, b in zip(listed, now)):
+            if capturing:
+                raise ValueError("a gradient was replaced: clip once before the capture")
             self._list_gradients()      # a sketch or gradient was replaced since
+        if capturing and not any(kept[0] is self._grad_list for kept in self._captured):
+            self._captured.append((self._grad_list, self._grad_ws))
         B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)
         return self.norm, self.coef
 

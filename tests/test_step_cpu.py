@@ -1,6 +1,7 @@
 """The step scheduler's ordering, on the CPU: streams, events and the library's
 calls are stand-ins that record which work each stream has waited for."""
 import os
+import weakref
 from types import SimpleNamespace
 
 import pytest
@@ -171,3 +172,52 @@ def test_a_callback_that_fails_leaves_no_lane_unjoined(sim, late):
             assert ln["stream"].seen <= st.main.seen
         assert st.callbacks is None or st.callbacks.seen <= st.main.seen
         assert sim.current == [st.main]
+
+
+class FakeList:
+    """Stands for a gradient list: alive as long as somebody holds it."""
+
+    def __init__(self, tensors, device=None):
+        self.tensors, self.workspace_bytes = list(tensors), 0
+
+
+def test_list_that_a_graph_reads_outlives_a_replaced_gradient(sim, monkeypatch):
+    """A captured clip's table and workspace stay when a later clip lists
+    other gradients: the graph still reads them at every replay. Lists that no
+    graph reads go."""
+    monkeypatch.setattr(B, "GradList", FakeList)
+    seen = []
+    monkeypatch.setattr(B, "logra_grad_clip", lambda lst, *a, ws, stream: seen.append((weakref.ref(lst), weakref.ref(ws))))
+    mats = [Matrix(D, H, 0, torch.zeros(D, H), torch.zeros(D))]
+    st = Step(mats, R, T, B.LOGRA_F32, grads=[torch.zeros(7)])
+    sim.capturing = True
+    st.clip(1.0)
+    st.clip(1.0)
+    sim.capturing = False
+    for n in (5, 9, 11):
+        st.grads[0] = torch.zeros(n)
+        st.clip(1.0)
+    alive = [lst() is not None for lst, _ in seen]
+    assert alive == [True, True, False, False, True]
+    assert [ws() is not None for _, ws in seen] == alive
+    sim.capturing = True                # the last list too, from now on
+    st.clip(1.0)
+    sim.capturing = False
+    st.grads[0] = torch.zeros(3)
+    st.clip(1.0)
+    assert seen[-2][0]() is not None and seen[-1][0]() is not None
+
+
+def test_clip_that_would_list_anew_is_refused_in_a_capture(sim, monkeypatch):
+    """Listing copies a table to the GPU, which a capture cannot."""
+    monkeypatch.setattr(B, "GradList", FakeList)
+    monkeypatch.setattr(B, "logra_grad_clip", lambda *a, **kw: None)
+    st = Step([Matrix(D, H, 0, torch.zeros(D, H), torch.zeros(D))], R, T, B.LOGRA_F32, grads=[torch.zeros(7)])
+    st.grads[0] = torch.zeros(8)
+    sim.capturing = True
+    with pytest.raises(ValueError):
+        st.clip(1.0)
+    sim.capturing = False
+    st.clip(1.0)
+    sim.capturing = True
+    st.clip(1.0)
