@@ -594,8 +594,9 @@ def _rows(where, t, h=None, dtype=None):
 class GradList:
     """The gradients of a step, described to the library once: logra_grad_norm
     and logra_grad_clip read them through a device table that holds their
-    addresses. The list keeps the tensors; they must stay where they are
-    (gradients written in place every step, as Step's sketches are). Making
+    addresses. The list keeps the tensors and the memory they had when it was
+    made; they must stay there (gradients written in place every step, as
+    Step's sketches are; `describes` tells whether they did). Making
     one copies the table to the GPU, so make it before a graph capture, and
     keep it as long as a graph that was captured from its calls.
 
@@ -607,6 +608,8 @@ class GradList:
     def __init__(self, tensors, device=None):
         self.tensors = list(tensors)
         where = "GradList"
+        self._memory = [t.detach() for t in self.tensors]       # also if a tensor's storage is exchanged
+        self._described = [self._description(t) for t in self.tensors]
         self.device = self.tensors[0].device if self.tensors else torch.device(device or "cuda")
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -631,6 +634,16 @@ class GradList:
         self.ref = ctypes.byref(self.desc)
         self.elements = int(self.desc.elements)
         self.workspace_bytes = int(lib.logra_grad_workspace_bytes(self.ref))
+
+    @staticmethod
+    def _description(t):
+        return t.data_ptr(), t.shape, t.stride(), t.dtype
+
+    def describes(self, tensors) -> bool:
+        """Whether the list was made of these very tensors, and each still has
+        the memory, shape, strides and type it had then."""
+        return len(tensors) == len(self.tensors) and all(
+            a is b and self._description(b) == d for a, b, d in zip(self.tensors, tensors, self._described))
 
     def _used_on(self, dev, stream, handle):
         """The table's memory goes to no other use before this stream's work

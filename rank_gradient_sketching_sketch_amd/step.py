@@ -376,16 +376,15 @@ class Step:
         without waiting for them; a norm that is not finite clips nothing.
 
         Captured in a graph, it clips the gradients of the capture at every
-        replay, also after another one has taken a gradient's place; the step
-        keeps what such a graph reads. After a replacement the first clip
+        replay, also after another one (or another storage of the same one)
+        has taken a gradient's place; the step keeps what such a graph reads. After a replacement the first clip
         lists the gradients anew, which a capture cannot: ValueError there."""
-        listed, now = self._grad_list.tensors, self._gradients()
         with torch.cuda.stream(self.main):
             capturing = torch.cuda.is_current_stream_capturing()
-        if len(listed) != len(now) or any(a is not b for a, b in zip(listed, now)):
+        if not self._grad_list.describes(self._gradients()):    # a sketch or gradient was replaced since
             if capturing:
                 raise ValueError("a gradient was replaced: clip once before the capture")
-            self._list_gradients()      # a sketch or gradient was replaced since
+            self._list_gradients()
         if capturing and not any(kept[0] is self._grad_list for kept in self._captured):
             self._captured.append((self._grad_list, self._grad_ws))
         B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)

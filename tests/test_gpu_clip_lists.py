@@ -101,3 +101,41 @@ def test_graph_of_a_clip_whose_gradient_was_replaced():
         torch.cuda.synchronize()
         assert abs(norm.item() - n_ref) <= 2.0 ** -23 * n_ref
     assert all((t == 5.0).all() for s in spare for t in s.tensors)
+
+
+def test_step_whose_gradients_storage_is_exchanged():
+    """t.data = and set_ under the same object: the new memory is what is
+    clipped, the old one is left as it was."""
+    dev = device()
+    say("exchanged storage")
+    D, R, H = 40, 64, 96
+    g = torch.Generator().manual_seed(8)
+
+    def new(*shape):
+        return torch.randn(*shape, generator=g).to(dev)
+
+    mat, grad = Matrix(D, H, 7, torch.zeros(D, H, device=dev), torch.zeros(D, device=dev)), new(300)
+    st = Step([mat], R, 200, B.LOGRA_BF16, grads=[grad])
+
+    def check():
+        grads = [to_f64(mat.S), to_f64(grad)]
+        n_ref, _, out = ox.clip(grads, 0.5)
+        norm, _ = st.clip(0.5)
+        torch.cuda.synchronize()
+        assert abs(norm.item() - n_ref) <= 2.0 ** -23 * n_ref
+        for got, want in zip((mat.S, grad), out):
+            assert np.all(np.abs(to_f64(got) - want) <= 2.0 ** -22 * np.abs(want))
+
+    mat.S.copy_(new(D, R))
+    check()
+    for exchange in (lambda: setattr(grad, "data", new(300)), lambda: setattr(grad, "data", new(17, 20)),
+                     lambda: grad.set_(new(5)), lambda: mat.S.set_(new(D, R))):
+        old = (grad.detach(), mat.S.detach())
+        kept = [t.clone() for t in old]
+        exchange()
+        now = {grad.data_ptr(), mat.S.data_ptr()}
+        if mat.S.data_ptr() == old[1].data_ptr():
+            mat.S.copy_(new(D, R))
+        check()
+        for t, k in zip(old, kept):
+            assert t.data_ptr() in now or torch.equal(t, k)

@@ -1,6 +1,7 @@
 """The gradient list's device table and the streams that read it, on the CPU:
 the GPU's parts are stand-ins that record what they are asked for."""
 import os
+import weakref
 from types import SimpleNamespace
 
 import pytest
@@ -108,3 +109,38 @@ def test_table_is_kept_for_every_stream_that_reads_it(gpu, as_int):
     gpu.current = FakeStream(9)                 # no stream named, another one current than at the making
     B.logra_grad_norm(out, gpu.one())
     assert gpu.calls[-1] == ("norm", 9) and 9 in out.table.kept
+
+
+def test_memory_of_a_listed_tensor_lives_as_long_as_the_list(gpu):
+    """A gradient whose storage is exchanged under it (t.data, set_) leaves
+    the list's addresses in memory that the list still holds."""
+    made = []
+
+    class Counted(Gradient):
+        def detach(self):
+            made.append(Gradient(self.ptr, *self.shape))
+            return made[-1]
+
+    grads = B.GradList([Counted(0x100000, 3, 4), Counted(0x200000, 9)])
+    held = [weakref.ref(t) for t in made]
+    made.clear()
+    assert len(held) == 2 and all(t() is not None for t in held)
+    del grads
+    assert all(t() is None for t in held)
+
+
+def test_list_tells_whether_it_describes_its_tensors(gpu):
+    """An exchanged storage, another shape, stride or type under the same
+    object is another gradient."""
+    a, b = Gradient(0x100000, 3, 4), Gradient(0x200000, 9)
+    grads = B.GradList([a, b])
+    assert grads.describes([a, b])
+    assert not grads.describes([a]) and not grads.describes([b, a]) and not grads.describes([a, b, b])
+    assert not grads.describes([a, Gradient(0x200000, 9)])          # another object: its memory may go any time
+    for change in (dict(ptr=0x300000), dict(shape=torch.Size((3, 3))), dict(shape=torch.Size((12,))),
+                   dict(dtype=torch.bfloat16)):
+        c = Gradient(0x100000, 3, 4)
+        grads = B.GradList([c, b])
+        for k, v in change.items():
+            setattr(c, k, v)
+        assert not grads.describes([c, b])

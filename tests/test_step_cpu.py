@@ -78,7 +78,7 @@ def sim(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Event", FakeEvent)
     monkeypatch.setattr(torch.cuda, "stream", Use)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: s.capturing)
-    monkeypatch.setattr(B, "GradList", lambda tensors, device=None: SimpleNamespace(tensors=list(tensors), workspace_bytes=0))
+    monkeypatch.setattr(B, "GradList", FakeList)
 
     def reads(name, st, *tensors):
         for t in tensors:
@@ -180,6 +180,9 @@ class FakeList:
     def __init__(self, tensors, device=None):
         self.tensors, self.workspace_bytes = list(tensors), 0
 
+    def describes(self, tensors):
+        return len(tensors) == len(self.tensors) and all(a is b for a, b in zip(self.tensors, tensors))
+
 
 def test_list_that_a_graph_reads_outlives_a_replaced_gradient(sim, monkeypatch):
     """A captured clip's table and workspace stay when a later clip lists
@@ -221,3 +224,28 @@ def test_clip_that_would_list_anew_is_refused_in_a_capture(sim, monkeypatch):
     st.clip(1.0)
     sim.capturing = True
     st.clip(1.0)
+
+
+def test_clip_lists_anew_when_a_storage_was_exchanged(sim, monkeypatch):
+    """Same object, other memory: the list made before does not describe it."""
+    class List(FakeList):
+        def __init__(self, tensors, device=None):
+            super().__init__(tensors)
+            self.ptrs = [t.data_ptr() for t in self.tensors]
+
+        def describes(self, tensors):
+            return len(tensors) == len(self.ptrs) and all(
+                a is b and b.data_ptr() == p for a, b, p in zip(self.tensors, tensors, self.ptrs))
+
+    monkeypatch.setattr(B, "GradList", List)
+    seen = []
+    monkeypatch.setattr(B, "logra_grad_clip", lambda lst, *a, ws, stream: seen.append(lst.ptrs))
+    grad = torch.zeros(7)
+    st = Step([Matrix(D, H, 0, torch.zeros(D, H), torch.zeros(D))], R, T, B.LOGRA_F32, grads=[grad])
+    st.clip(1.0)
+    grad.data = torch.ones(7)
+    st.clip(1.0)
+    st.mats[0].S.set_(torch.zeros(D, R))
+    st.clip(1.0)
+    assert [p[1] for p in seen[1:]] == [grad.data_ptr()] * 2 and seen[0] != seen[1] != seen[2]
+    assert seen[2][0] == st.mats[0].S.data_ptr()
