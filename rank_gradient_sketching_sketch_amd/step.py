@@ -81,7 +81,7 @@ class ExpertGroup:
     """One projection of every expert of a layer: expert e's W[e] is d x k and
     its matrix id matrix_id + e. W (experts x d x k) and v (experts x d) are
     the caller's state (W updated in place; v read at the first step, then
-    members[e].v is expert e's, as for a Matrix); topk choices of an expert per token make
+    members[e].v is expert e's, as for a Matrix; members[e].S is S[e]); topk choices of an expert per token make
     tokens topk rows of dY per microbatch."""
     n_experts: int
     d: int
@@ -96,6 +96,7 @@ class ExpertGroup:
     ws: Optional[torch.Tensor] = None
     members: Optional[List[Matrix]] = None
     lane: int = 0
+    bound: int = 0      # address of the S that the members' are views of
 
 
 def _event(stream):
@@ -177,8 +178,7 @@ class Step:
                                                                 tokens * g.topk, act_dtype))
             g.ws = torch.empty(nb, dtype=torch.uint8, device=dev)
             self.expert_ws_bytes += nb
-            for m, S in zip(g.members, g.S):
-                m.S = S
+            self._bind(g)
         for i, m in enumerate(self.mats):
             if m.S is None or i < len(self.dense):
                 m.S = torch.empty(m.d, r, dtype=torch.float32, device=dev)
@@ -236,6 +236,24 @@ class Step:
             e = torch.cuda.Event()
             e.record(ln["stream"])
             self.main.wait_event(e)
+
+    def _bind(self, g):
+        if (tuple(g.S.shape) != (g.n_experts, g.d, self.r) or g.S.dtype is not torch.float32
+                or not g.S.is_contiguous() or g.S.device != g.W.device):
+            raise ValueError("expert group %s: contiguous float32 S, experts x d x r, expected" % g.name)
+        for m, S in zip(g.members, g.S):
+            m.S = S
+        g.bound = g.S.data_ptr()
+
+    def _members(self):
+        """The experts' S follow their group's, if another one (or other
+        memory) was put in its place."""
+        for g in self.groups:
+            at = g.S.data_ptr()
+            if at != g.bound or tuple(g.S.shape) != (g.n_experts, g.d, self.r):
+                self._bind(g)
+            elif any(m.S.data_ptr() != at + 4 * e * g.d * self.r for e, m in enumerate(g.members)):
+                raise ValueError("expert group %s: its members' S are views of the group's" % g.name)
 
     @contextlib.contextmanager
     def _late_inputs(self):
@@ -317,6 +335,7 @@ class Step:
             raise ValueError("probe: the microbatch must have one before it")
         if late is None:
             late = bool(self.groups)
+        self._members()
         self.set_step(step)
         self._fork()
         try:                # a callback may fail: what is enqueued by then is joined all the same
@@ -379,6 +398,7 @@ class Step:
         replay, also after another one (or another storage of the same one)
         has taken a gradient's place; the step keeps what such a graph reads. After a replacement the first clip
         lists the gradients anew, which a capture cannot: ValueError there."""
+        self._members()
         with torch.cuda.stream(self.main):
             capturing = torch.cuda.is_current_stream_capturing()
         if not self._grad_list.describes(self._gradients()):    # a sketch or gradient was replaced since
@@ -392,6 +412,7 @@ class Step:
 
     def pass1(self, beta2: float, eps: float):
         """v' and sqnorm of every matrix (v unchanged)."""
+        self._members()
         self._fork()
         for li, chunk, sq, bws in self.batches:
             ln = self.lanes[li]
@@ -416,6 +437,7 @@ class Step:
         keep W and v. Returns the number of matrices updated."""
         if len(scales) != len(self.mats):
             raise ValueError("one scale (or None) per matrix")
+        self._members()
         self._fork()
         done = 0
         for m, sc in zip(self.mats, scales):

@@ -249,3 +249,49 @@ def test_clip_lists_anew_when_a_storage_was_exchanged(sim, monkeypatch):
     st.clip(1.0)
     assert [p[1] for p in seen[1:]] == [grad.data_ptr()] * 2 and seen[0] != seen[1] != seen[2]
     assert seen[2][0] == st.mats[0].S.data_ptr()
+
+
+def test_members_sketches_are_the_groups(sim, monkeypatch):
+    """The experts' S are views of their group's: one put in its place (or its
+    storage exchanged) is what every phase uses; a member's alone is refused."""
+    monkeypatch.setattr(B, "logra_grad_clip", lambda *a, **kw: None)
+    used = []
+    monkeypatch.setattr(B, "logra_update_sqnorm_batch",
+                        lambda descs, code, S, *a: used.append([t.data_ptr() for t in S]))
+    monkeypatch.setattr(B, "logra_rowadam_apply", lambda desc, code, S, *a, **kw: used.append([S.data_ptr()]))
+    st = _step(0, 1, apply_lanes=1)
+    group = st.groups[0]
+
+    def phases():
+        _run(st, sim, False)
+        st.clip(1.0)
+        for phase in (lambda: st.pass1(0.9, 1e-8), lambda: st.pass2(1e-3, [1.0] * E, 1e-8)):
+            used.clear()
+            phase()
+            assert [p for call in used for p in call] == [group.S[e].data_ptr() for e in range(E)]
+
+    phases()
+    for other in (lambda: setattr(group, "S", torch.zeros(E, D, R)), lambda: group.S.set_(torch.zeros(E, D, R)),
+                  lambda: setattr(group.S, "data", torch.zeros(E, D, R))):
+        old = [m.S.data_ptr() for m in group.members]
+        other()
+        st.pass1(0.9, 1e-8)                 # whichever phase comes first
+        phases()
+        assert old != [m.S.data_ptr() for m in group.members]
+    good = group.S
+    for bad in (torch.zeros(E, D, R + 1), torch.zeros(E, D, R, dtype=torch.float64), torch.zeros(E, R, D).transpose(1, 2)):
+        group.S = bad
+        for phase in (lambda: _run(st, sim, False), lambda: st.clip(1.0), lambda: st.pass1(0.9, 1e-8),
+                      lambda: st.pass2(1e-3, [1.0] * E, 1e-8)):
+            with pytest.raises(ValueError):
+                phase()
+    group.S = good
+    phases()
+    mine = group.members[1].S
+    group.members[1].S = torch.zeros(D, R)
+    for phase in (lambda: _run(st, sim, False), lambda: st.clip(1.0), lambda: st.pass1(0.9, 1e-8),
+                  lambda: st.pass2(1e-3, [1.0] * E, 1e-8)):
+        with pytest.raises(ValueError):
+            phase()
+    group.members[1].S = mine
+    phases()
