@@ -44,7 +44,7 @@ from __future__ import annotations
 import contextlib
 import dataclasses
 import math
-from typing import Callable, List, Optional, Sequence, Tuple
+from typing import Callable, Dict, List, Optional, Sequence, Tuple
 
 import torch
 
@@ -80,9 +80,12 @@ class Matrix:
 class ExpertGroup:
     """One projection of every expert of a layer: expert e's W[e] is d x k and
     its matrix id matrix_id + e. W (experts x d x k) and v (experts x d) are
-    the caller's state (W updated in place; v read at the first step, then
-    members[e].v is expert e's, as for a Matrix; members[e].S is S[e]); topk choices of an expert per token make
-    tokens topk rows of dY per microbatch."""
+    the caller's state: W is updated in place, v is read by the first pass
+    that needs it, then members[e].v is expert e's (as for a Matrix, and for
+    every step that the group is given to). members[e].W and .S are W[e] and
+    S[e]. Another tensor, or other memory, in the place of W, v or S is what
+    the next phase uses. topk choices of an expert per token make tokens topk
+    rows of dY per microbatch."""
     n_experts: int
     d: int
     k: int
@@ -96,7 +99,33 @@ class ExpertGroup:
     ws: Optional[torch.Tensor] = None
     members: Optional[List[Matrix]] = None
     lane: int = 0
-    bound: int = 0      # address of the S that the members' are views of
+    # what the members' W, v and S were last taken from, and its address
+    taken: Dict[str, Tuple[torch.Tensor, int]] = dataclasses.field(default_factory=dict, repr=False)
+
+    def bind(self, r: int):
+        """The members, and what they hold taken from the group's W, v and S
+        where that is not what it was."""
+        if self.members is None:
+            self.members = [Matrix(self.d, self.k, self.matrix_id + e, None, None, "%s.%d" % (self.name, e))
+                            for e in range(self.n_experts)]
+        shapes = {"W": (self.n_experts, self.d, self.k), "v": (self.n_experts, self.d), "S": (self.n_experts, self.d, r)}
+        for what, shape in shapes.items():
+            t = getattr(self, what)
+            if t is None:
+                continue
+            had, at = self.taken.get(what, (None, 0))
+            if had is t and at == t.data_ptr() and tuple(t.shape) == shape:
+                if what == "S" and any(m.S.data_ptr() != at + 4 * e * self.d * r for e, m in enumerate(self.members)):
+                    raise ValueError("expert group %s: its members' S are views of the group's" % self.name)
+                continue
+            if tuple(t.shape) != shape:
+                raise ValueError("expert group %s: W experts x d x k, v experts x d and S experts x d x r expected"
+                                 % self.name)
+            if what == "S" and (t.dtype is not torch.float32 or not t.is_contiguous() or t.device != self.W.device):
+                raise ValueError("expert group %s: contiguous float32 S expected" % self.name)
+            for m, x in zip(self.members, t):
+                setattr(m, what, x)
+            self.taken[what] = (t, t.data_ptr())
 
 
 def _event(stream):
@@ -138,10 +167,8 @@ class Step:
         self.grads = list(grads)
         self.mats: List[Matrix] = list(matrices)
         for g in self.groups:
-            if tuple(g.W.shape) != (g.n_experts, g.d, g.k) or tuple(g.v.shape) != (g.n_experts, g.d):
-                raise ValueError("expert group %s: W experts x d x k and v experts x d expected" % g.name)
-            g.members = [Matrix(g.d, g.k, g.matrix_id + e, g.W[e], g.v[e], "%s.%d" % (g.name, e))
-                         for e in range(g.n_experts)]
+            g.S = None
+            g.bind(int(r))
             self.mats.extend(g.members)
         self.r, self.tokens, self.code, self.seed = int(r), int(tokens), int(act_dtype), int(seed)
         dev = torch.device(device) if device is not None else self.mats[0].W.device
@@ -178,7 +205,7 @@ class Step:
                                                                 tokens * g.topk, act_dtype))
             g.ws = torch.empty(nb, dtype=torch.uint8, device=dev)
             self.expert_ws_bytes += nb
-            self._bind(g)
+            g.bind(int(r))
         for i, m in enumerate(self.mats):
             if m.S is None or i < len(self.dense):
                 m.S = torch.empty(m.d, r, dtype=torch.float32, device=dev)
@@ -237,23 +264,10 @@ class Step:
             e.record(ln["stream"])
             self.main.wait_event(e)
 
-    def _bind(self, g):
-        if (tuple(g.S.shape) != (g.n_experts, g.d, self.r) or g.S.dtype is not torch.float32
-                or not g.S.is_contiguous() or g.S.device != g.W.device):
-            raise ValueError("expert group %s: contiguous float32 S, experts x d x r, expected" % g.name)
-        for m, S in zip(g.members, g.S):
-            m.S = S
-        g.bound = g.S.data_ptr()
-
     def _members(self):
-        """The experts' S follow their group's, if another one (or other
-        memory) was put in its place."""
+        """The experts' W, v and S are their groups'."""
         for g in self.groups:
-            at = g.S.data_ptr()
-            if at != g.bound or tuple(g.S.shape) != (g.n_experts, g.d, self.r):
-                self._bind(g)
-            elif any(m.S.data_ptr() != at + 4 * e * g.d * self.r for e, m in enumerate(g.members)):
-                raise ValueError("expert group %s: its members' S are views of the group's" % g.name)
+            g.bind(self.r)
 
     @contextlib.contextmanager
     def _late_inputs(self):

@@ -295,3 +295,34 @@ def test_members_sketches_are_the_groups(sim, monkeypatch):
             phase()
     group.members[1].S = mine
     phases()
+
+
+def test_second_step_of_a_group_goes_on_where_the_first_left(sim, monkeypatch):
+    """A group given to another Step keeps its experts' state: v is what the
+    last update left, not what the group was made with."""
+    monkeypatch.setattr(B, "logra_update_sqnorm_batch", lambda *a, **kw: None)
+    monkeypatch.setattr(B, "logra_rowadam_apply", lambda *a, **kw: None)
+    group = ExpertGroup(E, D, H, 100, K, torch.zeros(E, D, H), torch.zeros(E, D))
+    first = Step([], R, T, B.LOGRA_F32, groups=[group], apply_lanes=1)
+    first.set_step(1)
+    first.pass2(1e-3, [1.0, None, 1.0], 1e-8)
+    now = [m.v.data_ptr() for m in group.members]
+    assert now[0] != group.v[0].data_ptr() and now[1] == group.v[1].data_ptr()
+    second = Step([], R, 2 * T, B.LOGRA_F32, groups=[group], apply_lanes=1)
+    assert [m.v.data_ptr() for m in second.mats] == now
+    assert [m.W.data_ptr() for m in second.mats] == [group.W[e].data_ptr() for e in range(E)]
+    second.set_step(2)
+    for st in (first, second):
+        st.pass1(0.9, 1e-8)
+        assert [m.S.data_ptr() for m in st.mats] == [group.S[e].data_ptr() for e in range(E)]
+    # state put in the group's place, and other memory under it, is what the next phase uses
+    for what, new in (("v", lambda: setattr(group, "v", torch.ones(E, D))),
+                      ("v", lambda: setattr(group.v, "data", torch.ones(E, D))),
+                      ("W", lambda: setattr(group, "W", torch.ones(E, D, H))), ("W", lambda: group.W.set_(torch.ones(E, D, H)))):
+        new()
+        first.pass1(0.9, 1e-8)
+        for st in (first, second):
+            assert [getattr(m, what).data_ptr() for m in st.mats] == [getattr(group, what)[e].data_ptr() for e in range(E)]
+    group.v = torch.ones(E, D + 1)
+    with pytest.raises(ValueError):
+        first.pass1(0.9, 1e-8)
