@@ -524,7 +524,11 @@ def _enter(where, stream, tensors):
             raise LograError(1, where + ": tensors on one GPU expected")
     if stream is None:
         return dev, _current_stream(dev)
-    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not hasattr(stream, "cuda_stream"):
+        return dev, int(stream)
+    if getattr(stream, "device_index", dev) != dev:
+        raise LograError(1, where + ": stream of another GPU than the tensors'")
+    return dev, stream.cuda_stream
 
 
 def _call(where, dev, fn, *args):

@@ -144,3 +144,15 @@ def test_list_tells_whether_it_describes_its_tensors(gpu):
         for k, v in change.items():
             setattr(c, k, v)
         assert not grads.describes([c, b])
+
+
+def test_stream_of_another_gpu_is_refused(gpu):
+    """A kernel launched there would run beside its tensors' GPU."""
+    grads = _list()
+    for call in (lambda **kw: B.logra_grad_norm(grads, gpu.one(), **kw),
+                 lambda **kw: B.logra_grad_clip(grads, 1.0, gpu.one(), gpu.one(), **kw)):
+        with pytest.raises(B.LograError):
+            call(stream=FakeStream(7, device_index=1))
+        assert not gpu.calls
+        call(stream=FakeStream(7))
+        assert gpu.calls.pop()[1] == 7
