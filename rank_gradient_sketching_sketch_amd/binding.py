@@ -504,8 +504,15 @@ def logra_ts_apply(m: MatrixDesc, ws: torch.Tensor, W: torch.Tensor, lr: float, 
 # short tensors), so the checks read each property of a tensor once and pass
 # plain integers.
 
+# torch's own short cuts, where it has them
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _current_stream is None:
+    def _current_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
+if _current_device is None:
+    def _current_device():
+        return torch.cuda.current_device()
 
 
 @functools.lru_cache(maxsize=None)

@@ -156,3 +156,20 @@ def test_stream_of_another_gpu_is_refused(gpu):
         assert not gpu.calls
         call(stream=FakeStream(7))
         assert gpu.calls.pop()[1] == 7
+
+
+def test_streams_without_torchs_short_cuts(monkeypatch):
+    """The two private functions of torch are short cuts: where it has them no
+    more, the public ones say the same."""
+    import importlib
+    kept = {n: getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice")}
+    try:
+        for n in kept:
+            monkeypatch.delattr(torch._C, n, raising=False)
+        fresh = importlib.util.module_from_spec(importlib.util.find_spec(B.__name__))
+        fresh.__spec__.loader.exec_module(fresh)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: FakeStream(40 + torch.device("cuda", dev).index))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
+        assert fresh._current_stream(1) == 41 and fresh._current_device() == 2
+    finally:
+        monkeypatch.undo()
