@@ -704,7 +704,7 @@ def logra_grad_clip(grads: GradList, max_norm: float, norm: torch.Tensor, coef: 
           norm.data_ptr(), coef.data_ptr(), p, nb, handle)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=256)
 def logra_expert_sort_workspace_bytes(T: int, topk: int, n_experts: int) -> int:
     return int(load_library().logra_expert_sort_workspace_bytes(T, topk, n_experts))
 

@@ -173,3 +173,8 @@ def test_streams_without_torchs_short_cuts(monkeypatch):
         assert fresh._current_stream(1) == 41 and fresh._current_device() == 2
     finally:
         monkeypatch.undo()
+
+
+def test_size_cache_is_bounded(gpu):
+    """One size per token count would grow with every new sequence length."""
+    assert B.logra_expert_sort_workspace_bytes.cache_info().maxsize is not None
