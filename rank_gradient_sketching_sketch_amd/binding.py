@@ -619,8 +619,8 @@ class GradList:
     def __init__(self, tensors, device=None):
         self.tensors = list(tensors)
         where = "GradList"
-        self._memory = [t.detach() for t in self.tensors]       # also if a tensor's storage is exchanged
-        self._described = [self._description(t) for t in self.tensors]
+        self._memory = [t.untyped_storage() for t in self.tensors]      # also if a tensor's is exchanged
+        self._described = []
         self.device = self.tensors[0].device if self.tensors else torch.device(device or "cuda")
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -631,8 +631,10 @@ class GradList:
         for t in self.tensors:
             if t.get_device() != index:
                 raise LograError(1, where + ": tensors on one GPU expected")
-            rows, cols, ld = self._rows_of(t)
-            words += (t.data_ptr(), rows, cols, ld, _dtype_code(t))
+            d = self._description(t)
+            self._described.append(d)
+            rows, cols, ld = self._rows_of(t, d[1], d[2])
+            words += (d[0], rows, cols, ld, _dtype_code(t))
         items = (ctypes.c_int64 * max(1, len(words)))(*words)
         lib = load_library()
         host = torch.empty(max(8, int(lib.logra_grad_table_bytes(len(self.tensors)))), dtype=torch.uint8)
@@ -664,7 +666,9 @@ class GradList:
             self.streams.add(handle)
 
     @staticmethod
-    def _rows_of(t):
+    def _rows_of(t, shape, stride):
+        if len(shape) == 2 and stride[1] == 1 and shape[0] > 1:     # without gaps or with them
+            return shape[0], shape[1], stride[0]
         if t.is_contiguous():
             cols = t.size(-1) if t.dim() else 1
             return (t.numel() // cols if cols else 0), cols, cols
