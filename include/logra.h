@@ -653,7 +653,8 @@ logra_status logra_ts_apply(const logra_matrix *m, const void *ws, size_t ws_byt
  * gradients of what is not sketched.
  *     norm = sqrt(sum over tensors and elements of g^2)
  *     coef = max_norm / norm   where max_norm < norm < infinity, else 1
- *     out  = coef * g          (rounded once, to nearest even)
+ *     out  = coef * g          (coef and the product rounded to fp32, a bf16
+ *                              result then to bf16; to nearest even)
  * A norm that is not finite (some gradient is not) clips nothing: the caller
  * reads it and skips the step, as with a sqnorm that is not finite. Squares
  * and sums are fp64, so a finite gradient's norm neither overflows nor
@@ -791,7 +792,8 @@ logra_status logra_expert_combine_backward(int64_t T, int topk, int64_t h, int d
  *            keeps its S (accumulate != 0) or gets zeros.
  *   act_dtype LOGRA_BF16: bf16 products with fp32 accumulation; the
  *            projection is kept in fp32 and multiplied as three bf16 terms
- *            (within 2^-24 of it), so S is what fp32 products give, closer
+ *            (within 2^-24 of it where 2^-100 < |P| < 2^127; a larger P
+ *            counts as not finite), so S is what fp32 products give, closer
  *            than logra_sketch_accumulate's, which rounds the projection to
  *            bf16. r in
  *            {32, 64, 128, 256}; d, k, ldx, lddy multiples of 8; X, dY

@@ -38,7 +38,8 @@ constexpr int kGradSmallThreads = 1024;
 // take it 5.0 us, two launches of the others 9.1 us.
 constexpr int64_t kGradSmallChunks = 32, kGradSmallElements = 32768;
 // Elements above which loads and stores are marked as not to be kept in the
-// caches (fp32: the last-level cache's 256 MB).
+// caches: 256 MB of fp32, what the last-level cache holds. A count of bytes
+// would let bf16 lists of 128 to 256 MB be kept; that was not measured.
 constexpr int64_t kGradStream = 1ll << 26;
 
 // Tensors need only their element's alignment (global memory takes 16-byte

@@ -15,7 +15,8 @@
 // P is kept in fp32 and taken apart by the second product into three bf16
 // terms, P = p0 + p1 + p2 with p0 = bf16(P), p1 = bf16(P - p0),
 // p2 = bf16(P - p0 - p1): each rounding is 2^-8 of what it rounds, so their
-// sum is within 2^-24 of P and S has the precision of fp32 products although
+// sum is within 2^-24 of P (unless P is so small that a term is subnormal, or
+// rounds to infinity in bf16) and S has the precision of fp32 products although
 // dY^T P runs on the bf16 matrix cores (dY is bf16 exactly). One term would
 // leave 2^-8 per product, two 2^-16. Storing the terms instead of the value
 // would cost half as many bytes again on the path that bounds that product.
@@ -30,6 +31,8 @@
 // the last units' latency. The second product takes 42 us with even experts:
 // 20 us are S's 100 MB written, which comes on top of 22 us of matrix
 // instructions because workgroups that start together finish together.
+// That is with S overwritten; added to, it takes the call to 164 us, since
+// each row of S is loaded, waited for and stored before the next one.
 #include <math.h>
 
 #include <type_traits>

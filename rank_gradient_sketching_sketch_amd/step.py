@@ -79,7 +79,8 @@ class Matrix:
 @dataclasses.dataclass
 class ExpertGroup:
     """One projection of every expert of a layer: expert e's W[e] is d x k and
-    its matrix id matrix_id + e. W (experts x d x k) and v (experts x d) are
+    its matrix id matrix_id + e (matrices of one id share their signs, so give
+    every group its own n_experts ids). W (experts x d x k) and v (experts x d) are
     the caller's state: W is updated in place, v is read by the first pass
     that needs it, then members[e].v is expert e's (as for a Matrix, and for
     every step that the group is given to). members[e].W and .S are W[e] and
