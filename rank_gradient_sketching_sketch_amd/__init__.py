@@ -20,6 +20,8 @@ __all__ = [
     "logra_expert_sort_workspace_bytes", "logra_expert_sort", "logra_expert_gather",
     "logra_expert_combine", "logra_expert_combine_backward",
     "logra_sketch_experts_workspace_bytes", "logra_sketch_experts",
+    "logra_route", "logra_route_backward", "logra_fp8_quantize", "logra_fp8_matmul", "AdamWList", "logra_adamw",
+    "LOGRA_SOFTMAX", "LOGRA_SIGMOID",
     "LograError", "MatrixDesc", "library_path", "load_library",
 ]
 
@@ -27,5 +29,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = value = getattr(binding, name)     # later look-ups do not come here
+        return value
     raise AttributeError(name)

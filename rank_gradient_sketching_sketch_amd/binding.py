@@ -75,6 +75,20 @@ class _GradListDesc(ctypes.Structure):
                 ("shapes", ctypes.c_uint64), ("n", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _AdamWTensor(ctypes.Structure):
+    """logra_adamw_tensor: one tensor of an AdamW list."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_param", ctypes.c_int64),
+                ("ld_grad", ctypes.c_int64), ("ld_copy", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _AdamWListDesc(ctypes.Structure):
+    """logra_adamw_list: what pack says of a list, and its table's device address."""
+    _fields_ = [("table", ctypes.c_void_p), ("elements", ctypes.c_int64), ("blocks", ctypes.c_int64),
+                ("n", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class KLBudget(ctypes.Structure):
     """logra_kl_budget: KL budget annealed linearly from delta_start to
     delta_end over anneal_steps steps."""
@@ -186,6 +200,21 @@ def load_library():
     lib.logra_sketch_experts_workspace_bytes.argtypes = [D, i32, i64, i32]
     lib.logra_sketch_experts.restype = i32
     lib.logra_sketch_experts.argtypes = [D, i32, u64, i64, i32, P, P, i32, P, i64, i64, P, i64, P, i32, P, sz, P]
+    lib.logra_route.restype = i32
+    lib.logra_route.argtypes = [i64, i32, i32, i32, P, i64, i32, P, i32, i32, i32, i32, f32, P, P, P]
+    lib.logra_route_backward.restype = i32
+    lib.logra_route_backward.argtypes = [i64, i32, i32, i32, P, i64, i32, P, P, i32, f32, P, i64, P]
+    lib.logra_fp8_quantize.restype = i32
+    lib.logra_fp8_quantize.argtypes = [i64, i64, i64, i32, P, i64, i32, i32, P, i64, P, P]
+    lib.logra_fp8_matmul.restype = i32
+    lib.logra_fp8_matmul.argtypes = [i64, i64, i64, i32, P, P, i32, P, i64, i64, P, P, i64, P, i32, P, i64, P]
+    A = ctypes.POINTER(_AdamWListDesc)
+    lib.logra_adamw_table_bytes.restype = sz
+    lib.logra_adamw_table_bytes.argtypes = [i64]
+    lib.logra_adamw_list_pack.restype = i32
+    lib.logra_adamw_list_pack.argtypes = [i64, ctypes.POINTER(_AdamWTensor), P, sz, A]
+    lib.logra_adamw.restype = i32
+    lib.logra_adamw.argtypes = [A, i32, P, P, P, dbl, dbl, dbl, dbl, dbl, u64, P, dbl, u64, P]
     _lib = lib
     return lib
 
@@ -813,3 +842,254 @@ def logra_sketch_experts(m: MatrixDesc, offsets: torch.Tensor, X: torch.Tensor, 
     _call(where, dev, load_library().logra_sketch_experts, ctypes.byref(m), E, id_stride, N, code,
           offsets.data_ptr(), None if order is None else order.data_ptr(), topk, X.data_ptr(), ldx, rows,
           dY.data_ptr(), lddy, S.data_ptr(), 1 if accumulate else 0, p, nb, handle)
+
+
+# ---- routing, products in 8 bits, AdamW ----
+
+LOGRA_SOFTMAX = 0
+LOGRA_SIGMOID = 1
+
+
+def _choices(where, t, dtype, T, name):
+    """topk of a contiguous T x topk tensor."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != T or t.dtype is not dtype or not t.is_contiguous():
+        raise LograError(1, "%s: contiguous %s %s of %d tokens expected" % (where, dtype, name, T))
+    return shape[1]
+
+
+def logra_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                score: int = LOGRA_SOFTMAX, groups: int = 1, topk_groups: int = 1, group_best: int = 1,
+                renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """ids (T x topk int32) and weights (T x topk float32) of the experts that
+    the tokens of logits (T x n_experts, float32 or bfloat16) take: the topk
+    highest of score + bias, among the topk_groups best groups of experts
+    (score: LOGRA_SOFTMAX or LOGRA_SIGMOID; weights: scale times the scores
+    without the bias, over their sum if renormalize). -1 with weight 0 where no
+    expert is left, as in a row of -inf. The ids are what logra_expert_sort
+    takes, the weights what gather and combine take."""
+    where = "logra_route"
+    T, E, ld = _rows(where, logits)
+    K = _choices(where, ids, torch.int32, T, "ids")
+    if _choices(where, weights, torch.float32, T, "weights") != K:
+        raise LograError(1, where + ": weights of the ids' shape expected")
+    if bias is not None:
+        _want(where, bias, torch.float32, (E,))
+    dev, handle = _enter(where, stream, (logits, ids, weights, bias))
+    _call(where, dev, load_library().logra_route, T, E, K, _dtype_code(logits), logits.data_ptr(), ld, score,
+          None if bias is None else bias.data_ptr(), groups, topk_groups, group_best, 1 if renormalize else 0, scale,
+          ids.data_ptr(), weights.data_ptr(), handle)
+
+
+def logra_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, dlogits: torch.Tensor,
+                         score: int = LOGRA_SOFTMAX, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """dlogits (of the logits' shape and type) from the gradient of the
+    weights that logra_route gave, with the same score, renormalize and scale;
+    the ids are held."""
+    where = "logra_route_backward"
+    T, E, ld = _rows(where, logits)
+    T2, _, ldd = _rows(where, dlogits, E, logits.dtype)
+    if T2 != T:
+        raise LograError(1, where + ": dlogits of the logits' shape expected")
+    K = _choices(where, ids, torch.int32, T, "ids")
+    if _choices(where, dweights, torch.float32, T, "dweights") != K:
+        raise LograError(1, where + ": dweights of the ids' shape expected")
+    dev, handle = _enter(where, stream, (logits, ids, dweights, dlogits))
+    _call(where, dev, load_library().logra_route_backward, T, E, K, _dtype_code(logits), logits.data_ptr(), ld, score,
+          ids.data_ptr(), dweights.data_ptr(), 1 if renormalize else 0, scale, dlogits.data_ptr(), ldd, handle)
+
+
+def _arrays(where, t, dtype=None):
+    """(arrays, rows, columns, row stride) of a 2-D tensor of rows or of a 3-D
+    one whose arrays follow each other without gaps."""
+    if t.dim() == 2:
+        return (1,) + _rows(where, t, None, dtype)
+    if t.dim() != 3:
+        raise LograError(1, where + ": 2-D or 3-D tensors expected")
+    b, n, k = t.shape
+    if dtype is not None and t.dtype is not dtype:
+        raise LograError(1, "%s: %s tensor expected" % (where, dtype))
+    sb, ld, unit = t.stride()
+    if n == 1:                  # rows of one array each: what lies between them is the row stride
+        ld = sb if b > 1 else k
+    if t.numel() and ((unit != 1 and k > 1) or (b > 1 and sb != n * ld)):
+        raise LograError(1, where + ": arrays without gaps between them, with unit column stride, expected")
+    return b, n, k, ld
+
+
+def logra_fp8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
+                       transpose: bool = False, stream=None) -> None:
+    """float8_e4m3fn codes of x (rows x columns or arrays x rows x columns,
+    float32 or bfloat16) and a float32 scale for each 1 x 128 block (block_rows
+    1) or 128 x 128 block (block_rows 128): x is about codes times scales.
+    transpose (of 128 x 128 blocks): codes and scales of the transposed arrays.
+    scales: ([arrays x] blocks of rows x blocks of columns), contiguous."""
+    where = "logra_fp8_quantize"
+    b, n, k, ldx = _arrays(where, x)
+    b2, n2, k2, ldc = _arrays(where, codes, torch.float8_e4m3fn)
+    if x.dim() != codes.dim() or b2 != b or (n2, k2) != ((k, n) if transpose else (n, k)):
+        raise LograError(1, where + ": codes of x's shape (transposed: of its transpose) expected")
+    if block_rows not in (1, 128):
+        raise LograError(1, where + ": block_rows of 1 or 128 expected")
+    grid = (-(-n // block_rows), -(-k // 128))
+    if transpose:
+        grid = grid[::-1]
+    _want(where, scales, torch.float32, (b,) + grid if x.dim() == 3 else grid)
+    dev, handle = _enter(where, stream, (x, codes, scales))
+    _call(where, dev, load_library().logra_fp8_quantize, b, n, k, _dtype_code(x), x.data_ptr(), ldx, block_rows,
+          1 if transpose else 0, codes.data_ptr(), ldc, scales.data_ptr(), handle)
+
+
+def logra_fp8_matmul(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                     out: torch.Tensor, offsets: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                     topk: int = 1, stream=None) -> None:
+    """out = x w^T of codes and scales as logra_fp8_quantize writes them
+    (x: block_rows 1, w: block_rows 128), float32 or bfloat16. With offsets
+    (n_experts + 1, of logra_expert_sort) w is n_experts x n x k and rows
+    offsets[e] .. of out are expert e's, from the same rows of x or, with the
+    sort's order and topk, from the activations before the sort; the other rows
+    of out stay as they are."""
+    where = "logra_fp8_matmul"
+    rows, k, ldx = _rows(where, x, None, torch.float8_e4m3fn)
+    E, n, kw, ldw = _arrays(where, w, torch.float8_e4m3fn)
+    M, _, ldy = _rows(where, out, n)
+    if kw != k or w.dim() != (2 if offsets is None else 3):
+        raise LograError(1, where + ": w of n x k codes (with offsets: experts x n x k) expected")
+    kb = -(-k // 128)
+    _want(where, x_scales, torch.float32, (rows, kb))
+    _want(where, w_scales, torch.float32, (-(-n // 128), kb) if offsets is None else (E, -(-n // 128), kb))
+    if offsets is not None:
+        _want(where, offsets, torch.int32, (E + 1,))
+    if order is not None:
+        _want(where, order, torch.int32, (M,))
+    dev, handle = _enter(where, stream, (x, x_scales, w, w_scales, out, offsets, order))
+    _call(where, dev, load_library().logra_fp8_matmul, M, n, k, E, None if offsets is None else offsets.data_ptr(),
+          None if order is None else order.data_ptr(), topk, x.data_ptr(), ldx, rows, x_scales.data_ptr(),
+          w.data_ptr(), ldw, w_scales.data_ptr(), _dtype_code(out), out.data_ptr(), ldy, handle)
+
+
+class AdamWList:
+    """The tensors of an AdamW step and their moments, described to the library
+    once; logra_adamw reads them through a device table that holds their
+    addresses. The list keeps the tensors and the memory they had when it was
+    made, and they must stay there (`describes` tells whether they did). Making
+    one copies the table to the GPU, so make it before a graph capture, and keep
+    it as long as a graph that was captured from its calls.
+
+    params   float32 or bfloat16 tensors on one GPU, contiguous of any shape or
+             2-D with unit column stride and a longer row stride.
+    grads    their gradients, of the same shapes, float32 or bfloat16, written
+             in place every step.
+    copies   tensors of the same shapes that are given the new parameters too
+             (bfloat16 weights of float32 parameters), or None; an entry may
+             be None.
+    state_bits  32: exp_avg and exp_avg_sq hold the moments in float32. 8: as
+             float8_e4m3fn codes of m and of sqrt(v), in blocks of 256 elements
+             with `scales` (2 x blocks): a value is its code times its block's
+             scale.
+    state    (exp_avg, exp_avg_sq) or (exp_avg, exp_avg_sq, scales) to go on
+             from, as a list of the same shapes had them; default: zeros.
+    Tensor i's elements lie in the state from element 256 first[i] on."""
+
+    def __init__(self, params, grads, state_bits: int = 32, copies=None, state=None, device=None):
+        where = "AdamWList"
+        self.params, self.grads = list(params), list(grads)
+        self.copies = [None] * len(self.params) if copies is None else list(copies)
+        self.state_bits = int(state_bits)
+        if len(self.grads) != len(self.params) or len(self.copies) != len(self.params):
+            raise LograError(1, where + ": a gradient (and a copy or None) for every parameter expected")
+        if self.state_bits not in (8, 32):
+            raise LograError(2, where + ": state_bits of 8 or 32 expected")
+        self.device = self.params[0].device if self.params else torch.device(device or "cuda")
+        if self.device.type != "cuda":
+            raise LograError(1, where + ": tensors on one GPU expected")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        index = self.device.index
+        tensors = self._tensors(self.params, self.grads, self.copies)
+        self._memory = [t.untyped_storage() for t in tensors]       # also if a tensor's is exchanged
+        self._described = [GradList._description(t) for t in tensors]
+        items = (_AdamWTensor * max(1, len(self.params)))()
+        self.first, blocks = [], 0
+        for i, (p, g, c) in enumerate(zip(self.params, self.grads, self.copies)):
+            if g.shape != p.shape or (c is not None and c.shape != p.shape):
+                raise LograError(1, where + ": gradients and copies of their parameters' shapes expected")
+            for t in (p, g) if c is None else (p, g, c):
+                if t.get_device() != index:
+                    raise LograError(1, where + ": tensors on one GPU expected")
+            # rows that all of them have: two dimensions where one has gaps between its rows
+            shape = p.shape
+            flat = all(t.is_contiguous() for t in ((p, g) if c is None else (p, g, c)))
+            rows, cols = (1, p.numel()) if flat else (shape[0], shape[1]) if len(shape) == 2 else (0, 0)
+
+            def ld(t):
+                if flat:
+                    return cols
+                if len(shape) != 2 or (t.stride(1) != 1 and cols > 1):
+                    raise LograError(1, where + ": contiguous tensors, or 2-D ones with unit column stride, expected")
+                return t.stride(0) if rows > 1 else cols
+
+            items[i] = _AdamWTensor(p.data_ptr(), g.data_ptr(), None if c is None else c.data_ptr(), rows, cols, ld(p),
+                                    ld(g), 0 if c is None else ld(c), _dtype_code(p), _dtype_code(g),
+                                    LOGRA_F32 if c is None else _dtype_code(c), 0)
+            self.first.append(blocks)
+            blocks += -(-p.numel() // 256)
+        lib = load_library()
+        host = torch.empty(max(8, int(lib.logra_adamw_table_bytes(len(self.params)))), dtype=torch.uint8)
+        self.desc = _AdamWListDesc()
+        _check(lib.logra_adamw_list_pack(len(self.params), items, _ptr(host), _nbytes(host), ctypes.byref(self.desc)),
+               "logra_adamw_list_pack")
+        self.blocks, self.elements = int(self.desc.blocks), int(self.desc.elements)
+        small = self.state_bits == 8
+        dtype = torch.float8_e4m3fn if small else torch.float32
+        if state is None:
+            state = [torch.zeros(256 * self.blocks, dtype=torch.uint8 if small else dtype, device=self.device).view(dtype)
+                     for _ in range(2)]
+            if small:
+                state.append(torch.zeros(2, self.blocks, dtype=torch.float32, device=self.device))
+        if len(state) != (3 if small else 2):
+            raise LograError(1, where + ": state of exp_avg and exp_avg_sq (8 bits: and scales) expected")
+        self.exp_avg, self.exp_avg_sq = state[0], state[1]
+        self.scales = state[2] if small else None
+        for t in state[:2]:
+            _want(where, t, dtype, (256 * self.blocks,))
+        if small:
+            _want(where, self.scales, torch.float32, (2, self.blocks))
+        for t in state:
+            if t.get_device() != index:
+                raise LograError(1, where + ": state on the tensors' GPU expected")
+        self.table = host.to(self.device)
+        self.streams = {_current_stream(index)}     # whose work the table's memory waits for
+        self.desc.table = self.table.data_ptr()
+        self.ref = ctypes.byref(self.desc)
+
+    @staticmethod
+    def _tensors(params, grads, copies):
+        return list(params) + list(grads) + [c for c in copies if c is not None]
+
+    def describes(self, params, grads, copies=None) -> bool:
+        """Whether the list was made of these very tensors, and each still has
+        the memory, shape, strides and type it had then."""
+        copies = [None] * len(params) if copies is None else copies
+        now, then = self._tensors(params, grads, copies), self._tensors(self.params, self.grads, self.copies)
+        return len(now) == len(then) and all(
+            a is b and GradList._description(b) == d for a, b, d in zip(then, now, self._described))
+
+    _used_on = GradList._used_on
+
+
+def logra_adamw(tensors: AdamWList, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float, step: int,
+                norm: Optional[torch.Tensor] = None, max_norm: float = float("inf"), seed: int = 0, stream=None) -> None:
+    """One AdamW step over the list's tensors, in place: parameters, copies and
+    moments. step counts from 1. norm (of logra_grad_norm): gradients are taken
+    times max_norm / norm where norm is above max_norm; a norm that is not
+    finite leaves everything as it is. seed keys the rounding of 8-bit moments."""
+    where = "logra_adamw"
+    if norm is not None:
+        _one_float(where, norm)
+    m, v, s = tensors.exp_avg, tensors.exp_avg_sq, tensors.scales
+    dev, handle = _enter(where, stream, (tensors.table, norm, m, v, s))
+    tensors._used_on(dev, stream, handle)
+    _call(where, dev, load_library().logra_adamw, tensors.ref, tensors.state_bits, m.data_ptr(), v.data_ptr(),
+          None if s is None else s.data_ptr(), lr, beta1, beta2, eps, weight_decay, step,
+          None if norm is None else norm.data_ptr(), max_norm, seed, handle)

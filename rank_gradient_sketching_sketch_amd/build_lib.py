@@ -33,6 +33,7 @@ COMMON_FLAGS = [
 # single-mode folds ran about 3 % faster (the pair-mode instances, which ran
 # slower with it, are in fold_pair_bf16.hip).
 FILE_FLAGS = {
+    "fp8_matmul.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fold_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 

@@ -908,4 +908,264 @@ logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t
     return from_hip(launch_expert_sketch(a, bf16 ? 1 : 0, static_cast<hipStream_t>(stream)));
 }
 
+// ---- routing ----
+
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == LOGRA_F32 || dtype == LOGRA_BF16; }
+
+// What routing and its gradient have in common.
+logra_status check_route(int64_t T, int n_experts, int topk, int dtype, int score, const void *logits, int64_t ld,
+                         const int32_t *ids, const float *w) {
+    if (T < 0 || n_experts < 1 || topk < 1 || topk > n_experts) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (score != LOGRA_SOFTMAX && score != LOGRA_SIGMOID) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!dtype_ok(dtype) || n_experts > kMaxExperts || topk > kMaxTopK || T > kMaxExpertTokens || ld > (1ll << 40))
+        return LOGRA_ERR_UNSUPPORTED;
+    if (!rows_ok(logits, ld, T, n_experts, dtype)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!ids || !aligned_to(ids, 4) || !w || !aligned_to(w, 4))) return LOGRA_ERR_INVALID_ARGUMENT;
+    return LOGRA_OK;
+}
+
+void route_call(RouteCall &c, int64_t T, int n_experts, int topk, int dtype, int score, const void *logits, int64_t ld,
+                int renormalize, float scale) {
+    c.logits = logits;
+    c.ld = ld;
+    c.T = T;
+    c.bf16 = dtype == LOGRA_BF16;
+    c.E = n_experts;
+    c.K = topk;
+    c.sigmoid = score == LOGRA_SIGMOID;
+    c.renorm = renormalize != 0;
+    c.scale = scale;
+}
+
+}  // namespace
+
+logra_status logra_route(int64_t T, int n_experts, int topk, int dtype, const void *logits, int64_t ld, int score,
+                         const float *bias, int groups, int topk_groups, int group_best, int renormalize, float scale,
+                         int32_t *ids, float *weights, void *stream) {
+    const logra_status e = check_route(T, n_experts, topk, dtype, score, logits, ld, ids, weights);
+    if (e != LOGRA_OK) return e;
+    if (!aligned_to(bias, 4) || groups < 1 || n_experts % groups || topk_groups < 1 || topk_groups > groups ||
+        (group_best != 1 && group_best != 2))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (groups > kMaxRouteGroups) return LOGRA_ERR_UNSUPPORTED;
+    if (T == 0) return LOGRA_OK;
+    RouteCall c;
+    route_call(c, T, n_experts, topk, dtype, score, logits, ld, renormalize, scale);
+    c.bias = bias;
+    c.groups = groups;
+    c.kept = topk_groups;
+    c.best = group_best;
+    c.ids = ids;
+    c.weights = weights;
+    return from_hip(launch_route(c, static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_route_backward(int64_t T, int n_experts, int topk, int dtype, const void *logits, int64_t ld,
+                                  int score, const int32_t *ids, const float *dweights, int renormalize, float scale,
+                                  void *dlogits, int64_t ldd, void *stream) {
+    const logra_status e = check_route(T, n_experts, topk, dtype, score, logits, ld, ids, dweights);
+    if (e != LOGRA_OK) return e;
+    if (!rows_ok(dlogits, ldd, T, n_experts, dtype)) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (ldd > (1ll << 40)) return LOGRA_ERR_UNSUPPORTED;
+    if (T == 0) return LOGRA_OK;
+    RouteCall c;
+    route_call(c, T, n_experts, topk, dtype, score, logits, ld, renormalize, scale);
+    c.ids = const_cast<int32_t *>(ids);
+    return from_hip(launch_route_backward(c, dweights, dlogits, ldd, static_cast<hipStream_t>(stream)));
+}
+
+// ---- products in 8 bits ----
+
+logra_status logra_fp8_quantize(int64_t batch, int64_t rows, int64_t cols, int dtype, const void *x, int64_t ldx,
+                                int block_rows, int transpose, void *codes, int64_t ldc, float *scales,
+                                void *stream) {
+    if (batch < 0 || rows < 0 || cols < 0 || (block_rows != 1 && block_rows != 128) || (transpose && block_rows == 1))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!dtype_ok(dtype)) return LOGRA_ERR_UNSUPPORTED;
+    if (batch == 0 || rows == 0 || cols == 0) return LOGRA_OK;
+    constexpr int64_t kMost = 1ll << 40;
+    if (batch > kMost || rows > kMost || cols > (1ll << 30) || ldx > kMost / rows || ldc > kMost / rows ||
+        ldc > kMost / cols || batch > kMost / rows)
+        return LOGRA_ERR_UNSUPPORTED;
+    if (!x || ldx < cols || !aligned_to(x, elem_bytes(dtype)) || !codes || ldc < (transpose ? rows : cols) || !scales ||
+        !aligned_to(scales, 4))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    // a launch has fewer than 2^32 threads: 16 of them a row's block, 256 a block of 128 rows
+    const int64_t kb = (cols + 127) / 128;
+    const int64_t blocks = block_rows == 1 ? batch * rows / 16 + 1 : batch * ((rows + 127) / 128);
+    if (blocks >= (1ll << 24) / kb) return LOGRA_ERR_UNSUPPORTED;
+    QuantizeCall c;
+    c.batch = batch;
+    c.rows = rows;
+    c.cols = cols;
+    c.x = x;
+    c.ldx = ldx;
+    c.bf16 = dtype == LOGRA_BF16;
+    c.block_rows = block_rows;
+    c.turned = transpose != 0;
+    c.codes = static_cast<uint8_t *>(codes);
+    c.ldc = ldc;
+    c.scales = scales;
+    return from_hip(launch_fp8_quantize(c, static_cast<hipStream_t>(stream)));
+}
+
+logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, const int32_t *offsets,
+                              const int32_t *order, int topk, const void *x, int64_t ldx, int64_t x_rows,
+                              const float *x_scales, const void *w, int64_t ldw, const float *w_scales, int y_dtype,
+                              void *y, int64_t ldy, void *stream) {
+    if (M < 0 || n < 1 || k < 1 || n_experts < 1 || x_rows < 0 || (!offsets && n_experts != 1))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (order ? !offsets || topk < 1 || !aligned_to(order, 4) : x_rows < M) return LOGRA_ERR_INVALID_ARGUMENT;
+    if (!dtype_ok(y_dtype) || n_experts > kMaxExperts || M > kMaxPairs || n > kMaxExpertDim || k > kMaxExpertDim || k % 16)
+        return LOGRA_ERR_UNSUPPORTED;
+    if (M == 0) return LOGRA_OK;
+    if (!aligned_to(offsets, 4) || !w || !aligned16(w) || ldw < k || ldw % 16 || !w_scales || !aligned_to(w_scales, 4) ||
+        !y || ldy < n || !aligned_to(y, elem_bytes(y_dtype)))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (x_rows > 0 && (!x || !aligned16(x) || ldx < k || ldx % 16 || !x_scales || !aligned_to(x_scales, 4)))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    // rows are read at 32-bit offsets: from a tile's first one, or all of x where the order picks them
+    if (ldx > kMaxExpertDim || ldw > kMaxExpertDim || ldy > (1ll << 40) || (order && x_rows > ((1ll << 31) - 1) / ldx))
+        return LOGRA_ERR_UNSUPPORTED;
+    if (!fp8_matmul_fits(M, n, offsets ? n_experts : 0)) return LOGRA_ERR_UNSUPPORTED;
+    MatmulCall c;
+    c.M = M;
+    c.N = static_cast<int>(n);
+    c.K = static_cast<int>(k);
+    c.E = n_experts;
+    c.topk = order ? topk : 1;
+    c.offsets = offsets;
+    c.order = order;
+    c.x = static_cast<const uint8_t *>(x);
+    c.w = static_cast<const uint8_t *>(w);
+    c.ldx = ldx;
+    c.x_rows = x_rows;
+    c.ldw = ldw;
+    c.xs = x_scales;
+    c.ws = w_scales;
+    c.y = y;
+    c.ldy = ldy;
+    c.y_bf16 = y_dtype == LOGRA_BF16;
+    return from_hip(launch_fp8_matmul(c, static_cast<hipStream_t>(stream)));
+}
+
+// ---- AdamW over many tensors ----
+
+namespace {
+
+// The matrix id whose counter stream rounds the 8-bit moments; no sketched
+// matrix should have it.
+constexpr uint64_t kAdamId = 0xFFFFFFFFFFFFFFFFull;
+
+bool adam_array(const void *p, int64_t rows, int64_t cols, int64_t ld, int dtype, uint64_t *end) {
+    const int64_t el = elem_bytes(dtype);
+    if (!p || ld < cols || !aligned_to(p, el)) return false;
+    *end = reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(((rows - 1) * ld + cols) * el);
+    return true;
+}
+
+}  // namespace
+
+size_t logra_adamw_table_bytes(int64_t n) {
+    return n < 0 || n > (1 << 20) ? 0 : static_cast<size_t>(n) * sizeof(AdamEntry);
+}
+
+logra_status logra_adamw_list_pack(int64_t n, const logra_adamw_tensor *tensors, void *table_host, size_t table_bytes,
+                                   logra_adamw_list *list) {
+    if (n < 0 || n > (1 << 20) || !list || (n > 0 && (!tensors || !table_host)) || !aligned_to(table_host, 8))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (table_bytes < logra_adamw_table_bytes(n)) return LOGRA_ERR_WORKSPACE;
+    constexpr int64_t kMost = 1ll << 40;
+    // the address ranges, in the table's memory before the table takes it
+    static_assert(3 * sizeof(GradSpan) <= sizeof(AdamEntry), "three ranges for an entry");
+    GradSpan *span = static_cast<GradSpan *>(table_host);
+    int64_t n_span = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const logra_adamw_tensor &t = tensors[i];
+        if (t.rows < 0 || t.cols < 0) return LOGRA_ERR_INVALID_ARGUMENT;
+        if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || !dtype_ok(t.copy_dtype)) return LOGRA_ERR_UNSUPPORTED;
+        if (t.rows == 0 || t.cols == 0) continue;
+        if (t.rows > kMost || t.cols > kMost || t.rows > kMost / t.cols) return LOGRA_ERR_UNSUPPORTED;
+        const struct {
+            const void *p;
+            int64_t ld;
+            int dtype;
+        } arrays[] = {{t.param, t.ld_param, t.param_dtype}, {t.grad, t.ld_grad, t.grad_dtype}, {t.copy, t.ld_copy, t.copy_dtype}};
+        for (int a = 0; a < 3; ++a) {
+            if (a == 2 && !t.copy) continue;
+            if (arrays[a].ld > kMost / t.rows) return LOGRA_ERR_UNSUPPORTED;
+            uint64_t end = 0;
+            if (!adam_array(arrays[a].p, t.rows, t.cols, arrays[a].ld, arrays[a].dtype, &end)) return LOGRA_ERR_INVALID_ARGUMENT;
+            span[n_span++] = GradSpan{reinterpret_cast<uint64_t>(arrays[a].p), end};
+        }
+    }
+    std::sort(span, span + n_span);
+    for (int64_t i = 1; i < n_span; ++i)
+        if (span[i].begin < span[i - 1].end) return LOGRA_ERR_INVALID_ARGUMENT;
+    AdamEntry *table = static_cast<AdamEntry *>(table_host);
+    logra_adamw_list out = {};
+    for (int64_t i = 0; i < n; ++i) {
+        const logra_adamw_tensor &t = tensors[i];
+        AdamEntry e;
+        e.param = reinterpret_cast<uint64_t>(t.param);
+        e.grad = reinterpret_cast<uint64_t>(t.grad);
+        e.copy = reinterpret_cast<uint64_t>(t.copy);
+        e.rows = t.rows;
+        e.cols = t.cols;
+        e.ld_param = t.rows == 1 ? t.cols : t.ld_param;
+        e.ld_grad = t.rows == 1 ? t.cols : t.ld_grad;
+        e.ld_copy = t.rows == 1 ? t.cols : t.ld_copy;
+        e.first = out.blocks;
+        e.blocks = (t.rows * t.cols + kAdamBlock - 1) / kAdamBlock;
+        e.param_bf16 = t.param_dtype == LOGRA_BF16;
+        e.grad_bf16 = t.grad_dtype == LOGRA_BF16;
+        e.copy_bf16 = t.copy_dtype == LOGRA_BF16;
+        out.blocks += e.blocks;
+        out.elements += t.rows * t.cols;
+        if (out.elements > (kMost << 4)) return LOGRA_ERR_UNSUPPORTED;
+        table[i] = e;
+    }
+    out.n = static_cast<int32_t>(n);
+    *list = out;
+    return LOGRA_OK;
+}
+
+logra_status logra_adamw(const logra_adamw_list *list, int state_bits, void *exp_avg, void *exp_avg_sq, float *scales,
+                         double lr, double beta1, double beta2, double eps, double weight_decay, uint64_t step,
+                         const float *norm, double max_norm, uint64_t seed, void *stream) {
+    if (!list || list->n < 0 || list->blocks < 0 || (list->n > 0 && (!list->table || !aligned16(list->table))))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (state_bits != 8 && state_bits != 32) return LOGRA_ERR_UNSUPPORTED;
+    if (!isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
+        !isfinite(eps) || !isfinite(weight_decay) || step < 1 || !aligned_to(norm, 4) || !(max_norm >= 0.0))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    if (list->blocks == 0) return LOGRA_OK;
+    if (!exp_avg || !aligned16(exp_avg) || !exp_avg_sq || !aligned16(exp_avg_sq) || exp_avg == exp_avg_sq ||
+        (state_bits == 8 && (!scales || !aligned_to(scales, 4))))
+        return LOGRA_ERR_INVALID_ARGUMENT;
+    AdamCall c;
+    c.table = static_cast<const AdamEntry *>(list->table);
+    c.n = list->n;
+    c.blocks = list->blocks;
+    c.m = exp_avg;
+    c.v = exp_avg_sq;
+    c.scales = scales;
+    c.norm = norm;
+    c.max_norm = max_norm;
+    c.beta1 = static_cast<float>(beta1);
+    c.rest1 = static_cast<float>(1.0 - beta1);
+    c.beta2 = static_cast<float>(beta2);
+    c.rest2 = static_cast<float>(1.0 - beta2);
+    // 1 - beta^t without the cancellation of a beta near 1 (beta 0: 1)
+    const auto past = [&](double beta) { return beta > 0.0 ? -expm1(static_cast<double>(step) * log(beta)) : 1.0; };
+    c.decay = static_cast<float>(lr * weight_decay);
+    c.rate = static_cast<float>(lr / past(beta1));
+    c.root_scale = static_cast<float>(1.0 / sqrt(past(beta2)));
+    c.eps = static_cast<float>(eps);
+    c.key = stream_key(seed, step, kAdamId);
+    return from_hip(launch_adamw(c, state_bits, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

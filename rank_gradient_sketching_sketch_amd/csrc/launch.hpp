@@ -266,4 +266,73 @@ struct ExpertSketchArgs {
 };
 hipError_t launch_expert_sketch(const ExpertSketchArgs &a, int bf16, hipStream_t st);
 
+// Routing (logits of T tokens and E experts to ids and weights) and its
+// gradient (which reads ids).
+constexpr int kMaxRouteGroups = 64;
+struct RouteCall {
+    const void *logits = nullptr;
+    int64_t ld = 0, T = 0;
+    int bf16 = 0;
+    const float *bias = nullptr;      // may be null
+    int E = 0, K = 0, sigmoid = 0, groups = 1, kept = 1, best = 1, renorm = 0;
+    float scale = 1.f;
+    int32_t *ids = nullptr;
+    float *weights = nullptr;
+};
+hipError_t launch_route(const RouteCall &c, hipStream_t st);
+hipError_t launch_route_backward(const RouteCall &c, const float *dw, void *dx, int64_t lddx, hipStream_t st);
+
+// e4m3 codes and a scale per block of block_rows (1 or 128) x 128 elements of
+// `batch` arrays of rows x cols.
+struct QuantizeCall {
+    int64_t batch = 1, rows = 0, cols = 0;
+    const void *x = nullptr;
+    int64_t ldx = 0;
+    int bf16 = 0, block_rows = 1, turned = 0;
+    uint8_t *codes = nullptr;
+    int64_t ldc = 0;
+    float *scales = nullptr;
+};
+hipError_t launch_fp8_quantize(const QuantizeCall &c, hipStream_t st);
+
+// Y (M x N) = X W^T of such codes; offsets null: one expert with all rows.
+struct MatmulCall {
+    int64_t M = 0;
+    int N = 0, K = 0, E = 1, topk = 1;
+    const int32_t *offsets = nullptr, *order = nullptr;
+    const uint8_t *x = nullptr, *w = nullptr;
+    int64_t ldx = 0, x_rows = 0, ldw = 0;
+    const float *xs = nullptr, *ws = nullptr;
+    void *y = nullptr;
+    int64_t ldy = 0;
+    int y_bf16 = 0;
+};
+hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st);
+// Whether one launch covers Y (E: 0 for a dense product).
+bool fp8_matmul_fits(int64_t M, int64_t N, int E);
+
+// One AdamW step over a list of tensors whose moments lie in blocks of
+// kAdamBlock elements, every tensor beginning a block.
+constexpr int kAdamBlock = 256;
+struct AdamEntry {
+    uint64_t param = 0, grad = 0, copy = 0;     // copy: 0 for none
+    int64_t rows = 0, cols = 0, ld_param = 0, ld_grad = 0, ld_copy = 0;
+    int64_t first = 0, blocks = 0;              // the tensor's blocks in the list
+    int32_t param_bf16 = 0, grad_bf16 = 0, copy_bf16 = 0, reserved = 0;
+};
+struct AdamCall {
+    const AdamEntry *table = nullptr;
+    int n = 0;
+    int64_t blocks = 0;
+    void *m = nullptr, *v = nullptr;            // fp32, or codes of m and sqrt(v)
+    float *scales = nullptr;                    // 8 bits: of m, then of sqrt(v)
+    const float *norm = nullptr;                // may be null
+    double max_norm = 0.0;
+    float beta1 = 0.f, rest1 = 0.f, beta2 = 0.f, rest2 = 0.f;   // rest: 1 - beta
+    float decay = 0.f, rate = 0.f;              // lr weight_decay, lr / (1 - beta1^t)
+    float root_scale = 0.f, eps = 0.f;          // 1 / sqrt(1 - beta2^t)
+    uint64_t key = 0;
+};
+hipError_t launch_adamw(const AdamCall &c, int bits, hipStream_t st);
+
 }  // namespace logra

@@ -1,0 +1,445 @@
+// Routing: the experts that every token takes, their weights, and the
+// weights' gradient carried back to the logits. What stands before the sort of
+// experts.hip, and behind combine's gradient.
+//
+// For a token's logits x and the experts' biases b (balance; not part of the
+// weights):
+//   s_e = softmax(x)_e or 1 / (1 + exp(-x_e)),   key_e = s_e + b_e,
+//   groups of E / G neighbouring experts: only the topk_groups whose best one
+//   or two keys sum highest are left,
+//   id_j = the j-th highest key left (ties: the lower index),
+//   w_j  = c s_(id_j), divided by the sum of the chosen s where renormalised.
+// An expert whose key is -inf or NaN is never chosen; a choice that finds
+// none is -1 with weight 0, which the sort drops.
+//
+// Choices are whole numbers that must not hang on rounding: keys are formed
+// and compared in fp64, or where no bias and no sum of two keys enters, the
+// logits themselves are compared, which sort like their scores. Weights are
+// fp32, as ratios of exponentials of differences that cannot overflow or all
+// vanish.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace logra {
+
+constexpr int kRouteThreads = 256, kRouteTokens = kRouteThreads / 64;
+
+template <int BF16>
+__device__ __forceinline__ float route_logit(const void *x, int64_t at) {
+    if (BF16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(x)[at]) << 16);
+    return static_cast<const float *>(x)[at];
+}
+
+// A step of a reduction towards lane 63: lane L gets lane L - n's value (rows
+// of 16 lanes), then the rows' last lanes are carried on. Lanes without a
+// source keep `old`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t old, uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(old), static_cast<int>(v), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double old, double v) {
+    const uint64_t o = __builtin_bit_cast(uint64_t, old), w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp_u32<CTRL, ROWS>(static_cast<uint32_t>(o), static_cast<uint32_t>(w));
+    const uint32_t hi = dpp_u32<CTRL, ROWS>(static_cast<uint32_t>(o >> 32), static_cast<uint32_t>(w >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_f32(float old, float v) {
+    return __uint_as_float(dpp_u32<CTRL, ROWS>(__float_as_uint(old), __float_as_uint(v)));
+}
+
+__device__ __forceinline__ uint32_t lane_u32(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ float lane_f32(float v, int lane) { return __uint_as_float(lane_u32(__float_as_uint(v), lane)); }
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = lane_u32(static_cast<uint32_t>(w), lane), hi = lane_u32(static_cast<uint32_t>(w >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Reductions over the wave, the same in every lane.
+__device__ __forceinline__ float wave_max_f32(float v) {
+    v = fmaxf(v, dpp_f32<0x111, 0xF>(v, v));
+    v = fmaxf(v, dpp_f32<0x112, 0xF>(v, v));
+    v = fmaxf(v, dpp_f32<0x114, 0xF>(v, v));
+    v = fmaxf(v, dpp_f32<0x118, 0xF>(v, v));
+    v = fmaxf(v, dpp_f32<0x142, 0xA>(v, v));
+    v = fmaxf(v, dpp_f32<0x143, 0xC>(v, v));
+    return lane_f32(v, 63);
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+    v += dpp_f32<0x111, 0xF>(0.f, v);
+    v += dpp_f32<0x112, 0xF>(0.f, v);
+    v += dpp_f32<0x114, 0xF>(0.f, v);
+    v += dpp_f32<0x118, 0xF>(0.f, v);
+    v += dpp_f32<0x142, 0xA>(0.f, v);
+    v += dpp_f32<0x143, 0xC>(0.f, v);
+    return lane_f32(v, 63);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v += dpp_f64<0x111, 0xF>(0.0, v);
+    v += dpp_f64<0x112, 0xF>(0.0, v);
+    v += dpp_f64<0x114, 0xF>(0.0, v);
+    v += dpp_f64<0x118, 0xF>(0.0, v);
+    v += dpp_f64<0x142, 0xA>(0.0, v);
+    v += dpp_f64<0x143, 0xC>(0.0, v);
+    return lane_f64(v, 63);
+}
+
+// The two kinds of keys. Logits as whole numbers that sort like them (0: not
+// to be chosen; both zeros of the logits are one key), and fp64 keys (-inf:
+// not to be chosen).
+struct LogitKey {
+    using Key = uint32_t;
+    static __device__ __forceinline__ Key none() { return 0u; }
+    static __device__ __forceinline__ Key of(float x) {
+        const uint32_t b = __float_as_uint(x + 0.f);
+        return x > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
+    }
+    static __device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
+    static __device__ __forceinline__ Key smaller(Key a, Key b) { return a > b ? b : a; }
+    static __device__ __forceinline__ Key lane(Key v, int l) { return lane_u32(v, l); }
+    static __device__ __forceinline__ Key other(Key v, int o) {
+        return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o));
+    }
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ Key step(Key v) { return larger(v, dpp_u32<CTRL, ROWS>(v, v)); }
+};
+struct ScoreKey {
+    using Key = double;
+    static __device__ __forceinline__ Key none() { return -INFINITY; }
+    static __device__ __forceinline__ Key larger(Key a, Key b) { return fmax(a, b); }
+    static __device__ __forceinline__ Key smaller(Key a, Key b) { return fmin(a, b); }
+    static __device__ __forceinline__ Key lane(Key v, int l) { return lane_f64(v, l); }
+    static __device__ __forceinline__ Key other(Key v, int o) { return __shfl_xor(v, o); }
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ Key step(Key v) { return larger(v, dpp_f64<CTRL, ROWS>(v, v)); }
+};
+
+template <class P>
+__device__ __forceinline__ typename P::Key wave_largest(typename P::Key v) {
+    v = P::template step<0x111, 0xF>(v);
+    v = P::template step<0x112, 0xF>(v);
+    v = P::template step<0x114, 0xF>(v);
+    v = P::template step<0x118, 0xF>(v);
+    v = P::template step<0x142, 0xA>(v);
+    v = P::template step<0x143, 0xC>(v);
+    return P::lane(v, 63);
+}
+
+// exp(min(x, 0) - shift) / (1 + exp(-|x|)): the sigmoid of x times exp(-shift).
+__device__ __forceinline__ float sigmoid_shifted(float x, float shift) {
+    return expf(fminf(x, 0.f) - shift) / (1.f + expf(-fabsf(x)));
+}
+
+struct RouteArgs {
+    const void *logits;
+    int64_t ld, T;
+    const float *bias;
+    int E, K, sigmoid, groups, kept, best, renorm;
+    int size, span;       // experts of a group, lanes of a group
+    float scale;
+    int32_t *ids;
+    float *weights;
+};
+
+// A wave per token. The lanes are dealt to the groups (span of them each, a
+// power of two) and each lane holds up to N neighbouring experts of its
+// group, so that lane and place in it sort like the expert's index, and what
+// concerns one group stays among its lanes.
+template <int N, int BF16, class P>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+    using Key = typename P::Key;
+    constexpr bool SCORES = sizeof(Key) == 8;
+    const int lane = threadIdx.x & 63;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
+    if (t >= a.T) return;
+    const int group = lane / a.span, q0 = (lane & (a.span - 1)) * N;
+    const int e0 = group * a.size + q0, have = group < a.groups ? max(0, min(N, a.size - q0)) : 0;
+    float x[N];
+    Key key[N];
+    bool nan = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = i < have ? route_logit<BF16>(a.logits, t * a.ld + e0 + i) : -INFINITY;
+        nan |= x[i] != x[i];
+        top = fmaxf(top, x[i]);
+    }
+    const bool any_nan = __ballot(nan) != 0;
+    // softmax: all logits against the largest
+    float denom = 1.f;
+    if (!a.sigmoid && (SCORES || !a.renorm)) {
+        top = wave_max_f32(top);
+        if (!a.renorm) {
+            denom = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) denom += x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+            denom = wave_sum_f32(denom);
+        }
+    }
+    if constexpr (SCORES) {
+        double s[N], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double d = x[i];
+            s[i] = x[i] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - static_cast<double>(top))) : 0.0;
+            sum += s[i];
+        }
+        if (!a.sigmoid) {
+            sum = wave_sum_f64(sum);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] /= sum;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const double k = s[i] + (a.bias && i < have ? static_cast<double>(a.bias[e0 + i]) : 0.0);
+            key[i] = x[i] > -INFINITY && k == k ? k : P::none();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = P::of(x[i]);
+    }
+
+    if (a.groups > 1) {
+        Key one = P::none(), two = P::none();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            two = P::larger(two, P::smaller(one, key[i]));
+            one = P::larger(one, key[i]);
+        }
+        for (int o = 1; o < a.span; o <<= 1) {
+            const Key one2 = P::other(one, o), two2 = P::other(two, o);
+            two = P::larger(P::smaller(one, one2), P::larger(two, two2));
+            one = P::larger(one, one2);
+        }
+        Key sum = one;
+        if constexpr (SCORES)
+            if (a.best == 2 && two > P::none()) sum += two;
+        int better = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const Key s = P::lane(sum, g * a.span);
+            better += s > sum || (s == sum && g < group);
+        }
+        if (better >= a.kept) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) key[i] = P::none();
+        }
+    }
+
+    // choice by choice: the largest of the lanes' largest, in the lowest lane
+    // that holds it; lane j keeps choice j
+    int my_id = -1;
+    float my_x = 0.f;
+    for (int j = 0; j < a.K; ++j) {
+        Key best = key[0];
+        float best_x = x[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            const bool more = key[i] > best;
+            best = more ? key[i] : best;
+            best_x = more ? x[i] : best_x;
+            at = more ? i : at;
+        }
+        const Key most = wave_largest<P>(best);
+        if (!(most > P::none())) break;
+        const int from = __builtin_ctzll(__ballot(best == most));
+        const int id = static_cast<int>(lane_u32(static_cast<uint32_t>(e0 + at), from));
+        const float its = lane_f32(best_x, from);
+        if (lane == j) {
+            my_id = id;
+            my_x = its;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane == from && i == at) key[i] = P::none();
+    }
+
+    const bool chosen = my_id >= 0;
+    float w;
+    if (a.renorm) {
+        const float most = wave_max_f32(chosen ? my_x : -INFINITY);
+        const float p = !chosen ? 0.f : a.sigmoid ? sigmoid_shifted(my_x, fminf(most, 0.f)) : expf(my_x - most);
+        w = p / wave_sum_f32(p);
+    } else {
+        w = a.sigmoid ? sigmoid_shifted(my_x, 0.f) : expf(my_x - top) / denom;
+    }
+    if (any_nan) w = NAN;
+    if (lane < a.K) {
+        a.ids[t * a.K + lane] = my_id;
+        a.weights[t * a.K + lane] = chosen ? a.scale * w : 0.f;
+    }
+}
+
+struct RouteBackwardArgs {
+    const void *logits;
+    int64_t ld, T;
+    int E, K, sigmoid, renorm;
+    float scale;
+    const int32_t *ids;
+    const float *dw;
+    void *dx;
+    int64_t lddx;
+};
+
+// A wave per token: lane j holds choice j and what the gradient puts at its
+// expert, q_j = dL/ds_j ds_j/dx_j; then the row is written by lanes that hold
+// experts lane + 64 i. With p the chosen scores, P their sum (1 where not
+// renormalised) and g_j = c dw_j:
+//   sigmoid  q_j = p_j / P (1 - s_j) (g_j - sum_i p_i / P g_i)   (without the sum: not renormalised)
+//   softmax  q_j = p_j / P (g_j - sum_i p_i / P g_i), or not renormalised
+//            q_j = p_j g_j and every expert's gradient gets - s_e sum_i q_i.
+// Two choices of one expert add up.
+template <int N, int BF16>
+__global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackwardArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
+    if (t >= a.T) return;
+    int id = lane < a.K ? a.ids[t * a.K + lane] : -1;
+    id = id >= 0 && id < a.E ? id : -1;
+    const bool chosen = id >= 0;
+    const float x = chosen ? route_logit<BF16>(a.logits, t * a.ld + id) : -INFINITY;
+    const float g = chosen ? a.scale * a.dw[t * a.K + lane] : 0.f;
+    const bool whole = !a.sigmoid && !a.renorm;
+    float row[N];
+    float q;
+    if (whole) {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = lane + 64 * i;
+            row[i] = e < a.E ? route_logit<BF16>(a.logits, t * a.ld + e) : -INFINITY;
+            top = fmaxf(top, row[i]);
+        }
+        top = wave_max_f32(top);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            row[i] = row[i] == -INFINITY ? 0.f : expf(row[i] - top);
+            sum += row[i];
+        }
+        sum = wave_sum_f32(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;       // a row of -inf alone
+        q = x == -INFINITY ? 0.f : expf(x - top) * inv * g;
+        const float all = wave_sum_f32(q);
+#pragma unroll
+        for (int i = 0; i < N; ++i) row[i] = -(row[i] * inv * all);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) row[i] = 0.f;
+        if (a.renorm) {
+            const float most = wave_max_f32(x);
+            float p = x == -INFINITY ? 0.f : a.sigmoid ? sigmoid_shifted(x, fminf(most, 0.f)) : expf(x - most);
+            const float sum = wave_sum_f32(p);
+            p = sum == 0.f ? 0.f : p / sum;
+            q = p * (g - wave_sum_f32(p * g));
+            if (a.sigmoid && chosen) q *= sigmoid_shifted(-x, 0.f);
+        } else {
+            q = x == -INFINITY ? 0.f : sigmoid_shifted(x, 0.f) * sigmoid_shifted(-x, 0.f) * g;
+        }
+    }
+    for (int j = 0; j < a.K; ++j) {
+        const int at = static_cast<int>(lane_u32(static_cast<uint32_t>(id), j));
+        const float add = lane_f32(q, j);
+        if (at < 0) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (at == lane + 64 * i) row[i] += add;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = lane + 64 * i;
+        if (e >= a.E) continue;
+        if (BF16)
+            static_cast<uint16_t *>(a.dx)[t * a.lddx + e] = static_cast<uint16_t>(pack_bf16x2(row[i], 0.f));
+        else
+            static_cast<float *>(a.dx)[t * a.lddx + e] = row[i];
+    }
+}
+
+// The lanes of a group: as many as divide the wave among the groups.
+static int route_span(int groups) {
+    int span = 64;
+    while (64 / span < groups) span >>= 1;
+    return span;
+}
+
+template <int N, int BF16>
+static void route_n(const RouteArgs &a, bool scores, dim3 grid, hipStream_t st) {
+    if (scores)
+        hipLaunchKernelGGL((route_kernel<N, BF16, ScoreKey>), grid, dim3(kRouteThreads), 0, st, a);
+    else
+        hipLaunchKernelGGL((route_kernel<N, BF16, LogitKey>), grid, dim3(kRouteThreads), 0, st, a);
+}
+
+hipError_t launch_route(const RouteCall &c, hipStream_t st) {
+    RouteArgs a;
+    a.logits = c.logits;
+    a.ld = c.ld;
+    a.T = c.T;
+    a.bias = c.bias;
+    a.E = c.E;
+    a.K = c.K;
+    a.sigmoid = c.sigmoid;
+    a.groups = c.kept < c.groups ? c.groups : 1;      // all groups kept: none matters
+    a.kept = c.kept;
+    a.best = c.best;
+    a.renorm = c.renorm;
+    a.size = c.E / a.groups;
+    a.span = route_span(a.groups);
+    a.scale = c.scale;
+    a.ids = c.ids;
+    a.weights = c.weights;
+    const bool scores = c.bias || (a.groups > 1 && c.best == 2);
+    const int n = (a.size + a.span - 1) / a.span;
+    const dim3 grid(static_cast<uint32_t>((c.T + kRouteTokens - 1) / kRouteTokens));
+    auto go = [&](auto width) {
+        constexpr int N = decltype(width)::value;
+        if (c.bf16) route_n<N, 1>(a, scores, grid, st);
+        else route_n<N, 0>(a, scores, grid, st);
+    };
+    if (n <= 1) go(std::integral_constant<int, 1>{});
+    else if (n <= 2) go(std::integral_constant<int, 2>{});
+    else if (n <= 4) go(std::integral_constant<int, 4>{});
+    else if (n <= 8) go(std::integral_constant<int, 8>{});
+    else if (n <= 16) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 32>{});
+    return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const RouteCall &c, const float *dw, void *dx, int64_t lddx, hipStream_t st) {
+    RouteBackwardArgs a;
+    a.logits = c.logits;
+    a.ld = c.ld;
+    a.T = c.T;
+    a.E = c.E;
+    a.K = c.K;
+    a.sigmoid = c.sigmoid;
+    a.renorm = c.renorm;
+    a.scale = c.scale;
+    a.ids = c.ids;
+    a.dw = dw;
+    a.dx = dx;
+    a.lddx = lddx;
+    const int n = (c.E + 63) / 64;
+    const dim3 grid(static_cast<uint32_t>((c.T + kRouteTokens - 1) / kRouteTokens));
+    auto go = [&](auto width) {
+        constexpr int N = decltype(width)::value;
+        if (c.bf16) hipLaunchKernelGGL((route_backward_kernel<N, 1>), grid, dim3(kRouteThreads), 0, st, a);
+        else hipLaunchKernelGGL((route_backward_kernel<N, 0>), grid, dim3(kRouteThreads), 0, st, a);
+    };
+    if (n <= 1) go(std::integral_constant<int, 1>{});
+    else if (n <= 2) go(std::integral_constant<int, 2>{});
+    else if (n <= 4) go(std::integral_constant<int, 4>{});
+    else if (n <= 8) go(std::integral_constant<int, 8>{});
+    else go(std::integral_constant<int, 16>{});
+    return hipGetLastError();
+}
+
+}  // namespace logra
