@@ -31,7 +31,8 @@ COMMON_FLAGS = [
 # compiler rotates accumulators between the two register files around every
 # unrolled step of the fold loop, and without that rotation the split- and
 # single-mode folds ran about 3 % faster (the pair-mode instances, which ran
-# slower with it, are in fold_pair_bf16.hip).
+# slower with it, are in fold_pair_bf16.hip). The 8-bit products scale every
+# matrix result with vector instructions, which read vector registers only.
 FILE_FLAGS = {
     "fp8_matmul.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "fold_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],

@@ -21,6 +21,8 @@
 // Y in fp32: the codes are made bf16 (exact) and multiplied by
 // v_mfma_f32_16x16x32_bf16, whose sums are fp32 (8e-8 of Y measured), at half
 // the rate.
+#include <math.h>
+
 #include <type_traits>
 
 #include "common.hpp"
@@ -29,11 +31,12 @@
 namespace logra {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void_t;
+typedef __attribute__((address_space(3))) char lds_char_t;
 
 constexpr uint32_t kMmOob = 0x80000000u;      // past every buffer view: loads give zeros
 constexpr int kMmK = 128;
 constexpr int kMmXcds = 8;
+constexpr int kMmGrid = 256;                   // one workgroup for each compute unit
 
 // Operand of 128 k: a lane has 32 of the k of row L % 16 of A or of column
 // L % 16 of B (which ones does not matter as long as both have the same), as
@@ -74,8 +77,9 @@ __device__ __forceinline__ f32x4_t mm_product(const MmOperand<WIDE> &a, const Mm
     }
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_view(const void *p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF, 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_view(const void *p, int64_t bytes = 0x7FFFFFFF) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
+                                             static_cast<int>(min(bytes, static_cast<int64_t>(0x7FFFFFFF))), 0x00020000);
 }
 __device__ __forceinline__ u32x4_t mm_load16(__amdgpu_buffer_rsrc_t rs, uint32_t off, int step) {
     return __builtin_amdgcn_raw_buffer_load_b128(rs, off, step, 0);
@@ -91,42 +95,58 @@ struct MmTile {
     int64_t row0;
 };
 
-// The workgroup's tile of (row tiles of all experts) x (feature tiles).
-// Workgroup ids of one XCD (id mod 8) have neighbouring tiles: BAND row tiles
-// by as many feature tiles as there are workgroups, so that they read the
-// same rows of x and w through the XCD's cache. False: none is left.
+// The tiles of a product: row tiles of all experts, times feature tiles.
+struct MmPlan {
+    int tiles, n_tn, band;        // row tiles, feature tiles
+    int per, mine, before;        // experts of a lane, their row tiles, and those before them
+};
+
+__device__ __forceinline__ void mm_rows_of(const MatmulCall &c, int e, int64_t *a, int64_t *b) {
+    *a = min(max(static_cast<int64_t>(c.offsets[e]), static_cast<int64_t>(0)), c.M);
+    *b = min(max(static_cast<int64_t>(c.offsets[e + 1]), *a), c.M);
+}
+
 template <int BM>
-__device__ __forceinline__ bool mm_tile(const MatmulCall &c, int n_tn, int band, MmTile *out) {
+__device__ __forceinline__ MmPlan mm_plan(const MatmulCall &c, int n_tn, int band) {
     const int lane = threadIdx.x & 63;
-    int tiles, per = 1, mine = 0, before = 0;
-    if (c.offsets) {
-        per = (c.E + 63) / 64;
-        for (int i = 0; i < per; ++i) {
-            const int e = lane * per + i;
-            if (e >= c.E) break;
-            const int64_t a = min(max(static_cast<int64_t>(c.offsets[e]), static_cast<int64_t>(0)), c.M);
-            const int64_t b = min(max(static_cast<int64_t>(c.offsets[e + 1]), a), c.M);
-            mine += static_cast<int>((b - a + BM - 1) / BM);
-        }
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(sum, o);
-            if (lane >= o) sum += up;
-        }
-        before = sum - mine;
-        tiles = __builtin_amdgcn_readlane(sum, 63);
-    } else {
-        tiles = static_cast<int>((c.M + BM - 1) / BM);
+    MmPlan p{0, n_tn, band, 1, 0, 0};
+    if (!c.offsets) {
+        p.tiles = static_cast<int>((c.M + BM - 1) / BM);
+        return p;
     }
-    const int64_t G = static_cast<int64_t>(tiles) * n_tn, id = blockIdx.x;
+    p.per = (c.E + 63) / 64;
+    for (int i = 0; i < p.per; ++i) {
+        const int e = lane * p.per + i;
+        if (e >= c.E) break;
+        int64_t a, b;
+        mm_rows_of(c, e, &a, &b);
+        p.mine += static_cast<int>((b - a + BM - 1) / BM);
+    }
+    int sum = p.mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int up = __shfl_up(sum, o);
+        if (lane >= o) sum += up;
+    }
+    p.before = sum - p.mine;
+    p.tiles = __builtin_amdgcn_readlane(sum, 63);
+    return p;
+}
+
+// The tile of workgroup id (any of 0 .. tiles n_tn - 1; workgroups take ids a
+// grid apart, which is a multiple of eight). Ids of one XCD (id mod 8) have
+// neighbouring tiles, `band` row tiles by as many feature tiles as there are
+// workgroups, so that they read the same rows of x and w through the XCD's
+// cache. False: none is left.
+template <int BM>
+__device__ __forceinline__ bool mm_tile(const MatmulCall &c, const MmPlan &p, uint32_t id, MmTile *out) {
+    const uint32_t n_tn = p.n_tn, G = static_cast<uint32_t>(p.tiles) * n_tn;      // below 2^23
     if (id >= G) return false;
-    const int64_t share = G / kMmXcds, rest = G % kMmXcds, x = id % kMmXcds;
-    const int64_t q = x * share + (x < rest ? x : rest) + id / kMmXcds;
-    const int64_t group = q / (static_cast<int64_t>(band) * n_tn);
-    const int64_t in = q - group * band * n_tn;
-    const int high = min(static_cast<int64_t>(band), tiles - group * band);    // the last band may be lower
-    const int tm = static_cast<int>(group * band + in % high);
+    const uint32_t share = G / kMmXcds, rest = G % kMmXcds, x = id % kMmXcds;
+    const uint32_t q = x * share + min(x, rest) + id / kMmXcds;
+    const uint32_t group = q / (p.band * n_tn), in = q - group * p.band * n_tn;
+    const uint32_t high = min(static_cast<uint32_t>(p.band), p.tiles - group * p.band);      // the last band may be lower
+    const int tm = static_cast<int>(group * p.band + in % high);
     out->tn = static_cast<int>(in / high);
     if (!c.offsets) {
         out->expert = 0;
@@ -135,11 +155,11 @@ __device__ __forceinline__ bool mm_tile(const MatmulCall &c, int n_tn, int band,
         return true;
     }
     // the lane whose experts hold the row tile, then the expert
-    const int from = __builtin_ctzll(__ballot(before + mine > tm));
-    int left = tm - __builtin_amdgcn_readlane(before, from);
-    for (int e = from * per;; ++e) {
-        const int64_t a = min(max(static_cast<int64_t>(c.offsets[e]), static_cast<int64_t>(0)), c.M);
-        const int64_t b = min(max(static_cast<int64_t>(c.offsets[e + 1]), a), c.M);
+    const int from = __builtin_ctzll(__ballot(p.before + p.mine > tm));
+    int left = tm - __builtin_amdgcn_readlane(p.before, from);
+    for (int e = from * p.per;; ++e) {
+        int64_t a, b;
+        mm_rows_of(c, e, &a, &b);
         const int n = static_cast<int>((b - a + BM - 1) / BM);
         if (left < n) {
             out->expert = e;
@@ -186,81 +206,162 @@ __device__ __forceinline__ void mm_store4(const MatmulCall &c, int64_t row, int 
     }
 }
 
+// Eight neighbouring features of a row in bf16 (n a multiple of eight).
+__device__ __forceinline__ void mm_store8(const MatmulCall &c, int64_t row, int n, const f32x4_t a, const f32x4_t b) {
+    typedef u32x4_t u32x4_m2_t __attribute__((aligned(2)));
+    uint16_t *dst = static_cast<uint16_t *>(c.y) + row * c.ldy + n;
+    const u32x4_t v = {pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+    if (n + 8 <= c.N) {
+        *reinterpret_cast<u32x4_m2_t *>(dst) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (n + e < c.N) dst[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e % 2)));
+}
+
 // ------------------------------------------------------------------ tiles --
-// BM rows x BN features by WM x WN waves. LDS holds two stages of 128 k: rows
-// of 128 bytes, eight granules of 16, granule q of row r at q ^ sw(r), so that
-// the sixteen rows of an operand fall on sixteen different bank groups. Loads
-// that write LDS directly fill one stage while the other is multiplied.
+// BM rows x BN features by WM x WN waves. LDS is a ring of D stages of 128 k:
+// rows of 128 bytes, eight granules of 16, granule q of row r at q ^ sw(r), so
+// that the sixteen rows of an operand fall on sixteen different bank groups;
+// lanes 16 g .. read granules g and 4 + g (with 2 g and 2 g + 1 the reads took
+// twice as long: the LDS takes lanes of several g together).
 //
 // Features of a wave are dealt to its blocks so that a pair of blocks gives a
 // lane eight neighbouring ones: row r of block b is feature
 // 32 (b / 2) + 8 (r / 4) + 4 (b % 2) + r % 4.
+//
+// A workgroup goes from tile to tile, and its loads run D - 1 blocks ahead of
+// its products, into the next tile too: its first blocks come while the last
+// ones of this tile are multiplied and its results are written.
 __device__ __forceinline__ int mm_swx(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int mm_sww(int r) { return (r >> 1 & 1) | (r >> 3 & 3) << 1; }
 
-template <int BM, int BN, int WM, int WN, int BF16>
-__device__ __forceinline__ void mm_tile_body(const MatmulCall &c, const MmTile &t, char *s0, char *s1) {
-    constexpr int WIDE = !BF16, WAVES = WM * WN, RT = BM / WM / 16, FT = BN / WN / 16;
-    constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;      // 1 KB loads of a wave per stage
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ i32x4_t mm_words(const void *p, int64_t bytes = 0x7FFFFFFF) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return i32x4_t{__builtin_amdgcn_readfirstlane(static_cast<int>(a)), __builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32 & 0xFFFF)),
+                   __builtin_amdgcn_readfirstlane(static_cast<int>(min(bytes, static_cast<int64_t>(0x7FFFFFFF)))), 0x00020000};
+}
+
+// 16 bytes per lane from the view at off + step straight into LDS at `to`
+// (lane order; out of the view: zeros). Written out so that the compiler does
+// not wait for all of them at the next LDS read, as it does for the builtin
+// where it cannot tell the stages apart: who reads waits (mm_wait) before.
+__device__ __forceinline__ void mm_fetch(i32x4_t view, uint32_t to, uint32_t off, int step) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(view), "s"(__builtin_amdgcn_readfirstlane(step))
+                 : "memory");
+}
+
+// At most N vector memory operations of the wave are left, its LDS reads are
+// done; then all waves of the workgroup are here.
+template <int N>
+__device__ __forceinline__ void mm_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int BM, int BN, int WM, int WN, int D>
+struct MmShape {
+    static constexpr int WAVES = WM * WN, RT = BM / WM / 16, FT = BN / WN / 16;
+    static constexpr int STAGE = (BM + BN) * kMmK;
+    // scales of eight blocks of k: of the rows, then of the features' blocks
+    static constexpr int SCALES = BM * 32 + 1024;
+    static constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;       // 1 KB loads of a wave for a block
+    static constexpr int SI = (BM / 32 + WAVES - 1) / WAVES;             // and for eight blocks' scales
+    static constexpr int LDS = D * (STAGE + SCALES);
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && 128 % (16 * FT) == 0, "whole loads, one scale");
+    static_assert(LDS <= 160 * 1024 && (D - 2) * (XI + WI) < 64, "what a compute unit has, what a wait can count");
+};
+
+template <int BM, int BN, int WM, int WN, int D, int BF16>
+__global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int n_tn, int band) {
+    using Sh = MmShape<BM, BN, WM, WN, D>;
+    constexpr int WIDE = !BF16, RT = Sh::RT, FT = Sh::FT, XI = Sh::XI, WI = Sh::WI, SI = Sh::SI;
+    __shared__ __attribute__((aligned(16))) char lds[Sh::LDS];
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t *)lds)), scales = ring + D * Sh::STAGE;
     const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int n0 = t.tn * BN;
-    const int64_t base = mm_base(c, t);
     const int kb = (c.K + kMmK - 1) / kMmK, nb = (c.N + 127) / 128;
-    const __amdgpu_buffer_rsrc_t x_rs = mm_view(c.x + base * c.ldx);
-    const __amdgpu_buffer_rsrc_t xs_rs = mm_view(c.xs + base * kb);
-    const __amdgpu_buffer_rsrc_t w_rs = mm_view(c.w + (static_cast<int64_t>(t.expert) * c.N + n0) * c.ldw);
-    const int fb = min((n0 + wn * 16 * FT) / 128, nb - 1);        // the wave's block of features
-    const __amdgpu_buffer_rsrc_t ws_rs = mm_view(c.ws + (static_cast<int64_t>(t.expert) * nb + fb) * kb);
+    const MmPlan plan = mm_plan<BM>(c, n_tn, band);
 
-    // the stage's loads: instruction i of a wave fills eight rows
-    uint32_t x_off[XI], w_off[WI];
-    int x_q[XI], w_q[WI];
+    // what is fetched: tile, block, and their places in the two rings
+    uint32_t f_id = blockIdx.x;
+    int f_b = 0, f_stage = 0, f_place = 0;
+    bool f_more;
+    i32x4_t x_rs, xs_rs, w_rs, ws_rs;
+    uint32_t x_off[XI], w_off[WI], xs_off[SI], ws_off;
+    auto enter = [&]() {
+        MmTile t;
+        f_more = mm_tile<BM>(c, plan, f_id, &t);
+        if (!f_more) return;
+        const int n0 = t.tn * BN;
+        const int64_t base = mm_base(c, t);
+        x_rs = mm_words(c.x + base * c.ldx);
+        xs_rs = mm_words(c.xs + base * kb, (c.x_rows - base) * kb * 4);
+        w_rs = mm_words(c.w + (static_cast<int64_t>(t.expert) * c.N + n0) * c.ldw);
+        const int64_t fb = static_cast<int64_t>(t.expert) * nb + n0 / 128;      // the tile's first block of features
+        ws_rs = mm_words(c.ws + fb * kb, (static_cast<int64_t>(c.E) * nb - fb) * kb * 4);
+        // instruction i of a wave fills eight rows
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-        const int r = 8 * (XI * wave + i) + (lane >> 3);
-        const int64_t row = mm_row(c, t, r);
-        x_q[i] = (lane & 7) ^ mm_swx(r);
-        x_off[i] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * c.ldx + 16 * x_q[i]);
-    }
+        for (int i = 0; i < XI; ++i) {
+            const int r = 8 * (XI * wave + i) + (lane >> 3);
+            const int64_t row = mm_row(c, t, r);
+            x_off[i] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * c.ldx + 16 * ((lane & 7) ^ mm_swx(r)));
+        }
 #pragma unroll
-    for (int i = 0; i < WI; ++i) {
-        const int r = 8 * (WI * wave + i) + (lane >> 3);
-        w_q[i] = (lane & 7) ^ mm_sww(r);
-        w_off[i] = n0 + r >= c.N ? kMmOob : static_cast<uint32_t>(static_cast<int64_t>(r) * c.ldw + 16 * w_q[i]);
-    }
-    // scales: of a lane's rows (one per 16-row block), and of the wave's features
-    uint32_t xs_off[RT];
+        for (int i = 0; i < WI; ++i) {
+            const int r = 8 * (WI * wave + i) + (lane >> 3);
+            w_off[i] = n0 + r >= c.N ? kMmOob : static_cast<uint32_t>(static_cast<int64_t>(r) * c.ldw + 16 * ((lane & 7) ^ mm_sww(r)));
+        }
+        // scales: two lanes a row
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        const int64_t row = mm_row(c, t, wm * 16 * RT + 16 * j + i16);
-        xs_off[j] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * kb * 4);
-    }
-    float xs[2][RT], ws[2];
-    auto issue = [&](int b, auto stage_c) {
-        constexpr int S = decltype(stage_c)::value;
-        char *st = S ? s1 : s0;
-        const int left = c.K - b * kMmK;        // <= 0 behind the last block: all of it zeros
-        const int step = left > 0 ? b * kMmK : 0, at = left > 0 ? 4 * b : 0;
-#pragma unroll
-        for (int j = 0; j < RT; ++j) xs[S][j] = mm_load4(xs_rs, left > 0 ? xs_off[j] : kMmOob, at);
-        ws[S] = mm_load4(ws_rs, left > 0 ? 0u : kMmOob, at);
-#pragma unroll
-        for (int i = 0; i < XI; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(x_rs, (lds_void_t *)(st + (XI * wave + i) * 1024), 16,
-                                                     16 * x_q[i] < left ? x_off[i] : kMmOob, step, 0, 0);
-#pragma unroll
-        for (int i = 0; i < WI; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (lds_void_t *)(st + BM * kMmK + (WI * wave + i) * 1024), 16,
-                                                     16 * w_q[i] < left ? w_off[i] : kMmOob, step, 0, 0);
+        for (int i = 0; i < SI; ++i) {
+            const int r = 32 * (SI * wave + i) + (lane >> 1);
+            const int64_t row = r < BM ? mm_row(c, t, r) : -1;
+            xs_off[i] = row < 0 ? kMmOob : static_cast<uint32_t>(((row - base) * kb + 4 * (lane & 1)) * 4);
+        }
+        ws_off = (lane >> 1) < BN / 128 ? static_cast<uint32_t>(((lane >> 1) * kb + 4 * (lane & 1)) * 4) : kMmOob;
     };
-    f32x4_t acc[FT][RT];
+    // The loads of a block in XI + WI pieces (behind the last tile: zeros, so
+    // that every wait finds as many), and the scales before every eighth.
+    auto fetch_scales = [&]() {
+        if ((f_b & 7) != 0 || !f_more) return;
+        const uint32_t to = scales + f_place * Sh::SCALES;
 #pragma unroll
-    for (int f = 0; f < FT; ++f)
-#pragma unroll
-        for (int j = 0; j < RT; ++j) acc[f][j] = zero_f32x4();
+        for (int i = 0; i < SI; ++i)
+            if (SI * Sh::WAVES * 32 == BM || SI * wave + i < BM / 32)
+                mm_fetch(xs_rs, to + (SI * wave + i) * 1024, xs_off[i], 4 * f_b);
+        if (wave == Sh::WAVES - 1) mm_fetch(ws_rs, to + BM * 32, ws_off, 4 * f_b);
+    };
+    auto fetch_piece = [&](int i) {
+        const uint32_t to = ring + f_stage * Sh::STAGE;
+        const int left = f_more ? c.K - f_b * kMmK : 0;
+        if (i < XI) {
+            const int q = 16 * ((lane & 7) ^ mm_swx(8 * (XI * wave + i) + (lane >> 3)));
+            mm_fetch(x_rs, to + (XI * wave + i) * 1024, q < left ? x_off[i] : kMmOob, f_b * kMmK);
+        } else {
+            const int q = 16 * ((lane & 7) ^ mm_sww(8 * (WI * wave + i - XI) + (lane >> 3)));
+            mm_fetch(w_rs, to + BM * kMmK + (WI * wave + i - XI) * 1024, q < left ? w_off[i - XI] : kMmOob, f_b * kMmK);
+        }
+    };
+    auto fetched = [&]() {
+        f_stage = f_stage + 1 == D ? 0 : f_stage + 1;
+        if (!f_more) return;
+        ++f_b;
+        if ((f_b & 7) == 0 || f_b == kb) f_place = f_place + 1 == D ? 0 : f_place + 1;
+        if (f_b == kb) {
+            f_b = 0;
+            f_id += gridDim.x;
+            enter();
+        }
+    };
 
     // operands in a stage: rows of one operand lie at constant distances, as
     // what the granules are permuted by is the same for all of a lane's rows
@@ -268,28 +369,37 @@ __device__ __forceinline__ void mm_tile_body(const MatmulCall &c, const MmTile &
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int rx = wm * 16 * RT + i16, rw = wn * 16 * FT + 8 * (i16 >> 2) + (i16 & 3);
-        x_at[h] = rx * kMmK + (((2 * g + h) ^ mm_swx(rx)) << 4);
-        w_at[h] = rw * kMmK + (((2 * g + h) ^ mm_sww(rw)) << 4);
+        x_at[h] = rx * kMmK + (((g + 4 * h) ^ mm_swx(rx)) << 4);
+        w_at[h] = (BM + rw) * kMmK + (((g + 4 * h) ^ mm_sww(rw)) << 4);
     }
-    auto multiply = [&](auto stage_c) {
-        constexpr int S = decltype(stage_c)::value;
-        const char *X = S ? s1 : s0, *W = X + BM * kMmK;
-        MmOperand<WIDE> xf[RT];
-        float s[RT];
+    const int xs_at = (wm * 16 * RT + i16) * 32, ws_at = BM * 32 + wn * 16 * FT / 128 * 32;
+    f32x4_t acc[FT][RT];
+    auto clear = [&]() {
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            xf[j] = mm_operand<WIDE>(load_u32x4(X + x_at[0] + 16 * j * kMmK), load_u32x4(X + x_at[1] + 16 * j * kMmK));
-            s[j] = xs[S][j] * ws[S];
-        }
+        for (int f = 0; f < FT; ++f)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[f][j] = zero_f32x4();
+    };
+    // One block: the operands' LDS reads first, then the products of one block
+    // of features while those of the one before are scaled and added, with the
+    // loads of the block to come between them.
+    auto multiply = [&](const char *st, const char *sc) {
+        MmOperand<WIDE> xf[RT], wf[2];
+        const char *X0 = st + x_at[0], *X1 = st + x_at[1], *W0 = st + w_at[0], *W1 = st + w_at[1];
         auto w_frag = [&](int f) {
-            const char *at = W + (32 * (f / 2) + 4 * (f % 2)) * kMmK;
-            return mm_operand<WIDE>(load_u32x4(at + w_at[0]), load_u32x4(at + w_at[1]));
+            const int at = (32 * (f / 2) + 4 * (f % 2)) * kMmK;
+            return mm_operand<WIDE>(load_u32x4(W0 + at), load_u32x4(W1 + at));
         };
-        // the products of one block of features while those of the one before
-        // are scaled and added
-        MmOperand<WIDE> wf[2];
-        f32x4_t p[2][RT];
         wf[0] = w_frag(0);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) xf[j] = mm_operand<WIDE>(load_u32x4(X0 + 16 * j * kMmK), load_u32x4(X1 + 16 * j * kMmK));
+        float s[RT];
+        const float ws = *reinterpret_cast<const float *>(sc + ws_at);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) s[j] = ws * *reinterpret_cast<const float *>(sc + xs_at + 16 * j * 32);
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int EACH = FT > 2 ? (2 * (XI + WI) + FT - 1) / FT : (XI + WI + FT - 1) / FT;     // pieces a time
+        f32x4_t p[2][RT];
 #pragma unroll
         for (int f = 0; f <= FT; ++f) {
             if (f + 1 < FT) wf[(f + 1) & 1] = w_frag(f + 1);
@@ -302,91 +412,112 @@ __device__ __forceinline__ void mm_tile_body(const MatmulCall &c, const MmTile &
                         acc[f - 1][j][e] = fmaf(s[j], p[(f - 1) & 1][j][e], acc[f - 1][j][e]);
                     asm volatile("" : "+v"(acc[f - 1][j]));      // here, not past the block's end
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int i = f * EACH; i < (f + 1) * EACH && i < XI + WI; ++i) fetch_piece(i);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    // per block: its loads have landed (all of them were issued a block ago)
-    // and every wave has read the stage that the next block's loads fill
-    auto turn = [&](int b, auto here, auto next) {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) expcnt(7) lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        issue(b + 1, next);
-        multiply(here);
+    auto write = [&](const MmTile &o) {
+        const int n0 = o.tn * BN + wn * 16 * FT;
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const int r = wm * 16 * RT + 16 * j + i16;
+            if (r >= o.rows) continue;
+#pragma unroll
+            for (int f = 0; f < FT; f += 2) {
+                const int n = n0 + 16 * f + 8 * g;
+                if constexpr (BF16) mm_store8(c, o.row0 + r, n, acc[f][j], acc[f + 1][j]);
+                else {
+                    mm_store4<0>(c, o.row0 + r, n, acc[f][j]);
+                    mm_store4<0>(c, o.row0 + r, n + 4, acc[f + 1][j]);
+                }
+            }
+        }
     };
-    issue(0, I0{});
-    for (int b = 0;; b += 2) {
-        turn(b, I0{}, I1{});
-        if (b + 1 >= kb) break;
-        turn(b + 1, I1{}, I0{});
-        if (b + 2 >= kb) break;
+
+    enter();
+    if (!f_more) return;
+    for (int i = 0; i < D - 1; ++i) {
+        fetch_scales();
+#pragma unroll
+        for (int q = 0; q < XI + WI; ++q) fetch_piece(q);
+        fetched();
     }
-    __builtin_amdgcn_s_waitcnt(0x0070);       // the last stage's zeros have landed
-#pragma unroll
-    for (int j = 0; j < RT; ++j) {
-        const int r = wm * 16 * RT + 16 * j + i16;
-        if (r >= t.rows) continue;
-#pragma unroll
-        for (int f = 0; f < FT; ++f) {
-            const int n = n0 + wn * 16 * FT + 32 * (f / 2) + 8 * g + 4 * (f % 2);
-            mm_store4<BF16>(c, t.row0 + r, n, acc[f][j]);
+    clear();
+    uint32_t id = blockIdx.x;
+    int b = 0, stage = 0, place = 0;
+    for (;;) {
+        // this block's loads have landed (D - 2 blocks' are younger), and every
+        // wave has read the block before, whose stage is filled next
+        mm_wait<(D - 2) * (XI + WI)>();
+        fetch_scales();
+        multiply(lds + stage * Sh::STAGE, lds + D * Sh::STAGE + place * Sh::SCALES + (b & 7) * 4);
+        fetched();
+        stage = stage + 1 == D ? 0 : stage + 1;
+        ++b;
+        if ((b & 7) == 0 || b == kb) place = place + 1 == D ? 0 : place + 1;
+        if (b == kb) {
+            MmTile o;
+            mm_tile<BM>(c, plan, id, &o);
+            write(o);
+            id += gridDim.x;
+            if (id >= static_cast<uint32_t>(plan.tiles) * n_tn) break;
+            clear();
+            b = 0;
         }
     }
-}
-
-template <int BM, int BN, int WM, int WN, int BF16>
-__global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int n_tn, int band) {
-    __shared__ __attribute__((aligned(16))) char s0[(BM + BN) * kMmK];
-    __shared__ __attribute__((aligned(16))) char s1[(BM + BN) * kMmK];
-    MmTile t;
-    if (!mm_tile<BM>(c, n_tn, band, &t)) return;
-    mm_tile_body<BM, BN, WM, WN, BF16>(c, t, s0, s1);
+    __builtin_amdgcn_s_waitcnt(0x0070);       // the zeros behind the last tile have landed: the LDS is free
 }
 
 // --------------------------------------------------------------- few rows --
 // Up to 16 RT rows: w is read once and sets the time, so it goes from memory
-// to the registers of the matrix instructions. A workgroup has 16 features;
-// its waves take the blocks of k in turn and their sums are added in LDS.
-template <int RT, int WAVES, int BF16>
-__global__ __launch_bounds__(64 * WAVES) void mm_rows_kernel(MatmulCall c, int n_tn, int band) {
-    constexpr int WIDE = !BF16, BM = 16 * RT, AHEAD = RT > 2 ? 2 : 4;
-    __shared__ f32x4_t part[WAVES][RT][64];
+// to the registers of the matrix instructions. A workgroup has 16 FT features;
+// its waves take the blocks of k in turn, AHEAD of them at a time, and their
+// sums are added in LDS.
+template <int RT, int FT, int WAVES, int AHEAD, int BF16>
+__global__ __launch_bounds__(64 * WAVES) void mm_rows_kernel(MatmulCall c, int n_tn) {
+    constexpr int WIDE = !BF16, BM = 16 * RT;
+    __shared__ f32x4_t part[WAVES][FT][RT][64];
     MmTile t;
-    if (!mm_tile<BM>(c, n_tn, band, &t)) return;
+    if (!mm_tile<BM>(c, mm_plan<BM>(c, n_tn, 1), blockIdx.x, &t)) return;
     const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = t.tn * 16;
+    const int n0 = t.tn * 16 * FT;
     const int64_t base = mm_base(c, t);
     const int kb = (c.K + kMmK - 1) / kMmK, nb = (c.N + 127) / 128;
     const __amdgpu_buffer_rsrc_t x_rs = mm_view(c.x + base * c.ldx);
     const __amdgpu_buffer_rsrc_t xs_rs = mm_view(c.xs + base * kb);
     const __amdgpu_buffer_rsrc_t w_rs = mm_view(c.w + (static_cast<int64_t>(t.expert) * c.N + n0) * c.ldw);
     const __amdgpu_buffer_rsrc_t ws_rs = mm_view(c.ws + (static_cast<int64_t>(t.expert) * nb + n0 / 128) * kb);
-    const uint32_t w_off = n0 + i16 < c.N ? static_cast<uint32_t>(static_cast<int64_t>(i16) * c.ldw + 32 * g) : kMmOob;
-    uint32_t x_off[RT], xs_off[RT];
+    uint32_t w_off[FT], x_off[RT], xs_off[RT];
+#pragma unroll
+    for (int f = 0; f < FT; ++f)
+        w_off[f] = n0 + 16 * f + i16 < c.N ? static_cast<uint32_t>(static_cast<int64_t>(16 * f + i16) * c.ldw + 32 * g) : kMmOob;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         const int64_t row = mm_row(c, t, 16 * j + i16);
         x_off[j] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * c.ldx + 32 * g);
         xs_off[j] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * kb * 4);
     }
-    f32x4_t acc[RT];
+    f32x4_t acc[FT][RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) acc[j] = zero_f32x4();
+    for (int f = 0; f < FT; ++f)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[f][j] = zero_f32x4();
     for (int b0 = wave; b0 < kb; b0 += AHEAD * WAVES) {
-        u32x4_t w[AHEAD][2], x[AHEAD][RT][2];
+        u32x4_t w[AHEAD][FT][2], x[AHEAD][RT][2];
         float s[AHEAD][RT], ws[AHEAD];
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int b = b0 + a * WAVES, left = c.K - b * kMmK;      // <= 0 behind the last block
             const int step = left > 0 ? b * kMmK : 0, at = left > 0 ? 4 * b : 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[a][h] = mm_load16(w_rs, 32 * g + 16 * h < left ? w_off + 16 * h : kMmOob, step);
+            for (int f = 0; f < FT; ++f)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    w[a][f][h] = mm_load16(w_rs, 32 * g + 16 * h < left && w_off[f] != kMmOob ? w_off[f] + 16 * h : kMmOob, step);
             ws[a] = mm_load4(ws_rs, left > 0 ? 0u : kMmOob, at);
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
@@ -397,26 +528,31 @@ __global__ __launch_bounds__(64 * WAVES) void mm_rows_kernel(MatmulCall c, int n
             }
         }
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const MmOperand<WIDE> wo = mm_operand<WIDE>(w[a][0], w[a][1]);
+        for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
-                const f32x4_t p = mm_product<WIDE>(wo, mm_operand<WIDE>(x[a][j][0], x[a][j][1]));
-                const float f = s[a][j] * ws[a];
+                const MmOperand<WIDE> xo = mm_operand<WIDE>(x[a][j][0], x[a][j][1]);
+                const float m = s[a][j] * ws[a];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(f, p[e], acc[j][e]);
+                for (int f = 0; f < FT; ++f) {
+                    const f32x4_t p = mm_product<WIDE>(mm_operand<WIDE>(w[a][f][0], w[a][f][1]), xo);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[f][j][e] = fmaf(m, p[e], acc[f][j][e]);
+                }
             }
-        }
     }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) part[wave][j][lane] = acc[j];
-    __syncthreads();
-    for (int j = wave; j < RT; j += WAVES) {
-        f32x4_t sum = part[0][j][lane];
+    for (int f = 0; f < FT; ++f)
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) sum += part[w][j][lane];
-        const int r = 16 * j + i16;
-        if (r < t.rows && n0 + 4 * g < c.N) mm_store4<BF16>(c, t.row0 + r, n0 + 4 * g, sum);
+        for (int j = 0; j < RT; ++j) part[wave][f][j][lane] = acc[f][j];
+    __syncthreads();
+    for (int q = wave; q < RT * FT; q += WAVES) {
+        const int f = q / RT, j = q % RT;
+        f32x4_t sum = part[0][f][j][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += part[w][f][j][lane];
+        const int r = 16 * j + i16, n = n0 + 16 * f + 4 * g;
+        if (r < t.rows && n < c.N) mm_store4<BF16>(c, t.row0 + r, n, sum);
     }
 }
 
@@ -426,19 +562,19 @@ static int64_t mm_row_tiles(int64_t M, int E, int bm) {
     return E ? M / bm + (M < E ? M : E) : (M + bm - 1) / bm;
 }
 
-template <int RT, int WAVES>
+template <int RT, int FT, int WAVES, int AHEAD, int BF16>
 static void mm_rows(const MatmulCall &c, hipStream_t st) {
-    const int n_tn = (c.N + 15) / 16;
+    const int n_tn = (c.N + 16 * FT - 1) / (16 * FT);
     const dim3 grid(static_cast<uint32_t>(mm_row_tiles(c.M, c.offsets ? c.E : 0, 16 * RT) * n_tn)), block(64 * WAVES);
-    if (c.y_bf16) hipLaunchKernelGGL((mm_rows_kernel<RT, WAVES, 1>), grid, block, 0, st, c, n_tn, 1);
-    else hipLaunchKernelGGL((mm_rows_kernel<RT, WAVES, 0>), grid, block, 0, st, c, n_tn, 1);
+    hipLaunchKernelGGL((mm_rows_kernel<RT, FT, WAVES, AHEAD, BF16>), grid, block, 0, st, c, n_tn);
 }
 
-template <int BM, int BN, int WM, int WN, int BF16>
+template <int BM, int BN, int WM, int WN, int D, int BF16>
 static void mm_tiles(const MatmulCall &c, int band, hipStream_t st) {
     const int n_tn = (c.N + BN - 1) / BN;
-    const dim3 grid(static_cast<uint32_t>(mm_row_tiles(c.M, c.offsets ? c.E : 0, BM) * n_tn)), block(64 * WM * WN);
-    hipLaunchKernelGGL((mm_tile_kernel<BM, BN, WM, WN, BF16>), grid, block, 0, st, c, n_tn, band);
+    const int64_t tiles = mm_row_tiles(c.M, c.offsets ? c.E : 0, BM) * n_tn;
+    const dim3 grid(static_cast<uint32_t>(tiles < kMmGrid ? tiles : kMmGrid)), block(64 * WM * WN);
+    hipLaunchKernelGGL((mm_tile_kernel<BM, BN, WM, WN, D, BF16>), grid, block, 0, st, c, n_tn, band);
 }
 
 // A launch has fewer than 2^32 threads; the smallest tiles are 16 x 16 of 256.
@@ -446,14 +582,61 @@ bool fp8_matmul_fits(int64_t M, int64_t N, int E) {
     return mm_row_tiles(M, E, 16) < (1ll << 23) / ((N + 15) / 16);
 }
 
+// Which kernel: the one expected to be done first. A product's tiles go to the
+// compute units in rounds, and a round takes a start and a step per block of
+// k; both were measured for each shape (us; fp32 results take the shapes up to
+// 128 x 128 with the same steps). Measured, us: 4096 rows of 3584 by 18944 features 275
+// in 256 x 256 tiles, 335 in 128 x 256; 256 rows 49 and 34; 128 rows 33 in 128 x
+// 256, 24 in 128 x 128; 64 rows 23 in 128 x 128, 20 in 64 x 128; 24 rows 20 in 64 x
+// 128, 17 in 32 x 128, 24.6 in rows of 32. 1536 features of k 8960: 512 rows 51 in
+// 128 x 128, 43 in 64 x 128, 36 in 32 x 128; 64 rows 36 in 32 x 128, 16 in rows
+// of 32. The rows kernels read w past the LDS and split k over the waves:
+// their time follows the blocks a compute unit has to stream.
+struct MmShapeTime {
+    int bm, bn;
+    double step, start;
+};
+constexpr MmShapeTime kMmTimes[] = {{32, 128, 0.55, 1.5}, {64, 128, 0.66, 2.0}, {128, 128, 0.78, 2.5}, {128, 256, 1.12, 3.0}, {256, 256, 1.72, 4.0}};
+
 hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
     const int64_t per = c.offsets ? (c.M + c.E - 1) / c.E : c.M;     // rows of an expert
+    const double kb = (c.K + kMmK - 1) / kMmK;
+    // row tiles: with experts, half of one is left over at each
+    const auto row_tiles = [&](int bm) {
+        return c.offsets ? static_cast<double>(c.M) / bm + 0.5 * static_cast<double>(c.M < c.E ? c.M : c.E)
+                         : static_cast<double>((c.M + bm - 1) / bm);
+    };
     const int band = c.offsets ? 2 : 8;
-    if (per <= 16) mm_rows<1, 4>(c, st);
-    else if (per <= 32) mm_rows<2, 4>(c, st);
-    else if (!c.y_bf16) mm_tiles<128, 128, 2, 2, 0>(c, band, st);
-    else if (per <= 128) mm_tiles<128, 128, 2, 2, 1>(c, band, st);
-    else mm_tiles<256, 256, 4, 2, 1>(c, band, st);
+    if (per <= 16) {
+        // one block of features for a workgroup while few rows make few loads
+        // of x (n 18944, k 3584: 1 row 13.6 us with one, 15.2 with two; 16 rows
+        // 19.8 and 18.5; 64 tokens to 8 of 128 experts 45 and 37) or there are few
+        // workgroups (n 1536, k 8960: 1 row 8.7 and 12.1)
+        const bool one = c.N < 8192 && !c.offsets;
+        if (one || (!c.offsets && per <= 8)) c.y_bf16 ? mm_rows<1, 1, 4, 8, 1>(c, st) : mm_rows<1, 1, 4, 8, 0>(c, st);
+        else c.y_bf16 ? mm_rows<1, 2, 4, 4, 1>(c, st) : mm_rows<1, 2, 4, 4, 0>(c, st);
+        return hipGetLastError();
+    }
+    const double wgs = row_tiles(32) * ((c.N + 15) / 16);
+    double best = kb * (wgs < 180 ? 0.15 : 0.00085 * wgs);
+    int which = -1;
+    for (int i = 0; i < (c.y_bf16 ? 5 : 3); ++i) {
+        const MmShapeTime &m = kMmTimes[i];
+        const double rounds = ceil(row_tiles(m.bm) * ((c.N + m.bn - 1) / m.bn) / kMmGrid);
+        const double time = rounds * (kb * m.step + m.start);
+        if (time < best) {
+            best = time;
+            which = i;
+        }
+    }
+    switch (which) {
+    case -1: c.y_bf16 ? mm_rows<2, 1, 4, 4, 1>(c, st) : mm_rows<2, 1, 4, 4, 0>(c, st); break;
+    case 0: c.y_bf16 ? mm_tiles<32, 128, 1, 4, 6, 1>(c, band, st) : mm_tiles<32, 128, 1, 4, 6, 0>(c, band, st); break;
+    case 1: c.y_bf16 ? mm_tiles<64, 128, 1, 4, 5, 1>(c, band, st) : mm_tiles<64, 128, 1, 4, 5, 0>(c, band, st); break;
+    case 2: c.y_bf16 ? mm_tiles<128, 128, 4, 2, 4, 1>(c, band, st) : mm_tiles<128, 128, 4, 2, 4, 0>(c, band, st); break;
+    case 3: mm_tiles<128, 256, 2, 4, 3, 1>(c, band, st); break;
+    default: mm_tiles<256, 256, 4, 2, 2, 1>(c, band, st);
+    }
     return hipGetLastError();
 }
 

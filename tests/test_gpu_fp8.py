@@ -187,6 +187,60 @@ def test_matmul_experts(T, topk, E, n, k, dt):
         assert torch.equal(out, again)
 
 
+# sizes of which every tile shape has some: more tiles than compute units, one and several
+# blocks of k, ragged ends, and more than eight blocks (a second set of scales)
+LARGE = [(4100, 4700, 16), (4100, 4700, 272), (2049, 2600, 1296), (1025, 5130, 640), (300, 18944, 144), (130, 18950, 1168),
+         (70, 9000, 2320), (40, 18944, 400)]
+
+
+def _large_check(x, xs, w, ws, y, half):
+    """Against a product in 64 bits on the GPU, by rows of 512. The bound of a block's sum (see the top) with the sum of
+    magnitudes in the place of the groups' largest products."""
+    kb = xs.shape[1]
+    wd = w.double() * ws.double().repeat_interleave(128, 0)[:w.shape[0]].repeat_interleave(128, 1)[:, :w.shape[1]]
+    for a in range(0, len(y), 512):
+        xd = x[a:a + 512].double() * xs[a:a + 512].double().repeat_interleave(128, 1)[:, :x.shape[1]]
+        ref, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+        cut = 7 * 2.0 ** -13 if y.dtype == torch.bfloat16 else 0.0
+        allowed = half * ref.abs() + (1 + half) * ((256 + 2 * kb + 4) * 2.0 ** -24 + cut) * mag
+        err = (y[a:a + 512].double() - ref).abs()
+        assert bool((err <= allowed).all())
+        # far fewer than the bound allows: a cut of 2^-13 is a thousandth of a usual product
+        assert float(err.norm() / ref.norm()) < (3e-3 if y.dtype == torch.bfloat16 else 1e-6)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,n,k", LARGE)
+def test_matmul_large(T, n, k, dt):
+    dev = device()
+    say("large", T, n, k, dt)
+    x, xs, w, ws = _operands(T + n, T, k, 0, n, dev)
+    y = torch.full((T, n + 1), 9.0, dtype=dt, device=dev)
+    L.logra_fp8_matmul(x, xs, w, ws, y[:, 1:])
+    assert bool((y[:, 0] == 9).all())
+    _large_check(x, xs, w, ws, y[:, 1:], 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("T,topk,E,n,k", [(5000, 4, 20, 520, 400), (3000, 8, 64, 260, 1168), (4096, 2, 8, 2000, 144), (700, 8, 16, 4100, 272)])
+def test_matmul_experts_large(T, topk, E, n, k):
+    dev = device()
+    say("experts large", T, topk, E, n, k)
+    g = np.random.default_rng(T)
+    ids = torch.from_numpy(np.where(g.random((T, topk)) < 0.05, -1, (E * g.random((T, topk)) ** 2).astype(int))).int().to(dev)
+    M = T * topk
+    offsets, order, slots = (torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
+                             torch.empty(T, topk, dtype=torch.int32, device=dev))
+    L.logra_expert_sort(ids, E, offsets, order, slots)
+    x, xs, w, ws = _operands(T, T, k, E, n, dev)
+    y = torch.full((M, n), 9.0, dtype=torch.bfloat16, device=dev)
+    L.logra_fp8_matmul(x, xs, w, ws, y, offsets=offsets, order=order, topk=topk)
+    off = offsets.tolist()
+    assert bool((y[off[-1]:] == 9).all())
+    for e in range(E):
+        rows = (order[off[e]:off[e + 1]] // topk).long()
+        _large_check(x.view(torch.uint8)[rows].view(F8), xs[rows], w[e], ws[e], y[off[e]:off[e + 1]], 2.0 ** -8)
+
+
 def test_matmul_odd_offsets_and_orders():
     """Experts without rows, all rows of one, offsets and orders that reach outside."""
     dev = device()
