@@ -12,11 +12,13 @@
 // An expert whose key is -inf or NaN is never chosen; a choice that finds
 // none is -1 with weight 0, which the sort drops.
 //
-// Choices are whole numbers that must not hang on rounding: keys are formed
-// and compared in fp64, or where no bias and no sum of two keys enters, the
-// logits themselves are compared, which sort like their scores. Weights are
-// fp32, as ratios of exponentials of differences that cannot overflow or all
-// vanish.
+// Choices are whole numbers that must not hang on rounding: they are those of
+// keys formed and compared in fp64. Where no bias and no sum of two keys
+// enters, the logits themselves are compared, which sort like their scores.
+// Otherwise fp32 keys are tried first, with what they may be off by: only a
+// token of which two keys (or sums) that had to be told apart are nearer than
+// that takes the fp64 ones. Weights are fp32, as ratios of exponentials of
+// differences that cannot overflow or all vanish.
 #include <math.h>
 
 #include <type_traits>
@@ -92,46 +94,53 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
     return lane_f64(v, 63);
 }
 
-// The two kinds of keys. Logits as whole numbers that sort like them (0: not
-// to be chosen; both zeros of the logits are one key), and fp64 keys (-inf:
-// not to be chosen).
-struct LogitKey {
+// The two kinds of keys. fp32 values as whole numbers that sort like them (0:
+// not to be chosen; both zeros are one key), and fp64 keys (-inf: not to be
+// chosen).
+struct FloatKey {
     using Key = uint32_t;
     static __device__ __forceinline__ Key none() { return 0u; }
     static __device__ __forceinline__ Key of(float x) {
         const uint32_t b = __float_as_uint(x + 0.f);
         return x > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
     }
+    static __device__ __forceinline__ float value(Key k) {
+        return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+    }
+    static __device__ __forceinline__ Key add(Key a, Key b) { return of(value(a) + value(b)); }
     static __device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
     static __device__ __forceinline__ Key smaller(Key a, Key b) { return a > b ? b : a; }
     static __device__ __forceinline__ Key lane(Key v, int l) { return lane_u32(v, l); }
     static __device__ __forceinline__ Key other(Key v, int o) {
         return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o));
     }
-    template <int CTRL, int ROWS>
-    static __device__ __forceinline__ Key step(Key v) { return larger(v, dpp_u32<CTRL, ROWS>(v, v)); }
+    // rows of 16 lanes by DPP (0 where a lane has no source), the four rows by scalars
+    static __device__ __forceinline__ Key over_wave(Key v) {
+        v = larger(v, dpp_u32<0x111, 0xF>(0u, v));
+        v = larger(v, dpp_u32<0x112, 0xF>(0u, v));
+        v = larger(v, dpp_u32<0x114, 0xF>(0u, v));
+        v = larger(v, dpp_u32<0x118, 0xF>(0u, v));
+        return larger(larger(lane_u32(v, 15), lane_u32(v, 31)), larger(lane_u32(v, 47), lane_u32(v, 63)));
+    }
 };
 struct ScoreKey {
     using Key = double;
     static __device__ __forceinline__ Key none() { return -INFINITY; }
+    static __device__ __forceinline__ Key add(Key a, Key b) { return a + b; }
     static __device__ __forceinline__ Key larger(Key a, Key b) { return fmax(a, b); }
     static __device__ __forceinline__ Key smaller(Key a, Key b) { return fmin(a, b); }
     static __device__ __forceinline__ Key lane(Key v, int l) { return lane_f64(v, l); }
     static __device__ __forceinline__ Key other(Key v, int o) { return __shfl_xor(v, o); }
-    template <int CTRL, int ROWS>
-    static __device__ __forceinline__ Key step(Key v) { return larger(v, dpp_f64<CTRL, ROWS>(v, v)); }
+    static __device__ __forceinline__ Key over_wave(Key v) {
+        v = larger(v, dpp_f64<0x111, 0xF>(v, v));
+        v = larger(v, dpp_f64<0x112, 0xF>(v, v));
+        v = larger(v, dpp_f64<0x114, 0xF>(v, v));
+        v = larger(v, dpp_f64<0x118, 0xF>(v, v));
+        v = larger(v, dpp_f64<0x142, 0xA>(v, v));
+        v = larger(v, dpp_f64<0x143, 0xC>(v, v));
+        return lane_f64(v, 63);
+    }
 };
-
-template <class P>
-__device__ __forceinline__ typename P::Key wave_largest(typename P::Key v) {
-    v = P::template step<0x111, 0xF>(v);
-    v = P::template step<0x112, 0xF>(v);
-    v = P::template step<0x114, 0xF>(v);
-    v = P::template step<0x118, 0xF>(v);
-    v = P::template step<0x142, 0xA>(v);
-    v = P::template step<0x143, 0xC>(v);
-    return P::lane(v, 63);
-}
 
 // exp(min(x, 0) - shift) / (1 + exp(-|x|)): the sigmoid of x times exp(-shift).
 __device__ __forceinline__ float sigmoid_shifted(float x, float shift) {
@@ -149,65 +158,24 @@ struct RouteArgs {
     float *weights;
 };
 
-// A wave per token. The lanes are dealt to the groups (span of them each, a
-// power of two) and each lane holds up to N neighbouring experts of its
-// group, so that lane and place in it sort like the expert's index, and what
-// concerns one group stays among its lanes.
-template <int N, int BF16, class P>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
-    using Key = typename P::Key;
-    constexpr bool SCORES = sizeof(Key) == 8;
-    const int lane = threadIdx.x & 63;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
-    if (t >= a.T) return;
-    const int group = lane / a.span, q0 = (lane & (a.span - 1)) * N;
-    const int e0 = group * a.size + q0, have = group < a.groups ? max(0, min(N, a.size - q0)) : 0;
-    float x[N];
-    Key key[N];
-    bool nan = false;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = i < have ? route_logit<BF16>(a.logits, t * a.ld + e0 + i) : -INFINITY;
-        nan |= x[i] != x[i];
-        top = fmaxf(top, x[i]);
+// What fp32 keys may be off by: `part` for a score, 2^-22 of the larger key
+// for the two sums with a bias (half of each would do).
+struct RouteDoubt {
+    float part;
+    __device__ __forceinline__ bool near(float a, float b, float terms) const {
+        return !(a - b > terms * (part + 0x1p-22f * fmaxf(fabsf(a), fabsf(b))));
     }
-    const bool any_nan = __ballot(nan) != 0;
-    // softmax: all logits against the largest
-    float denom = 1.f;
-    if (!a.sigmoid && (SCORES || !a.renorm)) {
-        top = wave_max_f32(top);
-        if (!a.renorm) {
-            denom = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) denom += x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
-            denom = wave_sum_f32(denom);
-        }
-    }
-    if constexpr (SCORES) {
-        double s[N], sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const double d = x[i];
-            s[i] = x[i] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - static_cast<double>(top))) : 0.0;
-            sum += s[i];
-        }
-        if (!a.sigmoid) {
-            sum = wave_sum_f64(sum);
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[i] /= sum;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const double k = s[i] + (a.bias && i < have ? static_cast<double>(a.bias[e0 + i]) : 0.0);
-            key[i] = x[i] > -INFINITY && k == k ? k : P::none();
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = P::of(x[i]);
-    }
+};
 
+// Which experts the lanes' keys lead to: lane j gets choice j, or -1.
+// CHECK: false where two keys that had to be told apart are in doubt.
+template <class P, bool CHECK, int N>
+__device__ __forceinline__ bool route_choose(const RouteArgs &a, typename P::Key (&key)[N], int e0, RouteDoubt doubt,
+                                             int *my_id) {
+    using Key = typename P::Key;
+    const int lane = threadIdx.x & 63;
     if (a.groups > 1) {
+        const int group = lane / a.span;
         Key one = P::none(), two = P::none();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -219,50 +187,133 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             two = P::larger(P::smaller(one, one2), P::larger(two, two2));
             one = P::larger(one, one2);
         }
-        Key sum = one;
-        if constexpr (SCORES)
-            if (a.best == 2 && two > P::none()) sum += two;
+        const Key sum = a.best == 2 && two > P::none() ? P::add(one, two) : one;
         int better = 0;
         for (int g = 0; g < a.groups; ++g) {
             const Key s = P::lane(sum, g * a.span);
             better += s > sum || (s == sum && g < group);
         }
-        if (better >= a.kept) {
+        const bool out = better >= a.kept;
+        if constexpr (CHECK) {
+            // the lowest sum that stays against the highest that does not
+            const float f = sum > P::none() ? P::value(sum) : -INFINITY;
+            const float low = -wave_max_f32(out || group >= a.groups ? -INFINITY : -f);
+            const float high = wave_max_f32(out ? f : -INFINITY);
+            if (high > -INFINITY && doubt.near(low, high, 2.f)) return false;
+        }
+        if (out) {
 #pragma unroll
             for (int i = 0; i < N; ++i) key[i] = P::none();
         }
     }
-
     // choice by choice: the largest of the lanes' largest, in the lowest lane
-    // that holds it; lane j keeps choice j
-    int my_id = -1;
-    float my_x = 0.f;
-    for (int j = 0; j < a.K; ++j) {
+    // that holds it
+    *my_id = -1;
+    float before = INFINITY;
+    for (int j = 0; j < a.K + (CHECK ? 1 : 0); ++j) {
         Key best = key[0];
-        float best_x = x[0];
         int at = 0;
 #pragma unroll
         for (int i = 1; i < N; ++i) {
             const bool more = key[i] > best;
             best = more ? key[i] : best;
-            best_x = more ? x[i] : best_x;
             at = more ? i : at;
         }
-        const Key most = wave_largest<P>(best);
+        const Key most = P::over_wave(best);
         if (!(most > P::none())) break;
+        if constexpr (CHECK) {
+            const float value = P::value(most);
+            if (j > 0 && doubt.near(before, value, 1.f)) return false;
+            before = value;
+        }
         const int from = __builtin_ctzll(__ballot(best == most));
         const int id = static_cast<int>(lane_u32(static_cast<uint32_t>(e0 + at), from));
-        const float its = lane_f32(best_x, from);
-        if (lane == j) {
-            my_id = id;
-            my_x = its;
-        }
+        if (lane == j && j < a.K) *my_id = id;
+        const int taken = lane == from ? at : -1;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (lane == from && i == at) key[i] = P::none();
+        for (int i = 0; i < N; ++i) key[i] = i == taken ? P::none() : key[i];
+    }
+    return true;
+}
+
+// A wave per token. The lanes are dealt to the groups (span of them each, a
+// power of two) and each lane holds up to N neighbouring experts of its
+// group, so that lane and place in it sort like the expert's index, and what
+// concerns one group stays among its lanes.
+template <int N, int BF16, int SCORES>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
+    if (t >= a.T) return;
+    const int group = lane / a.span, q0 = (lane & (a.span - 1)) * N;
+    const int e0 = group * a.size + q0, have = group < a.groups ? max(0, min(N, a.size - q0)) : 0;
+    float x[N];
+    bool nan = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = i < have ? route_logit<BF16>(a.logits, t * a.ld + e0 + i) : -INFINITY;
+        nan |= x[i] != x[i];
+        top = fmaxf(top, x[i]);
+    }
+    const bool any_nan = __ballot(nan) != 0;
+    // softmax: all logits against the largest
+    float denom = 1.f;
+    float score[N];
+    if (!a.sigmoid && (SCORES || !a.renorm)) {
+        top = wave_max_f32(top);
+        denom = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            score[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+            denom += score[i];
+        }
+        denom = wave_sum_f32(denom);
+    }
+
+    int my_id;
+    if constexpr (SCORES) {
+        float bias[N];
+        uint32_t key[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) bias[i] = a.bias && i < have ? a.bias[e0 + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = a.sigmoid ? 1.f / (1.f + expf(-x[i])) : score[i] / denom;
+            key[i] = FloatKey::of(x[i] > -INFINITY ? s + bias[i] : -INFINITY);
+        }
+        // A sigmoid is three roundings and an exponential within 2^-23 (together
+        // 2^-22; two of them 2^-21). A softmax has its exponential's argument
+        // rounded (score times |d| 2^-24, at most 0.37 2^-24 of the largest
+        // score), the exponential, up to N + 6 roundings of the sum (2^-18.7
+        // with N = 32) and the quotient: 2^-18 of the largest score for two.
+        const RouteDoubt doubt{a.sigmoid ? 0x1p-21f : 0x1p-18f / denom};
+        if (!route_choose<FloatKey, true>(a, key, e0, doubt, &my_id)) {
+            double wide[N], sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const double d = x[i];
+                wide[i] = x[i] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - static_cast<double>(top))) : 0.0;
+                sum += wide[i];
+            }
+            if (!a.sigmoid) sum = wave_sum_f64(sum);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (!a.sigmoid) wide[i] /= sum;
+                const double k = wide[i] + static_cast<double>(bias[i]);
+                wide[i] = x[i] > -INFINITY && k == k ? k : ScoreKey::none();
+            }
+            route_choose<ScoreKey, false>(a, wide, e0, doubt, &my_id);
+        }
+    } else {
+        uint32_t key[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) key[i] = FloatKey::of(x[i]);
+        route_choose<FloatKey, false>(a, key, e0, RouteDoubt{0.f}, &my_id);
     }
 
     const bool chosen = my_id >= 0;
+    const float my_x = chosen ? route_logit<BF16>(a.logits, t * a.ld + my_id) : 0.f;
     float w;
     if (a.renorm) {
         const float most = wave_max_f32(chosen ? my_x : -INFINITY);
@@ -276,6 +327,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         a.ids[t * a.K + lane] = my_id;
         a.weights[t * a.K + lane] = chosen ? a.scale * w : 0.f;
     }
+}
+
+// LDS accesses of the wave before this are done before those after it.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
 }
 
 struct RouteBackwardArgs {
@@ -297,8 +354,14 @@ struct RouteBackwardArgs {
 //   softmax  q_j = p_j / P (g_j - sum_i p_i / P g_i), or not renormalised
 //            q_j = p_j g_j and every expert's gradient gets - s_e sum_i q_i.
 // Two choices of one expert add up.
+//
+// Which choice an expert has is looked up in a row of bytes per wave: every
+// choice writes its lane there and reads it back, and only where one finds
+// another's lane (an expert chosen twice) are the choices gone through one by
+// one.
 template <int N, int BF16>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackwardArgs a) {
+    __shared__ uint8_t owner[kRouteTokens][64 * N];
     const int lane = threadIdx.x & 63;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
     if (t >= a.T) return;
@@ -344,13 +407,28 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
             q = x == -INFINITY ? 0.f : sigmoid_shifted(x, 0.f) * sigmoid_shifted(-x, 0.f) * g;
         }
     }
-    for (int j = 0; j < a.K; ++j) {
-        const int at = static_cast<int>(lane_u32(static_cast<uint32_t>(id), j));
-        const float add = lane_f32(q, j);
-        if (at < 0) continue;
+    uint8_t *who = owner[threadIdx.x >> 6];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (at == lane + 64 * i) row[i] += add;
+    for (int i = 0; i < N; ++i) who[lane + 64 * i] = 255;
+    wave_lds_order();
+    if (chosen) who[id] = static_cast<uint8_t>(lane);
+    wave_lds_order();
+    if (__ballot(chosen && who[id] != lane) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int j = who[lane + 64 * i];
+            const float add = __shfl(q, j & 63);
+            if (j < 64) row[i] += add;
+        }
+    } else {
+        for (int j = 0; j < a.K; ++j) {
+            const int at = static_cast<int>(lane_u32(static_cast<uint32_t>(id), j));
+            const float add = lane_f32(q, j);
+            if (at < 0) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (at == lane + 64 * i) row[i] += add;
+        }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -373,9 +451,9 @@ static int route_span(int groups) {
 template <int N, int BF16>
 static void route_n(const RouteArgs &a, bool scores, dim3 grid, hipStream_t st) {
     if (scores)
-        hipLaunchKernelGGL((route_kernel<N, BF16, ScoreKey>), grid, dim3(kRouteThreads), 0, st, a);
+        hipLaunchKernelGGL((route_kernel<N, BF16, 1>), grid, dim3(kRouteThreads), 0, st, a);
     else
-        hipLaunchKernelGGL((route_kernel<N, BF16, LogitKey>), grid, dim3(kRouteThreads), 0, st, a);
+        hipLaunchKernelGGL((route_kernel<N, BF16, 0>), grid, dim3(kRouteThreads), 0, st, a);
 }
 
 hipError_t launch_route(const RouteCall &c, hipStream_t st) {
