@@ -150,14 +150,47 @@ __device__ __forceinline__ float adam_scale(uint32_t most, float *inv) {
     return live ? amax / 448.f : 0.f;
 }
 
-// The e4m3 value below or above |x| inv, by chance: u is uniform in
+// The e4m3 values below or above |x| inv, by chance: u is uniform in
 // 0 .. 65535, taken in the middle of its step. 20 mantissa bits are dropped
-// from normal values; subnormal ones are whole multiples of 2^-9.
-__device__ __forceinline__ float adam_round(float x, float inv, uint32_t u) {
-    const float a = fminf(fabsf(x) * inv, 448.f);
-    const float normal = __uint_as_float((__float_as_uint(a) + (u << 4 | 8u)) & 0xFFF00000u);
-    const float small = floorf(a * 512.f + (static_cast<float>(u) + 0.5f) * 0x1p-16f) * 0x1p-9f;
-    return copysignf(a >= 0x1p-6f ? normal : small, x);
+// from normal values; subnormal ones (below 2^-6) are whole multiples of 2^-9,
+// which few blocks have: they are looked at only if a lane does.
+__device__ __forceinline__ void adam_round(float (&x)[8], float inv, const uint32_t (&u)[8]) {
+    float a[8], q[8];
+    bool small = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        a[e] = fminf(fabsf(x[e]) * inv, 448.f);
+        q[e] = __uint_as_float((__float_as_uint(a[e]) + (u[e] << 4 | 8u)) & 0xFFF00000u);      // zero stays
+        small |= a[e] < 0x1p-6f && a[e] > 0.f;
+    }
+    if (__ballot(small) != 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = floorf(a[e] * 512.f + (static_cast<float>(u[e]) + 0.5f) * 0x1p-16f) * 0x1p-9f;
+            q[e] = a[e] < 0x1p-6f ? s : q[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = copysignf(q[e], x[e]);
+}
+
+// Square roots: the reciprocal root's estimate (one unit off at most) and a
+// correction by the remainder, which is the correctly rounded root but where
+// that lies within 2^-20 of a unit of the middle between two values. Outside
+// of what the remainder is exact for, the library's.
+__device__ __forceinline__ void adam_roots(const float (&v)[8], float (&r)[8]) {
+    bool wide = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float y = __builtin_amdgcn_rsqf(fmaxf(v[e], 0x1p-100f));
+        const float s = v[e] * y;
+        r[e] = fmaf(fmaf(-s, s, v[e]), 0.5f * y, s);
+        wide |= !(v[e] < 0x1p100f) || (v[e] < 0x1p-100f && v[e] > 0.f);
+    }
+    if (__ballot(wide) != 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = sqrtf(v[e]);
+    }
 }
 
 // Eight exact e4m3 values as codes.
@@ -231,8 +264,13 @@ __device__ __forceinline__ void adam_block(const AdamCall &c, const AdamEntry &e
         const float gc = g[q] * coef;
         m[q] = c.beta1 * m[q] + c.rest1 * gc;
         v[q] = c.beta2 * v[q] + c.rest2 * (gc * gc);
-        r[q] = sqrtf(v[q]);
-        p[q] = p[q] - (c.decay * p[q] + c.rate * (m[q] / (r[q] * c.root_scale + c.eps)));
+    }
+    adam_roots(v, r);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        // a quotient by a reciprocal's estimate: within 2^-22 of the update
+        const float upd = m[q] * __builtin_amdgcn_rcpf(r[q] * c.root_scale + c.eps);
+        p[q] = p[q] - (c.decay * p[q] + c.rate * upd);
     }
     adam_store<P16>(e.param, i, n, e.cols, e.ld_param, p);
     if (e.copy) {
@@ -240,25 +278,35 @@ __device__ __forceinline__ void adam_block(const AdamCall &c, const AdamEntry &e
         else adam_store<0>(e.copy, i, n, e.cols, e.ld_copy, p);
     }
     if (BITS == 8) {
-        uint32_t mm = 0, mr = 0;
+        uint32_t mm = 0, mv = 0;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            const uint32_t a = __float_as_uint(m[q]) & 0x7FFFFFFFu, w = __float_as_uint(r[q]) & 0x7FFFFFFFu;
+            const uint32_t a = __float_as_uint(m[q]) & 0x7FFFFFFFu, w = __float_as_uint(v[q]) & 0x7FFFFFFFu;
             mm = mm > a ? mm : a;
-            mr = mr > w ? mr : w;
+            mv = mv > w ? mv : w;
         }
+        // the largest root is the root of the largest v
+        mv = half_max(mv);
         float inv_m, inv_r;
-        const float scale_m = adam_scale(half_max(mm), &inv_m), scale_r = adam_scale(half_max(mr), &inv_r);
+        const float scale_m = adam_scale(half_max(mm), &inv_m);
+        const float scale_r = adam_scale(mv >= 0x7F800000u ? mv : __float_as_uint(sqrtf(__uint_as_float(mv))), &inv_r);
+        uint32_t um[8], ur[8];
 #pragma unroll
         for (int q = 0; q < 8; q += 2) {
             const uint64_t w = splitmix_finalize(c.key + (static_cast<uint64_t>(s + q) / 2 + 1) * kGolden);
             const uint32_t lo = static_cast<uint32_t>(w), hi = static_cast<uint32_t>(w >> 32);
-            m[q] = adam_round(m[q], inv_m, lo & 0xFFFFu);
-            m[q + 1] = adam_round(m[q + 1], inv_m, hi & 0xFFFFu);
-            const float r0 = adam_round(r[q], inv_r, lo >> 16), r1 = adam_round(r[q + 1], inv_r, hi >> 16);
-            v[q] = r[q] > 0.f && scale_r > 0.f ? fmaxf(r0, 0x1p-9f) : r0;
-            v[q + 1] = r[q + 1] > 0.f && scale_r > 0.f ? fmaxf(r1, 0x1p-9f) : r1;
+            um[q] = lo & 0xFFFFu;
+            um[q + 1] = hi & 0xFFFFu;
+            ur[q] = lo >> 16;
+            ur[q + 1] = hi >> 16;
         }
+        const float least = scale_r > 0.f ? 0x1p-9f : 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = r[q];
+        adam_round(m, inv_m, um);
+        adam_round(v, inv_r, ur);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = r[q] > 0.f ? fmaxf(v[q], least) : v[q];
         *reinterpret_cast<u32x2_t *>(static_cast<uint8_t *>(c.m) + s) = adam_pack(m);
         *reinterpret_cast<u32x2_t *>(static_cast<uint8_t *>(c.v) + s) = adam_pack(v);
         if (l == 0) {
