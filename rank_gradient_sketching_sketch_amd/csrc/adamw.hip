@@ -156,14 +156,15 @@ __device__ __forceinline__ float adam_scale(uint32_t most, float *inv) {
 // which few blocks have: they are looked at only if a lane does.
 __device__ __forceinline__ void adam_round(float (&x)[8], float inv, const uint32_t (&u)[8]) {
     float a[8], q[8];
-    bool small = false;
+    uint32_t least = ~0u;          // of the bits above zero
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        a[e] = fminf(fabsf(x[e]) * inv, 448.f);
+        // the largest may come out a unit or two above 448: cut off again
+        a[e] = fabsf(x[e]) * inv;
         q[e] = __uint_as_float((__float_as_uint(a[e]) + (u[e] << 4 | 8u)) & 0xFFF00000u);      // zero stays
-        small |= a[e] < 0x1p-6f && a[e] > 0.f;
+        least = min(least, __float_as_uint(a[e]) - 1u);
     }
-    if (__ballot(small) != 0) {
+    if (__ballot(least < __float_as_uint(0x1p-6f) - 1u) != 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float s = floorf(a[e] * 512.f + (static_cast<float>(u[e]) + 0.5f) * 0x1p-16f) * 0x1p-9f;
@@ -179,15 +180,16 @@ __device__ __forceinline__ void adam_round(float (&x)[8], float inv, const uint3
 // that lies within 2^-20 of a unit of the middle between two values. Outside
 // of what the remainder is exact for, the library's.
 __device__ __forceinline__ void adam_roots(const float (&v)[8], float (&r)[8]) {
-    bool wide = false;
+    uint32_t least = ~0u, most = 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float y = __builtin_amdgcn_rsqf(fmaxf(v[e], 0x1p-100f));
         const float s = v[e] * y;
         r[e] = fmaf(fmaf(-s, s, v[e]), 0.5f * y, s);
-        wide |= !(v[e] < 0x1p100f) || (v[e] < 0x1p-100f && v[e] > 0.f);
+        least = min(least, __float_as_uint(v[e]) - 1u);
+        most = max(most, __float_as_uint(v[e]));
     }
-    if (__ballot(wide) != 0) {
+    if (__ballot(least < __float_as_uint(0x1p-100f) - 1u || most > __float_as_uint(0x1p100f)) != 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[e] = sqrtf(v[e]);
     }
@@ -269,8 +271,8 @@ __device__ __forceinline__ void adam_block(const AdamCall &c, const AdamEntry &e
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         // a quotient by a reciprocal's estimate: within 2^-22 of the update
-        const float upd = m[q] * __builtin_amdgcn_rcpf(r[q] * c.root_scale + c.eps);
-        p[q] = p[q] - (c.decay * p[q] + c.rate * upd);
+        const float upd = c.rate * (m[q] * __builtin_amdgcn_rcpf(fmaf(r[q], c.root_scale, c.eps)));
+        p[q] = p[q] - fmaf(c.decay, p[q], upd);
     }
     adam_store<P16>(e.param, i, n, e.cols, e.ld_param, p);
     if (e.copy) {
@@ -358,7 +360,10 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamCall c) {
 
 hipError_t launch_adamw(const AdamCall &c, int bits, hipStream_t st) {
     const int64_t wgs = (c.blocks + kAdamPerWG - 1) / kAdamPerWG;
-    const int64_t most = 256 * 16;
+    // 115 M elements with 8-bit moments, us with 1024 / 2048 / 4096 / 16384 workgroups
+    // at most: 402 / 401 / 392 / 363; 49 M with fp32 moments 283 / 280 / 275 / 260, 256
+    // with one for every eight blocks
+    const int64_t most = 1 << 16;
     const dim3 grid(static_cast<uint32_t>(wgs < most ? wgs : most));
     hipLaunchKernelGGL(bits == 8 ? adamw_kernel<8> : adamw_kernel<32>, grid, dim3(kAdamThreads), 0, st, c);
     return hipGetLastError();
