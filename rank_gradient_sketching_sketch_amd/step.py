@@ -31,6 +31,9 @@ A step, in the order the host drives it:
   5. pass 2: logra_rowadam_apply for every matrix given a scale; a matrix
      that is given none (or whose sqnorm is not finite, when the caller asks
      to skip those) keeps W and v. Each applied matrix then swaps v and v'.
+  6. the dense parameters that are not sketched (embeddings, norm gains, router
+     weights), if the step was given any: one AdamW step over all of them
+     (`dense_update`, logra_adamw), at any time after clipping.
 Every lane forks from the caller's current stream at the start of a phase
 and joins it at the end, so the caller can time phases with events on its
 own stream. Callbacks that make the sketch's inputs when they are called run on
@@ -143,6 +146,8 @@ class Step:
               `mats`, group by group (sqnorms, scales).
     grads     dense gradients that `clip` takes along with the sketches
               (device tensors written in place every step).
+    adamw     the B.AdamWList of the dense parameters that `dense_update` takes
+              a step with; `clip` takes its gradients along too.
     r, tokens the sketch rank and the tokens of every microbatch.
     act_dtype B.LOGRA_BF16 or B.LOGRA_F32 (X, dY and the compute dtype).
     sketch_lanes / apply_lanes  stream counts (0: min(4, n) for the sketch;
@@ -160,12 +165,17 @@ class Step:
     def __init__(self, matrices: Sequence[Matrix], r: int, tokens: int, act_dtype: int,
                  device=None, sketch_lanes: int = 0, apply_lanes: int = 0,
                  batch_pass1: bool = True, seed: int = 0, rowsq: bool = False, parts: str = "pair",
-                 groups: Sequence[ExpertGroup] = (), grads: Sequence[torch.Tensor] = ()):
+                 groups: Sequence[ExpertGroup] = (), grads: Sequence[torch.Tensor] = (),
+                 adamw: Optional[B.AdamWList] = None):
         if not matrices and not groups:
             raise ValueError("a step needs at least one matrix")
         self.dense: List[Matrix] = list(matrices)
         self.groups: List[ExpertGroup] = list(groups)
         self.grads = list(grads)
+        self.adamw = adamw
+        if adamw is not None:
+            self.grads += [g for g in adamw.grads if not any(g is x for x in self.grads)]
+        self._clipped = False       # whether `norm` is this step's
         self.mats: List[Matrix] = list(matrices)
         for g in self.groups:
             g.S = None
@@ -350,6 +360,7 @@ class Step:
             raise ValueError("probe: the microbatch must have one before it")
         if late is None:
             late = bool(self.groups)
+        self._clipped = False
         self._members()
         self.set_step(step)
         self._fork()
@@ -423,7 +434,22 @@ class Step:
         if capturing and not any(kept[0] is self._grad_list for kept in self._captured):
             self._captured.append((self._grad_list, self._grad_ws))
         B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)
+        self._clipped = True
         return self.norm, self.coef
+
+    def dense_update(self, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float, step: int):
+        """One AdamW step (its `step`-th, from 1) over the dense parameters
+        given to Step, on the caller's stream. After `clip`, a norm that is not
+        finite leaves parameters and moments as they are: the host that reads
+        the norm does not count that step. The step's seed keys the rounding of
+        8-bit moments."""
+        if self.adamw is None:
+            raise ValueError("the step was given no dense parameters")
+        a = self.adamw
+        if not a.describes(a.params, a.grads, a.copies):
+            raise ValueError("a dense parameter or gradient has other memory than its list was made with")
+        B.logra_adamw(a, lr, beta1, beta2, eps, weight_decay, step, norm=self.norm if self._clipped else None,
+                      seed=self.seed, stream=self.main)
 
     def pass1(self, beta2: float, eps: float):
         """v' and sqnorm of every matrix (v unchanged)."""

@@ -1,0 +1,217 @@
+"""Routing, the experts' 8-bit products, their gradients, the sketches and both
+optimizers used together, as a training program uses them: the router's logits
+choose the experts, tokens are sorted, activations quantised once per token and
+read through the sorted order, the experts' rows combined; the gradient goes
+back through the combination, the turned 8-bit weights and the router; the step
+sketches the experts' projections (its callback runs the layer), clips, and
+updates the experts by RowAdam and router and gains by AdamW. What is not the
+library's (the router's two products) is torch's.
+
+Every stage is checked against fp64 from that stage's own inputs, at the
+tolerances of its own tests: ids equal; weights (2 D + 48) 2^-24 with logits
+below D = 40; products in bf16 2^-8 of the result and the cut of eight 8-bit
+products (7 2^-13 of the sum of magnitudes); the weights' gradient carried back
+(4 D + 128 + K) 2^-24 of the magnitudes; AdamW 16 2^-24 of the update."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import rank_gradient_sketching_sketch_amd as L
+from oracle import experts as ox
+from oracle import layers as lx
+from rank_gradient_sketching_sketch_amd import binding as B
+from rank_gradient_sketching_sketch_amd.step import ExpertGroup, Step
+from gpu_util import BF16_TOL, device, rownorm_err, say, to_f64, w_update_err
+
+pytestmark = pytest.mark.gpu
+
+T, K, E, D, H, R, G, KEPT = 300, 3, 16, 144, 272, 64, 4, 2      # tokens, choices, experts, W's rows and columns, rank, groups
+MBS, PAD = 2, 9
+F8 = torch.float8_e4m3fn
+ROUTE = dict(score=B.LOGRA_SIGMOID, renormalize=True, scale=2.5)
+
+
+def _bytes(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+class Layer:
+    """One expert layer: fp32 router, bf16 activations, experts in e4m3 with their fp32 originals beside them."""
+
+    def __init__(self, dev, seed=1):
+        g = torch.Generator().manual_seed(seed)
+        self.dev = dev
+        self.router = (0.3 * torch.randn(E, H, generator=g)).to(dev)
+        self.bias = (0.1 * torch.randn(E, generator=g)).to(dev)
+        self.gains = torch.ones(H + 1).to(dev)
+        self.W = (0.1 * torch.randn(E, D, H, generator=g)).to(dev)
+        self.d_router, self.d_gains = torch.zeros_like(self.router), torch.zeros_like(self.gains)
+        f8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=dev).view(F8)  # noqa: E731
+        kb = lambda n: -(-n // 128)  # noqa: E731
+        self.w, self.ws = f8(E, D, H), torch.zeros(E, kb(D), kb(H), device=dev)
+        self.wt, self.wts = f8(E, H, D), torch.zeros(E, kb(H), kb(D), device=dev)
+        self.quantize()
+
+    def quantize(self):
+        L.logra_fp8_quantize(self.W, self.w, self.ws, block_rows=128)
+        L.logra_fp8_quantize(self.W, self.wt, self.wts, block_rows=128, transpose=True)
+
+    def inputs(self, mb):
+        g = torch.Generator().manual_seed(100 + mb)
+        X = torch.randn(T, H, generator=g).to(torch.bfloat16).to(self.dev)
+        return X, (1e-2 * torch.randn(T, D, generator=g)).to(torch.bfloat16).to(self.dev)
+
+    def run(self, mb, keep=None):
+        """Forward and backward of one microbatch; (X, dYs, offsets, order) for the sketch."""
+        dev, N = self.dev, T * K
+        i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
+        bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        X, dY = self.inputs(mb)
+        logits = X.float() @ self.router.t()
+        logits[T - PAD:] = -float("inf")                        # padding tokens
+        ids, weights = i32(T, K), torch.empty(T, K, device=dev)
+        L.logra_route(logits, ids, weights, bias=self.bias, groups=G, topk_groups=KEPT, group_best=2, **ROUTE)
+        offsets, order, slots = i32(E + 1), i32(N), i32(T, K)
+        L.logra_expert_sort(ids, E, offsets, order, slots)
+        x, xs = bf(T, H).to(F8), torch.empty(T, -(-H // 128), device=dev)
+        L.logra_fp8_quantize(X, x, xs)
+        Ys, Y = bf(N, D), bf(T, D)
+        L.logra_fp8_matmul(x, xs, self.w, self.ws, Ys, offsets=offsets, order=order, topk=K)
+        L.logra_expert_combine(Ys, slots, Y, weights=weights)
+        dYs, dw = bf(N, D), torch.empty(T, K, device=dev)
+        L.logra_expert_combine_backward(dY, Ys, slots, weights, dYs, dw)
+        dlogits = torch.empty_like(logits)
+        L.logra_route_backward(logits, ids, dw, dlogits, **ROUTE)
+        dy, dys = bf(N, D).to(F8), torch.empty(N, -(-D // 128), device=dev)
+        L.logra_fp8_quantize(dYs, dy, dys)
+        dXs, dX = bf(N, H), bf(T, H)
+        L.logra_fp8_matmul(dy, dys, self.wt, self.wts, dXs, offsets=offsets)
+        L.logra_expert_combine(dXs, slots, dX)
+        self.d_router.addmm_(dlogits.t(), X.float())
+        self.d_gains.add_(dX.float().sum(0).mean())
+        if keep is not None:
+            keep.update(X=X, dY=dY, logits=logits, ids=ids, weights=weights, offsets=offsets, order=order, slots=slots, x=x, xs=xs,
+                        Ys=Ys, Y=Y, dYs=dYs, dw=dw, dlogits=dlogits, dy=dy, dys=dys, dXs=dXs, dX=dX)
+        return X, dYs, offsets, order
+
+
+def _close(got, ref, allowed):
+    assert np.all(np.abs(to_f64(got) - ref) <= allowed)
+
+
+def _check_stages(layer, k):
+    half, tiny = 2.0 ** -8, 1e-37
+    ids, w = lx.route(to_f64(k["logits"]), K, lx.SIGMOID, to_f64(layer.bias), groups=G, topk_groups=KEPT, group_best=2, scale=2.5)
+    assert np.array_equal(k["ids"].cpu().numpy(), ids) and np.all(ids[T - PAD:] == -1)
+    _close(k["weights"], w, (2 * 40 + 48) * 2.0 ** -24 * np.abs(w))
+    off, order, slots = (k[n].cpu().numpy() for n in ("offsets", "order", "slots"))
+    for a, b in zip((off, order, slots), ox.expert_sort(ids, E)):
+        assert np.array_equal(a, b)
+    kept = off[-1]
+    cut = lambda mag: 7 * 2.0 ** -13 * mag  # noqa: E731
+    zero = np.zeros((T * K, D))
+    Y, mag = lx.matmul(_bytes(k["x"]), to_f64(k["xs"]), _bytes(layer.w), to_f64(layer.ws), zero, off, order, K)
+    _close(k["Ys"], Y, half * np.abs(Y) + (1 + half) * (cut(mag) + 300 * 2.0 ** -24 * mag))
+    w_gpu = to_f64(k["weights"])
+    ref, mag = ox.combine(to_f64(k["Ys"]), slots, w_gpu)
+    _close(k["Y"], ref, half * np.abs(ref) + (1 + half) * (K + 1) * 2.0 ** -24 * mag + tiny)
+    dX, mag = lx.matmul(_bytes(k["dy"]), to_f64(k["dys"]), _bytes(layer.wt), to_f64(layer.wts), np.zeros((T * K, H)), off)
+    _close(k["dXs"], dX, half * np.abs(dX) + (1 + half) * (cut(mag) + 300 * 2.0 ** -24 * mag))
+    assert not to_f64(k["dXs"])[kept:].any()
+    dl, mag = lx.route_backward(to_f64(k["logits"]), ids, to_f64(k["dw"]), lx.SIGMOID, True, 2.5)
+    _close(k["dlogits"], dl, (4 * 40 + 128 + K) * 2.0 ** -24 * mag + tiny)
+    # the codes stand for what was quantised: within 2^-4 of it, or 2^-10 scales
+    for what, code, scale in (("X", "x", "xs"), ("dYs", "dy", "dys")):
+        src = to_f64(k[what])
+        s = np.repeat(to_f64(k[scale]), 128, 1)[:, :src.shape[1]]
+        assert np.all(np.abs(lx.decode(_bytes(k[code])) * s - src) <= np.maximum(2.0 ** -4 * np.abs(src), 2.0 ** -10 * s) * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("max_norm", [1e-4, 1e6])
+def test_layer_and_step(max_norm, bits):
+    dev = device()
+    say("router step", max_norm, bits)
+    layer = Layer(dev)
+    W0, router0, gains0 = layer.W.clone(), layer.router.clone(), layer.gains.clone()
+    copy = torch.zeros(E, H, dtype=torch.bfloat16, device=dev)
+    dense = L.AdamWList([layer.router, layer.gains], [layer.d_router, layer.d_gains], state_bits=bits, copies=[copy, None])
+    group = ExpertGroup(E, D, H, 50, K, layer.W, torch.full((E, D), 1e-6, device=dev), name="up")
+    st = Step([], R, T, B.LOGRA_BF16, groups=[group], adamw=dense)
+    seen = [{} for _ in range(MBS)]
+
+    def inputs(i, mb):                      # the layer runs where the step asks for its tensors
+        return layer.run(mb, seen[mb])
+
+    st.sketch(3, MBS, None, expert_inputs=inputs)
+    torch.cuda.synchronize()
+    for k in seen:
+        _check_stages(layer, k)
+    S = np.zeros((E, D, R))
+    d_router = np.zeros((E, H))
+    for k in seen:
+        off, order = k["offsets"].cpu().numpy(), k["order"].cpu().numpy()
+        X, dYs = to_f64(k["X"]), to_f64(k["dYs"])
+        for e in range(E):
+            a, b = off[e], off[e + 1]
+            if a < b:
+                S[e] += oracle.sketch([X[order[a:b] // K]], [dYs[a:b]], oracle.sign_matrix(0, 3, 50 + e, R, H))
+        d_router += to_f64(k["dlogits"]).T @ X
+    for e in range(E):
+        if np.abs(S[e]).max() > 0:
+            assert rownorm_err(to_f64(group.S[e]), S[e]) < BF16_TOL
+    assert rownorm_err(to_f64(layer.d_router), d_router) < 1e-5
+    grads = [to_f64(group.S), to_f64(layer.d_router), to_f64(layer.d_gains)]
+    norm = np.sqrt(sum((x ** 2).sum() for x in grads))
+    got, coef = st.clip(max_norm)
+    assert abs(float(got) / norm - 1) < 1e-6
+    c = min(1.0, max_norm / norm)
+    clipped = [layer.d_router.clone(), layer.d_gains.clone()]
+    for a, b in zip(clipped, grads[1:]):
+        assert np.allclose(to_f64(a), c * b, rtol=1e-6, atol=0)
+    st.pass1(0.99, 1e-8)
+    scales = st.finite_scales(st.sqnorms(), [1.0] * E)
+    st.pass2(1e-3, scales, 1e-8)
+    st.dense_update(1e-3, 0.9, 0.99, 1e-8, 0.1, 1)
+    for p, p0, g in ((layer.router, router0, clipped[0]), (layer.gains, gains0, clipped[1])):
+        ref, m64, v64, _, _ = lx.adamw(to_f64(p0), to_f64(g), 0 * to_f64(g), 0 * to_f64(g), 1e-3, 0.9, 0.99, 1e-8, 0.1, 1)
+        # the first update is 1e-3 at most, and its rounding is of that size
+        assert np.all(np.abs(to_f64(p) - ref) <= 2.0 ** -24 * np.abs(ref) + 2.0 ** -22 * 1e-4 * np.abs(to_f64(p0)) + 16 * 2.0 ** -24 * 1e-3)
+    assert torch.equal(copy, layer.router.to(torch.bfloat16))
+    # the experts moved by the estimate that the sketch gives
+    for e in range(E):
+        if np.abs(S[e]).max() == 0:
+            continue
+        ref = oracle.rowadam_rows(to_f64(group.S[e]), oracle.sign_matrix(0, 3, 50 + e, R, H), np.full(D, float(np.float32(1e-6))),
+                                  to_f64(W0[e]), beta2=float(np.float32(0.99)), eps=float(np.float32(1e-8)), lr=float(np.float32(1e-3)), scale=1.0)
+        assert w_update_err(to_f64(layer.W[e]), ref["W_new"], to_f64(W0[e])) < BF16_TOL
+    # and the next step runs on what they have become
+    layer.quantize()
+    layer.run(0, seen[0])
+    _check_stages(layer, seen[0])
+
+
+def test_a_step_that_is_not_finite_changes_nothing():
+    dev = device()
+    layer = Layer(dev, seed=2)
+    dense = L.AdamWList([layer.router], [layer.d_router], state_bits=8)
+    group = ExpertGroup(E, D, H, 50, K, layer.W, torch.full((E, D), 1e-6, device=dev))
+    st = Step([], R, T, B.LOGRA_BF16, groups=[group], adamw=dense)
+    st.sketch(1, 1, None, expert_inputs=lambda i, mb: layer.run(mb))
+    layer.d_router[2, 3] = float("nan")
+    before = layer.router.clone()
+    st.clip(1.0)
+    st.dense_update(1e-3, 0.9, 0.99, 1e-8, 0.1, 1)
+    assert torch.isnan(st.norm).all() and torch.equal(before, layer.router) and not dense.exp_avg.view(torch.uint8).any()
+
+
+def test_same_bits_again():
+    dev = device()
+    runs = []
+    for _ in range(2):
+        layer, keep = Layer(dev), {}
+        layer.run(0, keep)
+        runs.append([keep[n] for n in ("ids", "weights", "Ys", "Y", "dw", "dlogits", "dX")])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
