@@ -37,6 +37,7 @@ constexpr uint32_t kMmOob = 0x80000000u;      // past every buffer view: loads g
 constexpr int kMmK = 128;
 constexpr int kMmXcds = 8;
 constexpr int kMmGrid = 256;                   // one workgroup for each compute unit
+constexpr int kMmList = 64;                    // tiles in a workgroup's list
 
 // Operand of 128 k: a lane has 32 of the k of row L % 16 of A or of column
 // L % 16 of B (which ones does not matter as long as both have the same), as
@@ -133,50 +134,62 @@ __device__ __forceinline__ MmPlan mm_plan(const MatmulCall &c, int n_tn, int ban
     return p;
 }
 
-// The tile of workgroup id (any of 0 .. tiles n_tn - 1; workgroups take ids a
-// grid apart, which is a multiple of eight). Ids of one XCD (id mod 8) have
-// neighbouring tiles, `band` row tiles by as many feature tiles as there are
-// workgroups, so that they read the same rows of x and w through the XCD's
-// cache. False: none is left.
+// Numbers below 2^24 are divided in a few instructions where the compiler sees that they are.
+__device__ __forceinline__ uint32_t mm_div(uint32_t a, uint32_t b) { return (a & 0xFFFFFF) / (b & 0xFFFFFF); }
+
+// Tile id (any of 0 .. tiles n_tn - 1; workgroups take ids a grid apart, which
+// is a multiple of eight where there are several). Ids of one XCD (id mod 8)
+// have neighbouring tiles, `band` row tiles by as many feature tiles as there
+// are workgroups, so that they read the same rows of x and w through the XCD's
+// cache. Lanes may ask for different ids, all 64 together; no rows: no such
+// tile.
 template <int BM>
-__device__ __forceinline__ bool mm_tile(const MatmulCall &c, const MmPlan &p, uint32_t id, MmTile *out) {
+__device__ __forceinline__ MmTile mm_tile(const MatmulCall &c, const MmPlan &p, uint32_t id) {
     const uint32_t n_tn = p.n_tn, G = static_cast<uint32_t>(p.tiles) * n_tn;      // below 2^23
-    if (id >= G) return false;
+    const bool is = id < G;
+    if (!is) id = 0;
     const uint32_t share = G / kMmXcds, rest = G % kMmXcds, x = id % kMmXcds;
     const uint32_t q = x * share + min(x, rest) + id / kMmXcds;
-    const uint32_t group = q / (p.band * n_tn), in = q - group * p.band * n_tn;
-    const uint32_t high = min(static_cast<uint32_t>(p.band), p.tiles - group * p.band);      // the last band may be lower
-    const int tm = static_cast<int>(group * p.band + in % high);
-    out->tn = static_cast<int>(in / high);
+    const uint32_t group = mm_div(q, p.band * n_tn), in = q - group * p.band * n_tn;
+    const uint32_t high = max(min(p.band, p.tiles - static_cast<int>(group) * p.band), 1);      // the last band may be lower
+    const uint32_t tn = mm_div(in, high);
+    const int tm = static_cast<int>(group * p.band + in - tn * high);
+    MmTile t{0, 0, static_cast<int>(tn), static_cast<int64_t>(tm) * BM};
     if (!c.offsets) {
-        out->expert = 0;
-        out->row0 = static_cast<int64_t>(tm) * BM;
-        out->rows = static_cast<int>(min(static_cast<int64_t>(BM), c.M - out->row0));
-        return true;
+        if (is) t.rows = static_cast<int>(min(static_cast<int64_t>(BM), c.M - t.row0));
+        return t;
     }
-    // the lane whose experts hold the row tile, then the expert
-    const int from = __builtin_ctzll(__ballot(p.before + p.mine > tm));
-    int left = tm - __builtin_amdgcn_readlane(p.before, from);
-    for (int e = from * p.per;; ++e) {
+    // the first lane whose experts end behind the row tile, then the expert
+    int from = 0;
+#pragma unroll
+    for (int h = 32; h; h >>= 1)
+        if (__shfl(p.before + p.mine, from + h - 1) <= tm) from += h;
+    int left = tm - __shfl(p.before, from);
+    for (int e = from * p.per; e < min((from + 1) * p.per, c.E); ++e) {
         int64_t a, b;
         mm_rows_of(c, e, &a, &b);
         const int n = static_cast<int>((b - a + BM - 1) / BM);
-        if (left < n) {
-            out->expert = e;
-            out->row0 = a + static_cast<int64_t>(left) * BM;
-            out->rows = static_cast<int>(min(static_cast<int64_t>(BM), b - out->row0));
-            return true;
+        if (left >= 0 && left < n && is) {
+            t.expert = e;
+            t.row0 = a + static_cast<int64_t>(left) * BM;
+            t.rows = static_cast<int>(min(static_cast<int64_t>(BM), b - t.row0));
         }
         left -= n;
     }
+    return t;
 }
 
-// Row of x (and of its scales) that the tile's row r reads; -1: none.
-__device__ __forceinline__ int64_t mm_row(const MatmulCall &c, const MmTile &t, int r) {
+// A tile that all lanes have alike.
+__device__ __forceinline__ MmTile mm_uniform(const MmTile &t) {
+    return MmTile{__builtin_amdgcn_readfirstlane(t.expert), __builtin_amdgcn_readfirstlane(t.rows), __builtin_amdgcn_readfirstlane(t.tn),
+                  __builtin_amdgcn_readfirstlane(static_cast<int>(t.row0))};
+}
+
+// Row of x (and of its scales) that the tile's row r reads, with what the order
+// says of it; -1: none.
+__device__ __forceinline__ int64_t mm_row(const MatmulCall &c, const MmTile &t, int r, int p) {
     if (r >= t.rows) return -1;
-    const int64_t i = t.row0 + r;
-    if (!c.order) return i;
-    const int p = c.order[i];
+    if (!c.order) return t.row0 + r;
     const int row = p / c.topk;
     return p >= 0 && row < c.x_rows ? row : -1;
 }
@@ -233,7 +246,11 @@ __device__ __forceinline__ void mm_store8(const MatmulCall &c, int64_t row, int 
 //
 // A workgroup goes from tile to tile, and its loads run D - 1 blocks ahead of
 // its products, into the next tile too: its first blocks come while the last
-// ones of this tile are multiplied and its results are written.
+// ones of this tile are multiplied and its results are written. Nothing on the
+// way waits for a load of its own: a list in LDS holds the workgroup's next
+// tiles, and what the order says of a tile's rows comes into LDS a tile ahead.
+// (With both looked up where a tile began, 32768 rows of 128 experts, n 768, k
+// 2048, took 97 us, as many rows of one expert 67.)
 __device__ __forceinline__ int mm_swx(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int mm_sww(int r) { return (r >> 1 & 1) | (r >> 3 & 3) << 1; }
 
@@ -245,6 +262,11 @@ __device__ __forceinline__ i32x4_t mm_words(const void *p, int64_t bytes = 0x7FF
                    __builtin_amdgcn_readfirstlane(static_cast<int>(min(bytes, static_cast<int64_t>(0x7FFFFFFF)))), 0x00020000};
 }
 
+__device__ __forceinline__ i32x4_t mm_scalar(i32x4_t v) {
+    return i32x4_t{__builtin_amdgcn_readfirstlane(v[0]), __builtin_amdgcn_readfirstlane(v[1]), __builtin_amdgcn_readfirstlane(v[2]),
+                   __builtin_amdgcn_readfirstlane(v[3])};
+}
+
 // 16 bytes per lane from the view at off + step straight into LDS at `to`
 // (lane order; out of the view: zeros). Written out so that the compiler does
 // not wait for all of them at the next LDS read, as it does for the builtin
@@ -252,7 +274,15 @@ __device__ __forceinline__ i32x4_t mm_words(const void *p, int64_t bytes = 0x7FF
 __device__ __forceinline__ void mm_fetch(i32x4_t view, uint32_t to, uint32_t off, int step) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
-                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(view), "s"(__builtin_amdgcn_readfirstlane(step))
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(mm_scalar(view)), "s"(__builtin_amdgcn_readfirstlane(step))
+                 : "memory");
+}
+
+// The same of 4 bytes per lane.
+__device__ __forceinline__ void mm_fetch4(i32x4_t view, uint32_t to, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(mm_scalar(view))
                  : "memory");
 }
 
@@ -271,10 +301,12 @@ struct MmShape {
     static constexpr int WAVES = WM * WN, RT = BM / WM / 16, FT = BN / WN / 16;
     static constexpr int STAGE = (BM + BN) * kMmK;
     // scales of eight blocks of k: of the rows, then of the features' blocks
-    static constexpr int SCALES = BM * 32 + 1024;
+    static constexpr int SCALES = BM * 32 + BN / 4;
     static constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES;       // 1 KB loads of a wave for a block
     static constexpr int SI = (BM / 32 + WAVES - 1) / WAVES;             // and for eight blocks' scales
-    static constexpr int LDS = D * (STAGE + SCALES);
+    // the next tiles, and the order's entries of two tiles' rows
+    static constexpr int LIST = D * (STAGE + SCALES), ROWS = LIST + kMmList * 16, ROWS_EACH = (BM < 64 ? 64 : BM) * 4;
+    static constexpr int LDS = ROWS + 2 * ROWS_EACH;
     static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && 128 % (16 * FT) == 0, "whole loads, one scale");
     static_assert(LDS <= 160 * 1024 && (D - 2) * (XI + WI) < 64, "what a compute unit has, what a wait can count");
 };
@@ -289,18 +321,37 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const int kb = (c.K + kMmK - 1) / kMmK, nb = (c.N + 127) / 128;
-    const MmPlan plan = mm_plan<BM>(c, n_tn, band);
+    // tiles first .. first + count - 1 of this workgroup into the list
+    auto list_tiles = [&](int first, int count) {
+        const MmTile t = mm_tile<BM>(c, mm_plan<BM>(c, n_tn, band), blockIdx.x + gridDim.x * static_cast<uint32_t>(first + lane));
+        if (lane < count)
+            *reinterpret_cast<i32x4_t *>(lds + Sh::LIST + (first + lane) % kMmList * 16) = i32x4_t{t.expert, t.rows, t.tn, static_cast<int>(t.row0)};
+    };
+    auto tile = [&](int i) {
+        const i32x4_t v = *reinterpret_cast<const i32x4_t *>(lds + Sh::LIST + i % kMmList * 16);
+        return mm_uniform(MmTile{v[0], v[1], v[2], v[3]});
+    };
+    auto fetch_rows = [&](int i) {
+        const MmTile t = tile(i);
+        if (c.order && wave < (BM + 63) / 64 && t.rows)
+            mm_fetch4(mm_words(c.order + t.row0, 4 * t.rows), ring + Sh::ROWS + i % 2 * Sh::ROWS_EACH + wave * 256, 4 * (64 * wave + lane));
+    };
 
     // what is fetched: tile, block, and their places in the two rings
-    uint32_t f_id = blockIdx.x;
-    int f_b = 0, f_stage = 0, f_place = 0;
+    int f_i = 0, f_b = 0, f_stage = 0, f_place = 0;
     bool f_more;
     i32x4_t x_rs, xs_rs, w_rs, ws_rs;
     uint32_t x_off[XI], w_off[WI], xs_off[SI], ws_off;
     auto enter = [&]() {
-        MmTile t;
-        f_more = mm_tile<BM>(c, plan, f_id, &t);
+        // the list's half whose tiles are done; the others read it 16 tiles on
+        if (f_i % (kMmList / 2) == 16 && wave == 0) list_tiles(f_i + 16, kMmList / 2);
+        // its rows were asked for a tile before: with so few blocks they may not be here
+        if (kb < D) mm_wait<0>();
+        const MmTile t = tile(f_i);
+        f_more = t.rows > 0;
         if (!f_more) return;
+        const int *order = reinterpret_cast<const int *>(lds + Sh::ROWS + f_i % 2 * Sh::ROWS_EACH);
+        fetch_rows(f_i + 1);
         const int n0 = t.tn * BN;
         const int64_t base = mm_base(c, t);
         x_rs = mm_words(c.x + base * c.ldx);
@@ -312,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const int r = 8 * (XI * wave + i) + (lane >> 3);
-            const int64_t row = mm_row(c, t, r);
+            const int64_t row = mm_row(c, t, r, order[r]);
             x_off[i] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * c.ldx + 16 * ((lane & 7) ^ mm_swx(r)));
         }
 #pragma unroll
@@ -324,10 +375,10 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
 #pragma unroll
         for (int i = 0; i < SI; ++i) {
             const int r = 32 * (SI * wave + i) + (lane >> 1);
-            const int64_t row = r < BM ? mm_row(c, t, r) : -1;
+            const int64_t row = r < BM ? mm_row(c, t, r, order[r]) : -1;
             xs_off[i] = row < 0 ? kMmOob : static_cast<uint32_t>(((row - base) * kb + 4 * (lane & 1)) * 4);
         }
-        ws_off = (lane >> 1) < BN / 128 ? static_cast<uint32_t>(((lane >> 1) * kb + 4 * (lane & 1)) * 4) : kMmOob;
+        ws_off = static_cast<uint32_t>(((lane >> 1) * kb + 4 * (lane & 1)) * 4);
     };
     // The loads of a block in XI + WI pieces (behind the last tile: zeros, so
     // that every wait finds as many), and the scales before every eighth.
@@ -338,7 +389,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         for (int i = 0; i < SI; ++i)
             if (SI * Sh::WAVES * 32 == BM || SI * wave + i < BM / 32)
                 mm_fetch(xs_rs, to + (SI * wave + i) * 1024, xs_off[i], 4 * f_b);
-        if (wave == Sh::WAVES - 1) mm_fetch(ws_rs, to + BM * 32, ws_off, 4 * f_b);
+        if (wave == Sh::WAVES - 1 && lane < BN / 64) mm_fetch(ws_rs, to + BM * 32, ws_off, 4 * f_b);
     };
     auto fetch_piece = [&](int i) {
         const uint32_t to = ring + f_stage * Sh::STAGE;
@@ -358,7 +409,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         if ((f_b & 7) == 0 || f_b == kb) f_place = f_place + 1 == D ? 0 : f_place + 1;
         if (f_b == kb) {
             f_b = 0;
-            f_id += gridDim.x;
+            ++f_i;
             enter();
         }
     };
@@ -437,6 +488,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         }
     };
 
+    if (wave == 0) list_tiles(0, kMmList);
+    __syncthreads();
+    if (c.order) {
+        fetch_rows(0);
+        mm_wait<0>();
+    }
     enter();
     if (!f_more) return;
     for (int i = 0; i < D - 1; ++i) {
@@ -446,8 +503,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         fetched();
     }
     clear();
-    uint32_t id = blockIdx.x;
-    int b = 0, stage = 0, place = 0;
+    int i = 0, b = 0, stage = 0, place = 0;
     for (;;) {
         // this block's loads have landed (D - 2 blocks' are younger), and every
         // wave has read the block before, whose stage is filled next
@@ -459,11 +515,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         ++b;
         if ((b & 7) == 0 || b == kb) place = place + 1 == D ? 0 : place + 1;
         if (b == kb) {
-            MmTile o;
-            mm_tile<BM>(c, plan, id, &o);
-            write(o);
-            id += gridDim.x;
-            if (id >= static_cast<uint32_t>(plan.tiles) * n_tn) break;
+            write(tile(i));
+            if (!tile(++i).rows) break;
             clear();
             b = 0;
         }
@@ -480,8 +533,8 @@ template <int RT, int FT, int WAVES, int AHEAD, int BF16>
 __global__ __launch_bounds__(64 * WAVES) void mm_rows_kernel(MatmulCall c, int n_tn) {
     constexpr int WIDE = !BF16, BM = 16 * RT;
     __shared__ f32x4_t part[WAVES][FT][RT][64];
-    MmTile t;
-    if (!mm_tile<BM>(c, mm_plan<BM>(c, n_tn, 1), blockIdx.x, &t)) return;
+    const MmTile t = mm_uniform(mm_tile<BM>(c, mm_plan<BM>(c, n_tn, 1), blockIdx.x));
+    if (!t.rows) return;
     const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = t.tn * 16 * FT;
@@ -497,7 +550,8 @@ __global__ __launch_bounds__(64 * WAVES) void mm_rows_kernel(MatmulCall c, int n
         w_off[f] = n0 + 16 * f + i16 < c.N ? static_cast<uint32_t>(static_cast<int64_t>(16 * f + i16) * c.ldw + 32 * g) : kMmOob;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-        const int64_t row = mm_row(c, t, 16 * j + i16);
+        const int r = 16 * j + i16;
+        const int64_t row = mm_row(c, t, r, c.order && r < t.rows ? c.order[t.row0 + r] : 0);
         x_off[j] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * c.ldx + 32 * g);
         xs_off[j] = row < 0 ? kMmOob : static_cast<uint32_t>((row - base) * kb * 4);
     }

@@ -241,6 +241,40 @@ def test_matmul_experts_large(T, topk, E, n, k):
         _large_check(x.view(torch.uint8)[rows].view(F8), xs[rows], w[e], ws[e], y[off[e]:off[e + 1]], 2.0 ** -8)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,topk,E,n,k", [(1200000, 0, 0, 1024, 128), (4096, 8, 128, 768, 128), (4096, 8, 128, 768, 384), (60000, 4, 3, 1100, 640),
+                                          (2500, 8, 1000, 2048, 256)])
+def test_matmul_many_tiles(T, topk, E, n, k, dt):
+    """Workgroups with many tiles of few blocks of k, over 64 each in the first; codes -1, 0, 1, whose sums (up to 128 in bf16) are exact."""
+    dev = device()
+    if T > 10 ** 6 and dt == torch.float32:
+        n = 260
+    say("many tiles", T, topk, E, n, k, dt)
+    g = torch.Generator(device=dev).manual_seed(T + k)
+    few = 8 if k > 128 else 2                                   # one code in so many is not zero, so that the sums stay small
+    whole = lambda *s: (torch.randint(-1, 2, s, generator=g, device=dev) * (torch.randint(0, few, s, generator=g, device=dev) == 0)).to(torch.float32).to(F8)  # noqa: E731
+    x, w = whole(T, k), whole(max(E, 1), n, k)
+    kb, nb = -(-k // 128), -(-n // 128)
+    xs, ws = torch.ones(T, kb, device=dev), torch.ones(max(E, 1), nb, kb, device=dev)
+    M = T * max(topk, 1)
+    y = torch.full((M, n), 9.0, dtype=dt, device=dev)
+    if not E:
+        L.logra_fp8_matmul(x, xs, w[0], ws[0], y)
+        parts = [(0, M, torch.arange(M, device=dev))]
+    else:
+        ids = (E * torch.rand(T, topk, generator=g, device=dev) ** 2).int()
+        offsets, order, slots = (torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(M, dtype=torch.int32, device=dev),
+                                 torch.empty(T, topk, dtype=torch.int32, device=dev))
+        L.logra_expert_sort(ids, E, offsets, order, slots)
+        L.logra_fp8_matmul(x, xs, w, ws, y, offsets=offsets, order=order, topk=topk)
+        off = offsets.tolist()
+        parts = [(off[e], off[e + 1], (order[off[e]:off[e + 1]] // topk).long()) for e in range(E)]
+    for e, (a, b, rows) in enumerate(parts):
+        want = x.view(torch.uint8)[rows].view(F8).float() @ w[e].float().t()
+        assert b == a or float(want.abs().max()) <= 256
+        assert torch.equal(y[a:b], want.to(dt)), e
+
+
 def test_matmul_odd_offsets_and_orders():
     """Experts without rows, all rows of one, offsets and orders that reach outside."""
     dev = device()
