@@ -1075,7 +1075,14 @@ class AdamWList:
         return len(now) == len(then) and all(
             a is b and GradList._description(b) == d for a, b, d in zip(then, now, self._described))
 
-    _used_on = GradList._used_on
+    def _used_on(self, dev, stream, handle):
+        """Neither the table's memory nor the state's goes to other use before
+        this stream's work is over."""
+        if handle not in self.streams:
+            on = _stream_object(dev, stream, handle)
+            for t in (self.table, self.exp_avg, self.exp_avg_sq) + (() if self.scales is None else (self.scales,)):
+                t.record_stream(on)
+            self.streams.add(handle)
 
 
 def logra_adamw(tensors: AdamWList, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float, step: int,

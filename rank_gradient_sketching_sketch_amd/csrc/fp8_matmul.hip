@@ -631,9 +631,13 @@ static void mm_tiles(const MatmulCall &c, int band, hipStream_t st) {
     hipLaunchKernelGGL((mm_tile_kernel<BM, BN, WM, WN, D, BF16>), grid, block, 0, st, c, n_tn, band);
 }
 
-// A launch has fewer than 2^32 threads; the smallest tiles are 16 x 16 of 256.
+// Tiles are numbered below 2^23: those of 32 x 128 at least, and of 16 x 16
+// where an expert has so few rows.
+constexpr int64_t kMmTiles = 1ll << 23;
+static bool mm_few_rows(int64_t M, int E) { return (E ? (M + E - 1) / E : M) <= 16; }
 bool fp8_matmul_fits(int64_t M, int64_t N, int E) {
-    return mm_row_tiles(M, E, 16) < (1ll << 23) / ((N + 15) / 16);
+    if (mm_few_rows(M, E) && mm_row_tiles(M, E, 16) >= kMmTiles / ((N + 15) / 16)) return false;
+    return mm_row_tiles(M, E, 32) < kMmTiles / ((N + 127) / 128);
 }
 
 // Which kernel: the one expected to be done first. A product's tiles go to the
@@ -653,7 +657,7 @@ struct MmShapeTime {
 constexpr MmShapeTime kMmTimes[] = {{32, 128, 0.55, 1.5}, {64, 128, 0.66, 2.0}, {128, 128, 0.78, 2.5}, {128, 256, 1.12, 3.0}, {256, 256, 1.72, 4.0}};
 
 hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
-    const int64_t per = c.offsets ? (c.M + c.E - 1) / c.E : c.M;     // rows of an expert
+    const int experts = c.offsets ? c.E : 0;
     const double kb = (c.K + kMmK - 1) / kMmK;
     // row tiles: with experts, half of one is left over at each
     const auto row_tiles = [&](int bm) {
@@ -661,18 +665,18 @@ hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
                          : static_cast<double>((c.M + bm - 1) / bm);
     };
     const int band = c.offsets ? 2 : 8;
-    if (per <= 16) {
+    if (mm_few_rows(c.M, experts)) {
         // one block of features for a workgroup while few rows make few loads
         // of x (n 18944, k 3584: 1 row 13.6 us with one, 15.2 with two; 16 rows
         // 19.8 and 18.5; 64 tokens to 8 of 128 experts 45 and 37) or there are few
         // workgroups (n 1536, k 8960: 1 row 8.7 and 12.1)
         const bool one = c.N < 8192 && !c.offsets;
-        if (one || (!c.offsets && per <= 8)) c.y_bf16 ? mm_rows<1, 1, 4, 8, 1>(c, st) : mm_rows<1, 1, 4, 8, 0>(c, st);
+        if (one || (!c.offsets && c.M <= 8)) c.y_bf16 ? mm_rows<1, 1, 4, 8, 1>(c, st) : mm_rows<1, 1, 4, 8, 0>(c, st);
         else c.y_bf16 ? mm_rows<1, 2, 4, 4, 1>(c, st) : mm_rows<1, 2, 4, 4, 0>(c, st);
         return hipGetLastError();
     }
     const double wgs = row_tiles(32) * ((c.N + 15) / 16);
-    double best = kb * (wgs < 180 ? 0.15 : 0.00085 * wgs);
+    double best = mm_row_tiles(c.M, experts, 32) < kMmTiles / ((c.N + 15) / 16) ? kb * (wgs < 180 ? 0.15 : 0.00085 * wgs) : INFINITY;
     int which = -1;
     for (int i = 0; i < (c.y_bf16 ? 5 : 3); ++i) {
         const MmShapeTime &m = kMmTimes[i];

@@ -228,6 +228,28 @@ def test_resume_streams_and_graph(bits):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_list_dropped_while_its_step_runs(bits):
+    """The memory of table and state is not given to other tensors before the stream's step is over."""
+    dev = device()
+    model = Model(11, [(1 << 22,)], dev, bits=bits, state=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50000000)
+    L.logra_adamw(model.list, 1e-3, 0.9, 0.99, 1e-8, 0.1, 1, stream=side)
+    kept = [t for t in (model.list.table, model.list.exp_avg, model.list.exp_avg_sq, model.list.scales) if t is not None]
+    old = {t.data_ptr() for t in kept}
+    sizes = [t.numel() * t.element_size() for t in kept]
+    model.list = None
+    del kept
+    new = [torch.full((n,), 255, dtype=torch.uint8, device=dev) for n in sizes]
+    busy = not side.query()
+    assert not busy or not old & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    assert busy and bool(torch.isfinite(model.p[0]).all())
+
+
 def test_list_refusals():
     dev = device()
     p, g = torch.zeros(8, device=dev), torch.zeros(8, device=dev)

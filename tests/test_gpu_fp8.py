@@ -275,6 +275,45 @@ def test_matmul_many_tiles(T, topk, E, n, k, dt):
         assert torch.equal(y[a:b], want.to(dt)), e
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 16, 100, 256])
+def test_matmul_every_code(rows, dt):
+    """Each code times one, and one times each code, subnormal codes too: exact (a NaN code: NaN in its row or feature)."""
+    dev = device()
+    k = 256
+    codes = torch.arange(256, dtype=torch.uint8, device=dev)
+    value = codes.view(F8).float()
+    one = torch.ones(1, device=dev).to(F8).view(torch.uint8)
+    for a in range(0, 256, rows):
+        code = codes[a:a + rows]
+        x = torch.zeros(len(code), k, dtype=torch.uint8, device=dev)
+        x[torch.arange(len(code)), (37 * codes[a:a + rows].long() + 5) % k] = code
+        w = one.expand(20, k).contiguous()
+        s = lambda *n: torch.ones(*n, device=dev)  # noqa: E731
+        y = torch.empty(len(code), 20, dtype=dt, device=dev)
+        L.logra_fp8_matmul(x.view(F8), s(len(code), 2), w.view(F8), s(1, 2), y)
+        assert torch.equal(torch.nan_to_num(y.float(), nan=7e7), torch.nan_to_num(value[a:a + rows, None], nan=7e7).expand(-1, 20))
+    w = torch.zeros(256, k, dtype=torch.uint8, device=dev)
+    w[torch.arange(256), (53 * codes.long() + 11) % k] = codes
+    x = one.expand(rows, k).contiguous()
+    y = torch.empty(rows, 256, dtype=dt, device=dev)
+    L.logra_fp8_matmul(x.view(F8), torch.ones(rows, 2, device=dev), w.view(F8), torch.ones(2, 2, device=dev), y)
+    assert torch.equal(torch.nan_to_num(y.float(), nan=7e7), torch.nan_to_num(value, nan=7e7).expand(rows, -1))
+
+
+def test_matmul_output_past_32_bits():
+    """More than 2^31 results, and past 2^32 bytes of them."""
+    dev = device()
+    M, n, k = 70001, 40004, 16
+    say("output past 32 bits")
+    g = torch.Generator(device=dev).manual_seed(1)
+    x, w = (torch.randint(-2, 3, s, generator=g, device=dev).float().to(F8) for s in ((M, k), (n, k)))
+    y = torch.full((M, n), 9.0, dtype=torch.bfloat16, device=dev)
+    L.logra_fp8_matmul(x, torch.ones(M, 1, device=dev), w, torch.ones(-(-n // 128), 1, device=dev), y)
+    for a in range(0, M, 8000):
+        assert torch.equal(y[a:a + 8000], (x[a:a + 8000].float() @ w.float().t()).to(torch.bfloat16)), a
+
+
 def test_matmul_odd_offsets_and_orders():
     """Experts without rows, all rows of one, offsets and orders that reach outside."""
     dev = device()
