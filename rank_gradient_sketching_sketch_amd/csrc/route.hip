@@ -15,10 +15,17 @@
 // Choices are whole numbers that must not hang on rounding: they are those of
 // keys formed and compared in fp64. Where no bias and no sum of two keys
 // enters, the logits themselves are compared, which sort like their scores.
-// Otherwise fp32 keys are tried first, with what they may be off by: only a
-// token of which two keys (or sums) that had to be told apart are nearer than
-// that takes the fp64 ones. Weights are fp32, as ratios of exponentials of
-// differences that cannot overflow or all vanish.
+// Otherwise fp32 keys are tried first, with what they may be off by: only
+// where two keys that had to be told apart are nearer than that are fp64 ones
+// formed, of the few experts in question (sigmoid) or of all (softmax, and
+// groups in doubt). Weights are fp32, as ratios of exponentials of differences
+// that cannot overflow or all vanish.
+//
+// A wave per token: up to some thousand tokens the time is one wave's chain of
+// choices, not memory (4 MB of logits are 1 us). 4096 tokens to 8 of 256
+// experts, four of eight groups: 9.2 us (a token or two in doubt, at the end of
+// it all, are 1.7 of them), 10.6 with fp64 keys for all; 16384 tokens 22.9 and
+// 29.1; 65536 tokens 75 and 96.
 #include <math.h>
 
 #include <type_traits>
@@ -167,13 +174,18 @@ struct RouteDoubt {
     }
 };
 
+__device__ __forceinline__ double route_sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
+
 // Which experts the lanes' keys lead to: lane j gets choice j, or -1.
-// CHECK: false where two keys that had to be told apart are in doubt.
+// CHECK: what could not be told. In doubt about choices, lane j has the j-th
+// highest key's expert of `found`, which are all that can be among the choices.
+enum RouteTold { kRouteAll, kRouteNotOrder, kRouteNothing };
 template <class P, bool CHECK, int N>
-__device__ __forceinline__ bool route_choose(const RouteArgs &a, typename P::Key (&key)[N], int e0, RouteDoubt doubt,
-                                             int *my_id) {
+__device__ __forceinline__ RouteTold route_choose(const RouteArgs &a, typename P::Key (&key)[N], int e0, RouteDoubt doubt,
+                                                  int *my_id, int *found) {
     using Key = typename P::Key;
     const int lane = threadIdx.x & 63;
+    *my_id = -1;
     if (a.groups > 1) {
         const int group = lane / a.span;
         Key one = P::none(), two = P::none();
@@ -196,10 +208,9 @@ __device__ __forceinline__ bool route_choose(const RouteArgs &a, typename P::Key
         const bool out = better >= a.kept;
         if constexpr (CHECK) {
             // the lowest sum that stays against the highest that does not
-            const float f = sum > P::none() ? P::value(sum) : -INFINITY;
-            const float low = -wave_max_f32(out || group >= a.groups ? -INFINITY : -f);
-            const float high = wave_max_f32(out ? f : -INFINITY);
-            if (high > -INFINITY && doubt.near(low, high, 2.f)) return false;
+            const Key low = P::lane(sum, __builtin_ctzll(__ballot(better == a.kept - 1)));
+            const Key high = P::lane(sum, __builtin_ctzll(__ballot(better == a.kept)));
+            if (high > P::none() && doubt.near(P::value(low), P::value(high), 2.f)) return kRouteNothing;
         }
         if (out) {
 #pragma unroll
@@ -208,9 +219,9 @@ __device__ __forceinline__ bool route_choose(const RouteArgs &a, typename P::Key
     }
     // choice by choice: the largest of the lanes' largest, in the lowest lane
     // that holds it
-    *my_id = -1;
-    float before = INFINITY;
-    for (int j = 0; j < a.K + (CHECK ? 1 : 0); ++j) {
+    float value = -INFINITY;        // lane j: of choice j
+    int id = -1;
+    auto next = [&](int j, Key *most) {
         Key best = key[0];
         int at = 0;
 #pragma unroll
@@ -219,21 +230,58 @@ __device__ __forceinline__ bool route_choose(const RouteArgs &a, typename P::Key
             best = more ? key[i] : best;
             at = more ? i : at;
         }
-        const Key most = P::over_wave(best);
-        if (!(most > P::none())) break;
-        if constexpr (CHECK) {
-            const float value = P::value(most);
-            if (j > 0 && doubt.near(before, value, 1.f)) return false;
-            before = value;
+        *most = P::over_wave(best);
+        if (!(*most > P::none())) return false;
+        const int from = __builtin_ctzll(__ballot(best == *most));
+        const int e = static_cast<int>(lane_u32(static_cast<uint32_t>(e0 + at), from));
+        if (lane == j) {
+            id = e;
+            if constexpr (CHECK) value = P::value(*most);
         }
-        const int from = __builtin_ctzll(__ballot(best == most));
-        const int id = static_cast<int>(lane_u32(static_cast<uint32_t>(e0 + at), from));
-        if (lane == j && j < a.K) *my_id = id;
         const int taken = lane == from ? at : -1;
 #pragma unroll
         for (int i = 0; i < N; ++i) key[i] = i == taken ? P::none() : key[i];
+        return true;
+    };
+    Key most;
+    int j = 0;
+    while (j < a.K && next(j, &most)) ++j;
+    *my_id = id;
+    if constexpr (CHECK) {
+        const float before = dpp_f32<0x138, 0xF>(value, value);      // the lane before's
+        bool close = __ballot(lane > 0 && lane < j && doubt.near(before, value, 1.f)) != 0;
+        if (j == a.K) {
+            // the experts that may come before the last choice
+            const float last = lane_f32(value, a.K - 1);
+            while (next(j, &most) && doubt.near(last, P::value(most), 1.f)) {
+                close = true;
+                if (++j > min(a.K + 8, 64)) return kRouteNothing;      // many alike, as where a router starts from zeros
+            }
+        }
+        *my_id = lane < j ? id : -1;
+        *found = j;
+        return close ? kRouteNotOrder : kRouteAll;
     }
-    return true;
+    return kRouteAll;
+}
+
+// The order of `found` experts, one in each of the first lanes, by keys of
+// sigmoids in fp64; lane j gets choice j.
+template <int BF16>
+__device__ __forceinline__ int route_order(const RouteArgs &a, int64_t t, int id, int found) {
+    const int lane = threadIdx.x & 63;
+    double key = ScoreKey::none();
+    if (lane < found) key = route_sigmoid(route_logit<BF16>(a.logits, t * a.ld + id)) + (a.bias ? static_cast<double>(a.bias[id]) : 0.0);
+    int rank = 0;
+    for (int i = 0; i < found; ++i) {
+        const double k = lane_f64(key, i);
+        rank += k > key || (k == key && static_cast<int>(lane_u32(static_cast<uint32_t>(id), i)) < id);
+    }
+    int out = -1;
+    for (int i = 0; i < found; ++i)
+        if (lane == static_cast<int>(lane_u32(static_cast<uint32_t>(rank), i)) && lane < a.K)
+            out = static_cast<int>(lane_u32(static_cast<uint32_t>(id), i));
+    return out;
 }
 
 // A wave per token. The lanes are dealt to the groups (span of them each, a
@@ -271,7 +319,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         denom = wave_sum_f32(denom);
     }
 
-    int my_id;
+    int my_id, found;
     if constexpr (SCORES) {
         float bias[N];
         uint32_t key[N];
@@ -288,12 +336,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         // score), the exponential, up to N + 6 roundings of the sum (2^-18.7
         // with N = 32) and the quotient: 2^-18 of the largest score for two.
         const RouteDoubt doubt{a.sigmoid ? 0x1p-21f : 0x1p-18f / denom};
-        if (!route_choose<FloatKey, true>(a, key, e0, doubt, &my_id)) {
+        const RouteTold told = route_choose<FloatKey, true>(a, key, e0, doubt, &my_id, &found);
+        if (told == kRouteNotOrder && a.sigmoid) {
+            my_id = route_order<BF16>(a, t, my_id, found);
+        } else if (told != kRouteAll) {
             double wide[N], sum = 0.0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const double d = x[i];
-                wide[i] = x[i] > -INFINITY ? (a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - static_cast<double>(top))) : 0.0;
+                wide[i] = x[i] > -INFINITY ? (a.sigmoid ? route_sigmoid(d) : exp(d - static_cast<double>(top))) : 0.0;
                 sum += wide[i];
             }
             if (!a.sigmoid) sum = wave_sum_f64(sum);
@@ -303,13 +354,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
                 const double k = wide[i] + static_cast<double>(bias[i]);
                 wide[i] = x[i] > -INFINITY && k == k ? k : ScoreKey::none();
             }
-            route_choose<ScoreKey, false>(a, wide, e0, doubt, &my_id);
+            route_choose<ScoreKey, false>(a, wide, e0, doubt, &my_id, &found);
         }
     } else {
         uint32_t key[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) key[i] = FloatKey::of(x[i]);
-        route_choose<FloatKey, false>(a, key, e0, RouteDoubt{0.f}, &my_id);
+        route_choose<FloatKey, false>(a, key, e0, RouteDoubt{0.f}, &my_id, &found);
     }
 
     const bool chosen = my_id >= 0;
@@ -358,7 +409,8 @@ struct RouteBackwardArgs {
 // Which choice an expert has is looked up in a row of bytes per wave: every
 // choice writes its lane there and reads it back, and only where one finds
 // another's lane (an expert chosen twice) are the choices gone through one by
-// one.
+// one (16384 tokens, 8 of 128 experts: 7.7 us; going through them always 9.3).
+// The rows read and written are 16.8 MB, 3.4 us at a copy's rate.
 template <int N, int BF16>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackwardArgs a) {
     __shared__ uint8_t owner[kRouteTokens][64 * N];

@@ -91,6 +91,35 @@ def test_route_groups(groups, E, kept, best):
             _check(x, K, score, bias, groups=groups, topk_groups=kept, group_best=best, renormalize=True)
 
 
+@pytest.mark.parametrize("alike", [2, 3, 9, 15, 16, 17, 40, 256])
+@pytest.mark.parametrize("K", [1, 7, 8, 60, 64])
+def test_route_keys_that_fp32_cannot_tell(K, alike):
+    """Some experts' keys within fp32 rounding of each other, above or below others; some equal; ids stay those of fp64 keys."""
+    dev = device()
+    E, T = 256, 48
+    g = np.random.default_rng(K * 1000 + alike)
+    bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+    x = (g.standard_normal((T, E)) - 2.0).astype(np.float32)
+    for t in range(T):
+        pick = g.choice(E, alike, replace=False)
+        c = 0.5 + 0.1 * g.random()
+        s = c - bias[pick].astype(np.float64)
+        x[t, pick] = np.log(s / (1 - s)).astype(np.float32)
+        x[t, pick[:alike // 3]] = np.nextafter(x[t, pick[:alike // 3]], np.float32(9))
+        rest = np.setdiff1d(np.arange(E), pick)
+        up = g.choice(rest, min(len(rest), t % 12), replace=False)
+        x[t, up] += 5.0
+    x[T - 2:] = x[T - 2:, :1]                                   # all logits equal
+    y = x.copy()
+    y[:, 1::2] = y[:, ::2]                                      # and pairs of equal keys
+    twice = bias.copy()
+    twice[1::2] = twice[::2]
+    for logits, b in ((x, bias), (y, twice), (y, np.zeros_like(bias))):
+        for kw in (dict(), dict(groups=8, topk_groups=4, group_best=2)):
+            _check(torch.from_numpy(logits).to(dev), K, ox.SIGMOID, torch.from_numpy(b).to(dev), renormalize=True, **kw)
+    _check(torch.from_numpy(x).to(dev), K, ox.SOFTMAX, torch.from_numpy(bias).to(dev), renormalize=True)
+
+
 @pytest.mark.parametrize("score", [ox.SOFTMAX, ox.SIGMOID])
 def test_route_edges(score):
     dev = device()
