@@ -950,11 +950,12 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
  *     mix(key + (j + 1) 0x9E3779B97F4A7C15), key of (seed, step, matrix_id
  *     2^64 - 1), see the top of this file. A root above zero keeps at least
  *     the smallest code.
+ *   eps 0: an element whose moments are both zero becomes NaN (0 / 0).
  *   step: 1 for the first step; it must grow by one with every step that is
  *   applied, and must not repeat (the rounding's chances would).
  * Errors of pack: as logra_grad_list_pack. Errors of the step:
  *   INVALID_ARGUMENT (nulls, misaligned table or moments (16 bytes), lr, eps or
- *   weight_decay not finite, eps < 0, betas outside [0, 1), step 0, max_norm
+ *   weight_decay not finite, eps < 0 or subnormal in fp32, betas outside [0, 1), step 0, max_norm
  *   negative or NaN), UNSUPPORTED (state_bits), HIP.
  */
 typedef struct logra_adamw_tensor {

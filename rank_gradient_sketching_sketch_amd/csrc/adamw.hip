@@ -24,8 +24,8 @@
 //
 // Bound by memory: parameters and moments read and written once, gradients
 // read, copies written. 49 M elements, fp32: 256 us, 5.4 TB/s; 115 M with bf16
-// gradients and copies and moments in 8 bits (16.03 bytes an element): 363 us,
-// 5.1 TB/s, 396 with square root and division instructions.
+// gradients and copies and moments in 8 bits (16.06 bytes an element): 363 us,
+// 5.1 TB/s.
 #include <math.h>
 
 #include <type_traits>

@@ -1139,7 +1139,7 @@ logra_status logra_adamw(const logra_adamw_list *list, int state_bits, void *exp
         return LOGRA_ERR_INVALID_ARGUMENT;
     if (state_bits != 8 && state_bits != 32) return LOGRA_ERR_UNSUPPORTED;
     if (!isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
-        !isfinite(eps) || !isfinite(weight_decay) || step < 1 || !aligned_to(norm, 4) || !(max_norm >= 0.0))
+        !isfinite(eps) || (eps > 0.0 && eps < 0x1p-126) || !isfinite(weight_decay) || step < 1 || !aligned_to(norm, 4) || !(max_norm >= 0.0))
         return LOGRA_ERR_INVALID_ARGUMENT;
     if (list->blocks == 0) return LOGRA_OK;
     if (!exp_avg || !aligned16(exp_avg) || !exp_avg_sq || !aligned16(exp_avg_sq) || exp_avg == exp_avg_sq ||

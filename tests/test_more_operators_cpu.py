@@ -136,7 +136,7 @@ def test_adamw_refusals(B):
     nan, inf = float("nan"), float("inf")
     for kw in (dict(list=None), dict(list=ctypes.byref(odd)), dict(m=None), dict(v=None), dict(m=EIGHT), dict(v=EIGHT), dict(v=FAKE),
                dict(s=None), dict(s=HALF), dict(lr=nan), dict(lr=inf), dict(b1=1.0), dict(b1=-0.1), dict(b1=nan), dict(b2=1.0),
-               dict(b2=nan), dict(eps=-1e-9), dict(eps=nan), dict(eps=inf), dict(wd=nan), dict(step=0), dict(norm=HALF),
+               dict(b2=nan), dict(eps=-1e-9), dict(eps=1e-40), dict(eps=nan), dict(eps=inf), dict(wd=nan), dict(step=0), dict(norm=HALF),
                dict(most=-1.0), dict(most=nan)):
         assert f(**kw) == BAD, kw
     assert f(bits=16) == UNSUP
