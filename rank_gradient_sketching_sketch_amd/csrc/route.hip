@@ -409,7 +409,7 @@ struct RouteBackwardArgs {
 // Which choice an expert has is looked up in a row of bytes per wave: every
 // choice writes its lane there and reads it back, and only where one finds
 // another's lane (an expert chosen twice) are the choices gone through one by
-// one (16384 tokens, 8 of 128 experts: 7.7 us; going through them always 9.3).
+// one (16384 tokens, 8 of 128 experts: 7.2 us; going through them always 9.3).
 // The rows read and written are 16.8 MB, 3.4 us at a copy's rate.
 template <int N, int BF16>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackwardArgs a) {
@@ -417,22 +417,28 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBack
     const int lane = threadIdx.x & 63;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteTokens + (threadIdx.x >> 6);
     if (t >= a.T) return;
+    const bool whole = !a.sigmoid && !a.renorm;
+    // what does not hang on the ids is asked for with them (65536 tokens of 128
+    // experts 21.3 -> 19.2 us)
     int id = lane < a.K ? a.ids[t * a.K + lane] : -1;
+    const float dw = lane < a.K ? a.dw[t * a.K + lane] : 0.f;
+    float row[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = -INFINITY;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane + 64 * i < a.E) row[i] = route_logit<BF16>(a.logits, t * a.ld + lane + 64 * i);
+    }
     id = id >= 0 && id < a.E ? id : -1;
     const bool chosen = id >= 0;
     const float x = chosen ? route_logit<BF16>(a.logits, t * a.ld + id) : -INFINITY;
-    const float g = chosen ? a.scale * a.dw[t * a.K + lane] : 0.f;
-    const bool whole = !a.sigmoid && !a.renorm;
-    float row[N];
+    const float g = chosen ? a.scale * dw : 0.f;
     float q;
     if (whole) {
         float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = lane + 64 * i;
-            row[i] = e < a.E ? route_logit<BF16>(a.logits, t * a.ld + e) : -INFINITY;
-            top = fmaxf(top, row[i]);
-        }
+        for (int i = 0; i < N; ++i) top = fmaxf(top, row[i]);
         top = wave_max_f32(top);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
