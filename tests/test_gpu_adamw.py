@@ -250,6 +250,28 @@ def test_a_list_dropped_while_its_step_runs(bits):
     assert busy and bool(torch.isfinite(model.p[0]).all())
 
 
+def test_elements_past_32_bits():
+    """A tensor of more than 2^31 elements, the second of its list: places at its ends and around 2^31 as in a list of their own."""
+    dev = device()
+    say("adamw past 32 bits")
+    n, hyper = (1 << 31) + 3000, (1e-3, 0.9, 0.99, 1e-8, 0.1)
+    g = torch.Generator(device=dev).manual_seed(3)
+    p = torch.empty(n, device=dev).normal_(generator=g)
+    d = torch.empty(n, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    spans = [(0, 1000), ((1 << 31) - 700, (1 << 31) + 800), (n - 1001, n)]
+    small = [p[a:b].clone() for a, b in spans]
+    grads = [d[a:b].clone() for a, b in spans]
+    one, oned = torch.ones(5, device=dev), torch.ones(5, device=dev)
+    big = L.AdamWList([one, p], [oned, d])
+    few = L.AdamWList(small, grads)
+    for step in (1, 2):
+        L.logra_adamw(big, *hyper, step)
+        L.logra_adamw(few, *hyper, step)
+    for (a, b), t in zip(spans, small):
+        assert torch.equal(p[a:b], t)
+    assert not torch.equal(small[0], torch.ones_like(small[0])) and big.first == [0, 1]
+
+
 def test_list_refusals():
     dev = device()
     p, g = torch.zeros(8, device=dev), torch.zeros(8, device=dev)

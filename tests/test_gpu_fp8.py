@@ -100,6 +100,27 @@ def test_quantize_edges():
     assert scales[0].tolist() == [1.0, 1.0] and not _bytes(codes)[0].any()
 
 
+def test_quantize_past_32_bits():
+    """More than 2^31 elements: the last rows and arrays as by themselves."""
+    dev = device()
+    say("quantize past 32 bits")
+    g = torch.Generator(device=dev).manual_seed(5)
+    x = torch.empty(66000, 33000, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    kb = 258
+    codes, scales = torch.zeros(66000, 33000, dtype=torch.uint8, device=dev).view(F8), torch.zeros(66000, kb, device=dev)
+    L.logra_fp8_quantize(x, codes, scales)
+    for a, b in ((0, 50), (65000, 65100), (65950, 66000)):
+        c, s = torch.zeros(b - a, 33000, dtype=torch.uint8, device=dev).view(F8), torch.zeros(b - a, kb, device=dev)
+        L.logra_fp8_quantize(x[a:b], c, s)
+        assert torch.equal(codes[a:b].view(torch.uint8), c.view(torch.uint8)) and torch.equal(scales[a:b], s)
+    turned, ts = torch.zeros(33000, 66000, dtype=torch.uint8, device=dev).view(F8), torch.zeros(kb, 516, device=dev)
+    L.logra_fp8_quantize(x, turned, ts, block_rows=128, transpose=True)
+    a = 66000 // 128 * 128 - 128
+    c, s = torch.zeros(33000, 66000 - a, dtype=torch.uint8, device=dev).view(F8), torch.zeros(kb, -(-(66000 - a) // 128), device=dev)
+    L.logra_fp8_quantize(x[a:], c, s, block_rows=128, transpose=True)
+    assert torch.equal(turned[:, a:].contiguous().view(torch.uint8), c.view(torch.uint8)) and torch.equal(ts[:, a // 128:], s)
+
+
 def _operands(seed, rows, k, E, n, dev, whole=False, padx=0, padw=0):
     g = torch.Generator().manual_seed(seed)
     kb, nb = -(-k // 128), -(-n // 128)
