@@ -898,8 +898,7 @@ logra_status logra_route_backward(int64_t T, int n_experts, int topk, int dtype,
  *   k, ldx, ldw multiples of 16; x, w 16-byte aligned; arrays of w follow
  *   each other after n row strides; n and M as they are.
  * Limits: M <= 2^26, n, k, ldx, ldw <= 2^22, n_experts <= 1024; with order x
- *   (x_rows ldx codes) below 2^31 bytes; Y in fewer than 2^23 tiles of 32 x 128
- *   (of 16 x 16 where an expert has 16 rows or fewer on average).
+ *   (x_rows ldx codes) below 2^31 bytes; Y in fewer than 2^23 tiles of 32 x 128.
  * Errors: INVALID_ARGUMENT (nulls with something to do, sizes, ld,
  *   misalignment, order without offsets, topk < 1), UNSUPPORTED (dtype,
  *   k % 16, limits), HIP.

@@ -635,64 +635,76 @@ static void mm_tiles(const MatmulCall &c, int band, hipStream_t st) {
     hipLaunchKernelGGL((mm_tile_kernel<BM, BN, WM, WN, D, BF16>), grid, block, 0, st, c, n_tn, band);
 }
 
-// Tiles are numbered below 2^23: those of 32 x 128 at least, and of 16 x 16
-// where an expert has so few rows.
+// Tiles are numbered below 2^23, those of 32 x 128 at least.
 constexpr int64_t kMmTiles = 1ll << 23;
-static bool mm_few_rows(int64_t M, int E) { return (E ? (M + E - 1) / E : M) <= 16; }
-bool fp8_matmul_fits(int64_t M, int64_t N, int E) {
-    if (mm_few_rows(M, E) && mm_row_tiles(M, E, 16) >= kMmTiles / ((N + 15) / 16)) return false;
-    return mm_row_tiles(M, E, 32) < kMmTiles / ((N + 127) / 128);
-}
+bool fp8_matmul_fits(int64_t M, int64_t N, int E) { return mm_row_tiles(M, E, 32) < kMmTiles / ((N + 127) / 128); }
 
 // Which kernel: the one expected to be done first. A product's tiles go to the
-// compute units in rounds, and a round takes a start and a step per block of
-// k; both were measured for each shape (us; fp32 results take the shapes up to
-// 128 x 128 with the same steps). Measured, us: 4096 rows of 3584 by 18944 features 275
-// in 256 x 256 tiles, 335 in 128 x 256; 256 rows 49 and 34; 128 rows 33 in 128 x
-// 256, 24 in 128 x 128; 64 rows 23 in 128 x 128, 20 in 64 x 128; 24 rows 20 in 64 x
-// 128, 17 in 32 x 128, 24.6 in rows of 32. 1536 features of k 8960: 512 rows 51 in
-// 128 x 128, 43 in 64 x 128, 36 in 32 x 128; 64 rows 36 in 32 x 128, 16 in rows
-// of 32. The rows kernels read w past the LDS and split k over the waves:
-// their time follows the blocks a compute unit has to stream.
+// compute units in rounds, and a round takes a start (the results' stores) and a
+// step per block of k; both were measured for each shape (us; fp32 results take
+// the shapes up to 128 x 128 with the same steps). Measured, us: 4096 rows of
+// 3584 by 18944 features 275 in 256 x 256 tiles, 335 in 128 x 256; 256 rows 49 and
+// 34; 128 rows 33 in 128 x 256, 24 in 128 x 128; 64 rows 23 in 128 x 128, 20 in
+// 64 x 128; 24 rows 20 in 64 x 128, 17 in 32 x 128, 24.6 in rows of 32. 1536
+// features of k 8960: 512 rows 51 in 128 x 128, 43 in 64 x 128, 36 in 32 x 128; 64
+// rows 36 in 32 x 128, 16 in rows of 32. The rows kernels read w past the LDS and
+// split k over the waves: their time follows the blocks a compute unit has to
+// stream.
+// 128 experts, n 768, k 2048, 8 choices: 4096 tokens 95 in 128 x 256, 112 in 256 x
+// 256 and in 128 x 128; 1024 tokens 53, 73 and 61; 256 tokens 44 in 32 x 128, 50 in 128 x
+// 256, 69 in rows of 16; 16 tokens 23 and 23 in rows; 4 tokens 14 and 12. n 2048,
+// k 768: 64 tokens 39 in 32 x 128, 70 in rows; one token 9 and 7.
 struct MmShapeTime {
     int bm, bn;
     double step, start;
 };
-constexpr MmShapeTime kMmTimes[] = {{32, 128, 0.55, 1.5}, {64, 128, 0.66, 2.0}, {128, 128, 0.78, 2.5}, {128, 256, 1.12, 3.0}, {256, 256, 1.72, 4.0}};
+constexpr MmShapeTime kMmTimes[] = {{32, 128, 0.55, 0.8}, {64, 128, 0.66, 1.3}, {128, 128, 0.78, 2.0}, {128, 256, 1.12, 4.0}, {256, 256, 1.72, 7.0}};
 
 hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
-    const int experts = c.offsets ? c.E : 0;
     const double kb = (c.K + kMmK - 1) / kMmK;
-    // row tiles: with experts, half of one is left over at each
-    const auto row_tiles = [&](int bm) {
-        return c.offsets ? static_cast<double>(c.M) / bm + 0.5 * static_cast<double>(c.M < c.E ? c.M : c.E)
-                         : static_cast<double>((c.M + bm - 1) / bm);
-    };
     const int band = c.offsets ? 2 : 8;
-    if (mm_few_rows(c.M, experts)) {
+    // Experts that have rows, were they chosen by chance, and their row tiles:
+    // one at least, half of one left over where they have many.
+    const double used = c.offsets ? c.E * (1 - exp(-static_cast<double>(c.M) / c.E)) : 1;
+    const auto row_tiles = [&](int bm) {
+        const double r = c.M / (used * bm);
+        return c.offsets ? used * (r + 0.5 + 0.5 * exp(-2 * r)) : static_cast<double>((c.M + bm - 1) / bm);
+    };
+    double best, fill;
+    if (c.offsets) {
+        const double wgs = row_tiles(16) * ((c.N + 31) / 32);
+        const bool fits = mm_row_tiles(c.M, c.E, 16) < kMmTiles / ((c.N + 31) / 32);
+        best = fits ? 2.5 + wgs * (0.0045 * ceil(kb / 16) + 0.00045 * kb) : INFINITY;
+        fill = 3.5;         // offsets, order and rows, one after the other
+    } else if (c.M <= 16) {
         // one block of features for a workgroup while few rows make few loads
         // of x (n 18944, k 3584: 1 row 13.6 us with one, 15.2 with two; 16 rows
-        // 19.8 and 18.5; 64 tokens to 8 of 128 experts 45 and 37) or there are few
-        // workgroups (n 1536, k 8960: 1 row 8.7 and 12.1)
-        const bool one = c.N < 8192 && !c.offsets;
-        if (one || (!c.offsets && c.M <= 8)) c.y_bf16 ? mm_rows<1, 1, 4, 8, 1>(c, st) : mm_rows<1, 1, 4, 8, 0>(c, st);
+        // 19.8 and 18.5) or there are few workgroups (n 1536, k 8960: 1 row 8.7
+        // and 12.1)
+        if (c.N < 8192 || c.M <= 8) c.y_bf16 ? mm_rows<1, 1, 4, 8, 1>(c, st) : mm_rows<1, 1, 4, 8, 0>(c, st);
         else c.y_bf16 ? mm_rows<1, 2, 4, 4, 1>(c, st) : mm_rows<1, 2, 4, 4, 0>(c, st);
         return hipGetLastError();
+    } else {
+        const double wgs = row_tiles(32) * ((c.N + 15) / 16);
+        const bool fits = mm_row_tiles(c.M, 0, 32) < kMmTiles / ((c.N + 15) / 16);
+        best = fits ? kb * (wgs < 180 ? 0.15 : 0.00085 * wgs) : INFINITY;
+        fill = 1.2;
     }
-    const double wgs = row_tiles(32) * ((c.N + 15) / 16);
-    double best = mm_row_tiles(c.M, experts, 32) < kMmTiles / ((c.N + 15) / 16) ? kb * (wgs < 180 ? 0.15 : 0.00085 * wgs) : INFINITY;
     int which = -1;
     for (int i = 0; i < (c.y_bf16 ? 5 : 3); ++i) {
         const MmShapeTime &m = kMmTimes[i];
         const double rounds = ceil(row_tiles(m.bm) * ((c.N + m.bn - 1) / m.bn) / kMmGrid);
-        const double time = rounds * (kb * m.step + m.start);
+        const double time = fill + rounds * (kb * m.step + m.start);
         if (time < best) {
             best = time;
             which = i;
         }
     }
     switch (which) {
-    case -1: c.y_bf16 ? mm_rows<2, 1, 4, 4, 1>(c, st) : mm_rows<2, 1, 4, 4, 0>(c, st); break;
+    case -1:
+        if (c.offsets) c.y_bf16 ? mm_rows<1, 2, 4, 4, 1>(c, st) : mm_rows<1, 2, 4, 4, 0>(c, st);
+        else c.y_bf16 ? mm_rows<2, 1, 4, 4, 1>(c, st) : mm_rows<2, 1, 4, 4, 0>(c, st);
+        break;
     case 0: c.y_bf16 ? mm_tiles<32, 128, 1, 4, 6, 1>(c, band, st) : mm_tiles<32, 128, 1, 4, 6, 0>(c, band, st); break;
     case 1: c.y_bf16 ? mm_tiles<64, 128, 1, 4, 5, 1>(c, band, st) : mm_tiles<64, 128, 1, 4, 5, 0>(c, band, st); break;
     case 2: c.y_bf16 ? mm_tiles<128, 128, 4, 2, 4, 1>(c, band, st) : mm_tiles<128, 128, 4, 2, 4, 0>(c, band, st); break;
