@@ -642,18 +642,18 @@ bool fp8_matmul_fits(int64_t M, int64_t N, int E) { return mm_row_tiles(M, E, 32
 // Which kernel: the one expected to be done first. A product's tiles go to the
 // compute units in rounds, and a round takes a start (the results' stores) and a
 // step per block of k; both were measured for each shape (us; fp32 results take
-// the shapes up to 128 x 128 with the same steps). Measured, us: 4096 rows of
-// 3584 by 18944 features 275 in 256 x 256 tiles, 335 in 128 x 256; 256 rows 49 and
-// 34; 128 rows 33 in 128 x 256, 24 in 128 x 128; 64 rows 23 in 128 x 128, 20 in
-// 64 x 128; 24 rows 20 in 64 x 128, 17 in 32 x 128, 24.6 in rows of 32. 1536
-// features of k 8960: 512 rows 51 in 128 x 128, 43 in 64 x 128, 36 in 32 x 128; 64
-// rows 36 in 32 x 128, 16 in rows of 32. The rows kernels read w past the LDS and
-// split k over the waves: their time follows the blocks a compute unit has to
-// stream.
-// 128 experts, n 768, k 2048, 8 choices: 4096 tokens 95 in 128 x 256, 112 in 256 x
-// 256 and in 128 x 128; 1024 tokens 53, 73 and 61; 256 tokens 44 in 32 x 128, 50 in 128 x
-// 256, 69 in rows of 16; 16 tokens 23 and 23 in rows; 4 tokens 14 and 12. n 2048,
-// k 768: 64 tokens 39 in 32 x 128, 70 in rows; one token 9 and 7.
+// the shapes up to 128 x 256, whose steps are half as long again, each by about
+// as much: 8192 rows, n 8960, k 1536 244, in 128 x 128 296). The rows kernels read w past the LDS and split k over the waves:
+// their time follows the blocks a compute unit has to stream. Measured, us:
+//   n 18944, k 3584: 4096 rows 275 in 256 x 256 tiles, 335 in 128 x 256; 256 rows
+//   49 and 34; 128 rows 33 in 128 x 256, 24 in 128 x 128; 64 rows 23 in 128 x 128,
+//   20 in 64 x 128; 24 rows 20 in 64 x 128, 17 in 32 x 128, 24.6 in rows of 32.
+//   n 1536, k 8960: 512 rows 51 in 128 x 128, 43 in 64 x 128, 36 in 32 x 128; 64
+//   rows 36 in 32 x 128, 16 in rows of 32.
+//   128 experts, 8 choices, n 768, k 2048: 4096 tokens 95 in 128 x 256, 112 in 256
+//   x 256 and in 128 x 128; 1024 tokens 53, 73 and 61; 256 tokens 44 in 32 x 128,
+//   50 in 128 x 256, 69 in rows of 16; 16 tokens 23 and 23 in rows; 4 tokens 14
+//   and 12. n 2048, k 768: 64 tokens 39 in 32 x 128, 70 in rows; one token 9 and 7.
 struct MmShapeTime {
     int bm, bn;
     double step, start;
@@ -691,7 +691,7 @@ hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
         fill = 1.2;
     }
     int which = -1;
-    for (int i = 0; i < (c.y_bf16 ? 5 : 3); ++i) {
+    for (int i = 0; i < (c.y_bf16 ? 5 : 4); ++i) {
         const MmShapeTime &m = kMmTimes[i];
         const double rounds = ceil(row_tiles(m.bm) * ((c.N + m.bn - 1) / m.bn) / kMmGrid);
         const double time = fill + rounds * (kb * m.step + m.start);
@@ -708,7 +708,7 @@ hipError_t launch_fp8_matmul(const MatmulCall &c, hipStream_t st) {
     case 0: c.y_bf16 ? mm_tiles<32, 128, 1, 4, 6, 1>(c, band, st) : mm_tiles<32, 128, 1, 4, 6, 0>(c, band, st); break;
     case 1: c.y_bf16 ? mm_tiles<64, 128, 1, 4, 5, 1>(c, band, st) : mm_tiles<64, 128, 1, 4, 5, 0>(c, band, st); break;
     case 2: c.y_bf16 ? mm_tiles<128, 128, 4, 2, 4, 1>(c, band, st) : mm_tiles<128, 128, 4, 2, 4, 0>(c, band, st); break;
-    case 3: mm_tiles<128, 256, 2, 4, 3, 1>(c, band, st); break;
+    case 3: c.y_bf16 ? mm_tiles<128, 256, 2, 4, 3, 1>(c, band, st) : mm_tiles<128, 256, 2, 4, 3, 0>(c, band, st); break;
     default: mm_tiles<256, 256, 4, 2, 2, 1>(c, band, st);
     }
     return hipGetLastError();
