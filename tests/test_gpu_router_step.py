@@ -215,3 +215,55 @@ def test_same_bits_again():
         runs.append([keep[n] for n in ("ids", "weights", "Ys", "Y", "dw", "dlogits", "dX")])
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def test_layer_captured():
+    """The library's calls of a layer in one graph, replayed on new inputs, with eager work between the replays."""
+    dev = device()
+    layer, N = Layer(dev, seed=4), T * K
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=dev)  # noqa: E731
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    f32 = lambda *s: torch.zeros(*s, device=dev)  # noqa: E731
+    f8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=dev).view(F8)  # noqa: E731
+
+    def buffers():
+        return dict(logits=f32(T, E), X=bf(T, H), dY=bf(T, D), ids=i32(T, K), weights=f32(T, K), offsets=i32(E + 1), order=i32(N),
+                    slots=i32(T, K), x=f8(T, H), xs=f32(T, 3), Ys=bf(N, D), Y=bf(T, D), dYs=bf(N, D), dw=f32(T, K), dlogits=f32(T, E),
+                    dy=f8(N, D), dys=f32(N, 2), dXs=bf(N, H), dX=bf(T, H))
+
+    def run(b):
+        L.logra_route(b["logits"], b["ids"], b["weights"], bias=layer.bias, groups=G, topk_groups=KEPT, group_best=2, **ROUTE)
+        L.logra_expert_sort(b["ids"], E, b["offsets"], b["order"], b["slots"])
+        L.logra_fp8_quantize(b["X"], b["x"], b["xs"])
+        L.logra_fp8_matmul(b["x"], b["xs"], layer.w, layer.ws, b["Ys"], offsets=b["offsets"], order=b["order"], topk=K)
+        L.logra_expert_combine(b["Ys"], b["slots"], b["Y"], weights=b["weights"])
+        L.logra_expert_combine_backward(b["dY"], b["Ys"], b["slots"], b["weights"], b["dYs"], b["dw"])
+        L.logra_route_backward(b["logits"], b["ids"], b["dw"], b["dlogits"], **ROUTE)
+        L.logra_fp8_quantize(b["dYs"], b["dy"], b["dys"])
+        L.logra_fp8_matmul(b["dy"], b["dys"], layer.wt, layer.wts, b["dXs"], offsets=b["offsets"])
+        L.logra_expert_combine(b["dXs"], b["slots"], b["dX"])
+
+    held, eager = buffers(), buffers()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(held)
+    for mb in range(4):
+        X, dY = layer.inputs(mb)
+        logits = X.float() @ layer.router.t()
+        logits[7 * mb:7 * mb + 5 + mb] = -float("inf")          # other padding every time
+        for b in (held, eager):
+            for name, t in (("X", X), ("dY", dY), ("logits", logits)):
+                b[name].copy_(t)
+        graph.replay()
+        run(eager)
+        torch.cuda.synchronize()
+        kept = int(eager["offsets"][-1])
+        assert 0 < kept < N
+        for name, t in eager.items():
+            rows = slice(0, kept) if name in ("Ys", "dYs", "dXs", "dy", "dys", "order") else slice(None)
+            assert torch.equal(held[name][rows].view(torch.uint8), t[rows].view(torch.uint8)), (mb, name)
