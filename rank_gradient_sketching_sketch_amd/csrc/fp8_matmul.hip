@@ -350,7 +350,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         // the list's half whose tiles are done; the others read it 16 tiles on
         if (f_i % (kMmList / 2) == 16 && wave == 0) list_tiles(f_i + 16, kMmList / 2);
         // its rows were asked for a tile before: with so few blocks they may not be here
-        if (kb < D) mm_wait<0>();
+        if (c.order && kb < D) mm_wait<0>();
         const MmTile t = tile(f_i);
         f_more = t.rows > 0;
         if (!f_more) return;
