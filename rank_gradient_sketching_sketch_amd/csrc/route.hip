@@ -165,12 +165,20 @@ struct RouteArgs {
     float *weights;
 };
 
-// What fp32 keys may be off by: `part` for a score, 2^-22 of the larger key
-// for the two sums with a bias (half of each would do).
+// What fp32 keys may be off by: `part` for two scores, and 2^-24 of each key
+// where the bias is added to its score: 2^-22 of the larger of two keys is twice
+// that. A group's sum of two keys has the roundings of both, which are those of
+// the keys' sizes, however small a sum they leave where their signs differ, and
+// one of its own: two groups 2^-22 of the most that a group's two magnitudes add
+// up to, taken twice again. That is the most of all groups, not of the two that
+// are compared: one above the border with large keys may belong below it.
 struct RouteDoubt {
     float part;
-    __device__ __forceinline__ bool near(float a, float b, float terms) const {
-        return !(a - b > terms * (part + 0x1p-22f * fmaxf(fabsf(a), fabsf(b))));
+    __device__ __forceinline__ bool near(float a, float b) const {
+        return !(a - b > part + 0x1p-22f * fmaxf(fabsf(a), fabsf(b)));
+    }
+    __device__ __forceinline__ bool near_sums(float a, float b, float size) const {
+        return !(a - b > 2.f * part + 0x1p-21f * size);
     }
 };
 
@@ -210,7 +218,14 @@ __device__ __forceinline__ RouteTold route_choose(const RouteArgs &a, typename P
             // the lowest sum that stays against the highest that does not
             const Key low = P::lane(sum, __builtin_ctzll(__ballot(better == a.kept - 1)));
             const Key high = P::lane(sum, __builtin_ctzll(__ballot(better == a.kept)));
-            if (high > P::none() && doubt.near(P::value(low), P::value(high), 2.f)) return kRouteNothing;
+            if (high > P::none()) {
+                if (a.best == 2) {
+                    const float size = (one > P::none() ? fabsf(P::value(one)) : 0.f) + (two > P::none() ? fabsf(P::value(two)) : 0.f);
+                    if (doubt.near_sums(P::value(low), P::value(high), wave_max_f32(size))) return kRouteNothing;
+                } else if (doubt.near(P::value(low), P::value(high))) {
+                    return kRouteNothing;
+                }
+            }
         }
         if (out) {
 #pragma unroll
@@ -249,11 +264,11 @@ __device__ __forceinline__ RouteTold route_choose(const RouteArgs &a, typename P
     *my_id = id;
     if constexpr (CHECK) {
         const float before = dpp_f32<0x138, 0xF>(value, value);      // the lane before's
-        bool close = __ballot(lane > 0 && lane < j && doubt.near(before, value, 1.f)) != 0;
+        bool close = __ballot(lane > 0 && lane < j && doubt.near(before, value)) != 0;
         if (j == a.K) {
             // the experts that may come before the last choice
             const float last = lane_f32(value, a.K - 1);
-            while (next(j, &most) && doubt.near(last, P::value(most), 1.f)) {
+            while (next(j, &most) && doubt.near(last, P::value(most))) {
                 close = true;
                 if (++j > min(a.K + 8, 64)) return kRouteNothing;      // many alike, as where a router starts from zeros
             }
