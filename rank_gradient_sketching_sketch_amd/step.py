@@ -175,7 +175,8 @@ class Step:
         self.adamw = adamw
         if adamw is not None:
             self.grads += [g for g in adamw.grads if not any(g is x for x in self.grads)]
-        self._clipped = False       # whether `norm` is this step's
+        self._clipped = False       # whether the host called `clip` since the last `sketch`
+        self._clip_captured = False     # whether a graph may write `norm` without the host's knowing
         self.mats: List[Matrix] = list(matrices)
         for g in self.groups:
             g.S = None
@@ -363,6 +364,11 @@ class Step:
         self._clipped = False
         self._members()
         self.set_step(step)
+        if self.adamw is not None:
+            with torch.cuda.stream(self.main):
+                # a norm that `dense_update` reads also in a step that is not clipped
+                if self._clip_captured or torch.cuda.is_current_stream_capturing():
+                    self.norm.zero_()
         self._fork()
         try:                # a callback may fail: what is enqueued by then is joined all the same
             with self._late_inputs() if late else contextlib.nullcontext():
@@ -431,6 +437,7 @@ class Step:
             if capturing:
                 raise ValueError("a gradient was replaced: clip once before the capture")
             self._list_gradients()
+        self._clip_captured |= capturing
         if capturing and not any(kept[0] is self._grad_list for kept in self._captured):
             self._captured.append((self._grad_list, self._grad_ws))
         B.logra_grad_clip(self._grad_list, max_norm, self.norm, self.coef, ws=self._grad_ws, stream=self.main)
@@ -439,16 +446,17 @@ class Step:
 
     def dense_update(self, lr: float, beta1: float, beta2: float, eps: float, weight_decay: float, step: int):
         """One AdamW step (its `step`-th, from 1) over the dense parameters
-        given to Step, on the caller's stream. After `clip`, a norm that is not
-        finite leaves parameters and moments as they are: the host that reads
-        the norm does not count that step. The step's seed keys the rounding of
-        8-bit moments."""
+        given to Step, on the caller's stream. After `clip` (or a replay of a
+        graph that holds one), a norm that is not finite leaves parameters and
+        moments as they are: the host that reads the norm does not count that
+        step. The step's seed keys the rounding of 8-bit moments."""
         if self.adamw is None:
             raise ValueError("the step was given no dense parameters")
         a = self.adamw
         if not a.describes(a.params, a.grads, a.copies):
             raise ValueError("a dense parameter or gradient has other memory than its list was made with")
-        B.logra_adamw(a, lr, beta1, beta2, eps, weight_decay, step, norm=self.norm if self._clipped else None,
+        clipped = self._clipped or self._clip_captured
+        B.logra_adamw(a, lr, beta1, beta2, eps, weight_decay, step, norm=self.norm if clipped else None,
                       seed=self.seed, stream=self.main)
 
     def pass1(self, beta2: float, eps: float):
