@@ -832,8 +832,9 @@ logra_status logra_sketch_experts(const logra_matrix *m, int n_experts, uint64_t
  *   An expert whose logit, bias or key is -inf or NaN is not chosen; a choice
  *   that finds no expert left is id -1 with weight 0, which the sort drops (so
  *   a padding token is a row of -inf). A token with a NaN among its logits has
- *   NaN weights where an expert was chosen. With softmax scores a logit of
- *   +inf has no score: the token's weights are NaN.
+ *   NaN weights where an expert was chosen. With softmax scores and a logit
+ *   of +inf there are no scores: such a token's experts are chosen by their
+ *   logits (of those whose bias is neither -inf nor NaN), its weights are NaN.
  *   Keys are formed and compared in fp64; without a bias and without sums of
  *   two the logits are compared, which sort alike. Weights are fp32.
  * logra_route_backward -- dlogits (T x n_experts, written whole) from

@@ -27,13 +27,19 @@ def scores(x, score):
 
 
 def route(x, topk, score, bias=None, groups=1, topk_groups=1, group_best=1, renormalize=True, scale=1.0):
-    """(ids, weights) of rows of logits, choice by choice."""
+    """(ids, weights) of rows of logits, choice by choice. A softmax with a logit
+    of +inf has no values: choices are by the logits, weights NaN."""
     x = np.asarray(x, np.float64)
     T, E = x.shape
     s = scores(x, score)
     key = s + (0.0 if bias is None else np.asarray(bias, np.float64))
     if bias is None and not (groups > topk_groups and group_best == 2):
         key = x.copy()                          # sorts alike, also where scores are equal in 64 bits
+    lost = (x == np.inf).any(1) & (score == SOFTMAX)
+    if bias is not None:
+        key[lost] = np.where(np.asarray(bias, np.float64) > -np.inf, x[lost], -np.inf)
+    else:
+        key[lost] = x[lost]
     key = np.where((x > -np.inf) & (key > -np.inf), key, -np.inf)
     ids, w = np.full((T, topk), -1), np.zeros((T, topk))
     for t in range(T):
@@ -56,7 +62,7 @@ def route(x, topk, score, bias=None, groups=1, topk_groups=1, group_best=1, reno
                 c = x[t, ids[t, :n]]
                 w[t, :n] = np.exp(np.minimum(c, 0) - min(c.max(), 0)) / (1 + np.exp(-np.abs(c)))
             w[t, :n] /= w[t, :n].sum()
-        if np.isnan(x[t]).any():
+        if np.isnan(x[t]).any() or lost[t]:
             w[t, :n] = np.nan
     return ids, scale * w
 

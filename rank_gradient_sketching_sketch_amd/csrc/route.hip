@@ -10,7 +10,8 @@
 //   id_j = the j-th highest key left (ties: the lower index),
 //   w_j  = c s_(id_j), divided by the sum of the chosen s where renormalised.
 // An expert whose key is -inf or NaN is never chosen; a choice that finds
-// none is -1 with weight 0, which the sort drops.
+// none is -1 with weight 0, which the sort drops. A softmax with a logit of
+// +inf has no values: there the logits are the keys and the weights NaN.
 //
 // Choices are whole numbers that must not hang on rounding: they are those of
 // keys formed and compared in fp64. Where no bias and no sum of two keys
@@ -322,6 +323,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     const bool any_nan = __ballot(nan) != 0;
     // softmax: all logits against the largest
     float denom = 1.f;
+    bool no_scores = false;      // a logit of +inf
     float score[N];
     if (!a.sigmoid && (SCORES || !a.renorm)) {
         top = wave_max_f32(top);
@@ -332,6 +334,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             denom += score[i];
         }
         denom = wave_sum_f32(denom);
+        no_scores = top == INFINITY;
     }
 
     int my_id, found;
@@ -352,9 +355,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         // with N = 32) and the quotient: 2^-18 of the largest score for two.
         const RouteDoubt doubt{a.sigmoid ? 0x1p-21f : 0x1p-18f / denom};
         const RouteTold told = route_choose<FloatKey, true>(a, key, e0, doubt, &my_id, &found);
+        // keys are NaN where there are no scores: none was found
         if (told == kRouteNotOrder && a.sigmoid) {
             my_id = route_order<BF16>(a, t, my_id, found);
-        } else if (told != kRouteAll) {
+        } else if (told != kRouteAll || no_scores) {
             double wide[N], sum = 0.0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -366,7 +370,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (!a.sigmoid) wide[i] /= sum;
-                const double k = wide[i] + static_cast<double>(bias[i]);
+                const double d = x[i];
+                const double k = no_scores ? (bias[i] > -INFINITY ? d : NAN) : wide[i] + static_cast<double>(bias[i]);
                 wide[i] = x[i] > -INFINITY && k == k ? k : ScoreKey::none();
             }
             route_choose<ScoreKey, false>(a, wide, e0, doubt, &my_id, &found);
@@ -388,7 +393,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     } else {
         w = a.sigmoid ? sigmoid_shifted(my_x, 0.f) : expf(my_x - top) / denom;
     }
-    if (any_nan) w = NAN;
+    if (any_nan || no_scores) w = NAN;
     if (lane < a.K) {
         a.ids[t * a.K + lane] = my_id;
         a.weights[t * a.K + lane] = chosen ? a.scale * w : 0.f;
