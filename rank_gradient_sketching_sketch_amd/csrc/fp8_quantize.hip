@@ -38,7 +38,9 @@ __device__ __forceinline__ float quant_clamp(float q) {      // a NaN stays
 // where nothing under- or overflows on the way: quotients that matter are
 // above 2^-11 and the scale is kept above 2^-90. There no quotient is above 448
 // but by its own rounding, either. Elsewhere (in a lane of the wave) the
-// division itself.
+// division itself. The remainder is taken as s q - x, whose zero times -y leaves a
+// quotient of -0 its sign (x - s q would make it +0): which way is taken hangs on
+// the wave's other blocks, a code must not.
 __device__ __forceinline__ u32x2_t quant_codes(const float (&x)[8], float scale) {
     float q[8];
     if (__ballot(!(scale > 0x1p-90f && scale < 0x1p90f)) == 0) {
@@ -46,8 +48,8 @@ __device__ __forceinline__ u32x2_t quant_codes(const float (&x)[8], float scale)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q0 = x[e] * y;
-            const float q1 = fmaf(fmaf(-scale, q0, x[e]), y, q0);
-            q[e] = fmaf(fmaf(-scale, q1, x[e]), y, q1);
+            const float q1 = fmaf(fmaf(scale, q0, -x[e]), -y, q0);
+            q[e] = fmaf(fmaf(scale, q1, -x[e]), -y, q1);
         }
     } else {
 #pragma unroll
