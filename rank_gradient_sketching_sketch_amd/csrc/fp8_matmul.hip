@@ -279,7 +279,7 @@ __device__ __forceinline__ void mm_fetch(i32x4_t view, uint32_t to, uint32_t off
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(mm_scalar(view)), "s"(__builtin_amdgcn_readfirstlane(step))
-                 : "memory");
+                 : "m0", "memory");
 }
 
 // The same of 4 bytes per lane.
@@ -287,7 +287,7 @@ __device__ __forceinline__ void mm_fetch4(i32x4_t view, uint32_t to, uint32_t of
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(mm_scalar(view))
-                 : "memory");
+                 : "m0", "memory");
 }
 
 // At most N vector memory operations of the wave are left, its LDS reads are
