@@ -889,7 +889,8 @@ logra_status logra_route_backward(int64_t T, int n_experts, int topk, int dtype,
  *     then the activations before the sort. Rows of Y that no expert has are
  *     not written; offsets are read on the device, values outside 0 .. M
  *     count as the nearest bound; a row that order names outside
- *     0 .. x_rows - 1 counts as zeros.
+ *     0 .. x_rows - 1 counts as zeros (so x_rows may be 0, and x, ldx and
+ *     x_scales are not looked at then).
  *   A block's products are summed by the matrix cores, scaled by the product
  *   of the two scales and added in fp32; Y (y_dtype LOGRA_F32 or LOGRA_BF16,
  *   row stride ldy) is rounded once. With LOGRA_F32 a block's sum is fp32, at

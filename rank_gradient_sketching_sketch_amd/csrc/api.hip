@@ -1027,8 +1027,8 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
     if (x_rows > 0 && (!x || !aligned16(x) || ldx < k || ldx % 16 || !x_scales || !aligned_to(x_scales, 4)))
         return LOGRA_ERR_INVALID_ARGUMENT;
     // rows are read at 32-bit offsets: from a tile's first one, or all of x where the order picks them
-    if (ldx > kMaxExpertDim || ldw > kMaxExpertDim || ldy > (1ll << 40) || (order && x_rows > ((1ll << 31) - 1) / ldx))
-        return LOGRA_ERR_UNSUPPORTED;
+    if (ldw > kMaxExpertDim || ldy > (1ll << 40)) return LOGRA_ERR_UNSUPPORTED;
+    if (x_rows > 0 && (ldx > kMaxExpertDim || (order && x_rows > ((1ll << 31) - 1) / ldx))) return LOGRA_ERR_UNSUPPORTED;
     if (!fp8_matmul_fits(M, n, offsets ? n_experts : 0)) return LOGRA_ERR_UNSUPPORTED;
     MatmulCall c;
     c.M = M;
