@@ -359,7 +359,9 @@ __global__ __launch_bounds__(64 * WM * WN) void mm_tile_kernel(MatmulCall c, int
         const int n0 = t.tn * BN;
         const int64_t base = mm_base(c, t);
         x_rs = mm_words(c.x + base * c.ldx);
-        xs_rs = mm_words(c.xs + base * kb, (c.x_rows - base) * kb * 4);
+        // x without rows: one row's length, as a step behind a view of nothing would
+        // make its end wrap around
+        xs_rs = mm_words(c.xs + base * kb, max(c.x_rows - base, static_cast<int64_t>(1)) * kb * 4);
         w_rs = mm_words(c.w + (static_cast<int64_t>(t.expert) * c.N + n0) * c.ldw);
         const int64_t fb = static_cast<int64_t>(t.expert) * nb + n0 / 128;      // the tile's first block of features
         ws_rs = mm_words(c.ws + fb * kb, (static_cast<int64_t>(c.E) * nb - fb) * kb * 4);
