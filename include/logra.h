@@ -883,14 +883,16 @@ logra_status logra_route_backward(int64_t T, int n_experts, int topk, int dtype,
  *   (n_experts arrays of n x k codes) and their scales as quantize writes
  *   them (x: block_rows 1; w: block_rows 128):
  *     offsets NULL: n_experts 1, row i of Y from row i of x (x_rows >= M);
- *     offsets (n_experts + 1 int32, as logra_expert_sort): rows offsets[e] ..
- *     offsets[e + 1] - 1 of Y are expert e's, from the same rows of x (order
- *     NULL) or, with order (M int32) and topk, from row order[i] / topk: x is
- *     then the activations before the sort. Rows of Y that no expert has are
- *     not written; offsets are read on the device, values outside 0 .. M
- *     count as the nearest bound; a row that order names outside
- *     0 .. x_rows - 1 counts as zeros (so x_rows may be 0, and x, ldx and
- *     x_scales are not looked at then).
+ *     offsets (n_experts + 1 int32, non-decreasing, as logra_expert_sort):
+ *     rows offsets[e] .. offsets[e + 1] - 1 of Y are expert e's, from the same
+ *     rows of x (order NULL) or, with order (M int32) and topk, from row
+ *     order[i] / topk: x is then the activations before the sort. Rows of Y
+ *     that no expert has are not written; offsets are read on the device,
+ *     values outside 0 .. M count as the nearest bound (where they decrease,
+ *     an element of a row that experts have gets the product of one of them
+ *     or stays); a row that order names outside 0 .. x_rows - 1 counts as
+ *     zeros (so x_rows may be 0, and x, ldx and x_scales are not looked at
+ *     then).
  *   A block's products are summed by the matrix cores, scaled by the product
  *   of the two scales and added in fp32; Y (y_dtype LOGRA_F32 or LOGRA_BF16,
  *   row stride ldy) is rounded once. With LOGRA_F32 a block's sum is fp32, at

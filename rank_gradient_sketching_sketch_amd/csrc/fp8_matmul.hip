@@ -42,6 +42,7 @@ constexpr int kMmK = 128;
 constexpr int kMmXcds = 8;
 constexpr int kMmGrid = 256;                   // one workgroup for each compute unit
 constexpr int kMmList = 64;                    // tiles in a workgroup's list
+constexpr int kMmTiles = 1 << 23;              // tiles of a product are numbered below this
 
 // Operand of 128 k: a lane has 32 of the k of row L % 16 of A or of column
 // L % 16 of B (which ones does not matter as long as both have the same), as
@@ -127,6 +128,9 @@ __device__ __forceinline__ MmPlan mm_plan(const MatmulCall &c, int n_tn, int ban
         mm_rows_of(c, e, &a, &b);
         p.mine += static_cast<int>((b - a + BM - 1) / BM);
     }
+    // offsets that decrease somewhere give rows to several experts and could give
+    // more tiles than can be numbered: those left out are not written
+    p.mine = min(p.mine, kMmTiles);
     int sum = p.mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -134,7 +138,7 @@ __device__ __forceinline__ MmPlan mm_plan(const MatmulCall &c, int n_tn, int ban
         if (lane >= o) sum += up;
     }
     p.before = sum - p.mine;
-    p.tiles = __builtin_amdgcn_readlane(sum, 63);
+    p.tiles = min(__builtin_amdgcn_readlane(sum, 63), (kMmTiles - 1) / n_tn);
     return p;
 }
 
@@ -149,7 +153,7 @@ __device__ __forceinline__ uint32_t mm_div(uint32_t a, uint32_t b) { return (a &
 // tile.
 template <int BM>
 __device__ __forceinline__ MmTile mm_tile(const MatmulCall &c, const MmPlan &p, uint32_t id) {
-    const uint32_t n_tn = p.n_tn, G = static_cast<uint32_t>(p.tiles) * n_tn;      // below 2^23
+    const uint32_t n_tn = p.n_tn, G = static_cast<uint32_t>(p.tiles) * n_tn;      // below kMmTiles
     const bool is = id < G;
     if (!is) id = 0;
     const uint32_t share = G / kMmXcds, rest = G % kMmXcds, x = id % kMmXcds;
@@ -637,8 +641,7 @@ static void mm_tiles(const MatmulCall &c, int band, hipStream_t st) {
     hipLaunchKernelGGL((mm_tile_kernel<BM, BN, WM, WN, D, BF16>), grid, block, 0, st, c, n_tn, band);
 }
 
-// Tiles are numbered below 2^23, those of 32 x 128 at least.
-constexpr int64_t kMmTiles = 1ll << 23;
+// Those of 32 x 128 at least can be numbered.
 bool fp8_matmul_fits(int64_t M, int64_t N, int E) { return mm_row_tiles(M, E, 32) < kMmTiles / ((N + 127) / 128); }
 
 // Which kernel: the one expected to be done first. A product's tiles go to the
