@@ -7,6 +7,8 @@ built.
 """
 from __future__ import annotations
 
+import types
+
 __all__ = [
     "logra_abi_version", "logra_status_string", "logra_sign_words",
     "logra_sketch_workspace_bytes", "logra_sketch_accumulate",
@@ -26,9 +28,32 @@ __all__ = [
 ]
 
 
+_kept = {}                      # names that were looked up, as the binding has them
+
+
+class _Binding(types.ModuleType):
+    """The binding's module: what is replaced in it shows through the package."""
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        _forget()
+
+    def __delattr__(self, name):
+        super().__delattr__(name)
+        _forget()
+
+
+def _forget():
+    while _kept:
+        name, value = _kept.popitem()
+        if globals().get(name) is value:        # not one that a caller has put here
+            del globals()[name]
+
+
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        globals()[name] = value = getattr(binding, name)     # later look-ups do not come here
+        binding.__class__ = _Binding
+        globals()[name] = _kept[name] = value = getattr(binding, name)     # later look-ups do not come here
         return value
     raise AttributeError(name)
