@@ -935,7 +935,10 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
  *   list->table, and keeps both as long as calls or graphs use them.
  * logra_adamw_tensor: param, grad and copy (NULL: none) are rows x cols with
  *   row strides of their own, each LOGRA_F32 or LOGRA_BF16. No two of a
- *   list's arrays may overlap.
+ *   list's arrays may share an element. Rows of one may lie between the rows
+ *   of others where all have the same row stride in bytes (column slices of
+ *   one buffer) and at most 256 arrays do so at a time; a gradient list,
+ *   which the gradients may have to go through too, has no such arrays.
  * The moments are the caller's, zero before the first step: exp_avg and
  *   exp_avg_sq, blocks of 256 elements one after the other, tensor i's
  *   elements (rows end to end) from the begin of its first block, the sum of
@@ -956,7 +959,8 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
  *   eps 0: an element whose moments are both zero becomes NaN (0 / 0).
  *   step: 1 for the first step; it must grow by one with every step that is
  *   applied, and must not repeat (the rounding's chances would).
- * Errors of pack: as logra_grad_list_pack. Errors of the step:
+ * Errors of pack: as logra_grad_list_pack (UNSUPPORTED too for more arrays
+ *   between each other's rows). Errors of the step:
  *   INVALID_ARGUMENT (nulls, misaligned table or moments (16 bytes), lr, eps or
  *   weight_decay not finite, eps < 0 or subnormal in fp32, betas outside [0, 1), step 0, max_norm
  *   negative or NaN), UNSUPPORTED (state_bits), HIP.

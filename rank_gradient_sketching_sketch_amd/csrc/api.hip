@@ -1059,11 +1059,49 @@ namespace {
 // matrix should have it.
 constexpr uint64_t kAdamId = 0xFFFFFFFFFFFFFFFFull;
 
-bool adam_array(const void *p, int64_t rows, int64_t cols, int64_t ld, int dtype, uint64_t *end) {
+// The bytes of an array: rows of `width` at a stride, or one run of them (stride 0).
+struct AdamSpan {
+    uint64_t begin, end, stride, width;
+    bool operator<(const AdamSpan &o) const { return begin < o.begin; }
+};
+constexpr int kAdamLive = 256;      // arrays that may lie between each other's rows
+
+bool adam_array(const void *p, int64_t rows, int64_t cols, int64_t ld, int dtype, AdamSpan *span) {
     const int64_t el = elem_bytes(dtype);
     if (!p || ld < cols || !aligned_to(p, el)) return false;
-    *end = reinterpret_cast<uint64_t>(p) + static_cast<uint64_t>(((rows - 1) * ld + cols) * el);
+    span->begin = reinterpret_cast<uint64_t>(p);
+    span->end = span->begin + static_cast<uint64_t>(((rows - 1) * ld + cols) * el);
+    const bool run = rows == 1 || ld == cols;
+    span->stride = run ? 0 : static_cast<uint64_t>(ld * el);
+    span->width = run ? span->end - span->begin : static_cast<uint64_t>(cols * el);
     return true;
+}
+
+// Whether b, which begins between a's begin and end, has bytes of a. Rows of the
+// same stride that start in a gap of a's and end there do so everywhere; of
+// different strides they are not told apart.
+bool adam_clash(const AdamSpan &a, const AdamSpan &b) {
+    if (a.stride == 0 || (b.stride != 0 && b.stride != a.stride)) return true;
+    const uint64_t at = (b.begin - a.begin) % a.stride;
+    return at < a.width || b.width > a.stride - at;
+}
+
+logra_status adam_apart(AdamSpan *span, int64_t n) {
+    std::sort(span, span + n);
+    const AdamSpan *live[kAdamLive];        // those that have not ended
+    int n_live = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        int kept = 0;
+        for (int j = 0; j < n_live; ++j) {
+            if (live[j]->end <= span[i].begin) continue;
+            if (adam_clash(*live[j], span[i])) return LOGRA_ERR_INVALID_ARGUMENT;
+            live[kept++] = live[j];
+        }
+        n_live = kept;
+        if (n_live == kAdamLive) return LOGRA_ERR_UNSUPPORTED;
+        live[n_live++] = span + i;
+    }
+    return LOGRA_OK;
 }
 
 }  // namespace
@@ -1079,8 +1117,8 @@ logra_status logra_adamw_list_pack(int64_t n, const logra_adamw_tensor *tensors,
     if (table_bytes < logra_adamw_table_bytes(n)) return LOGRA_ERR_WORKSPACE;
     constexpr int64_t kMost = 1ll << 40;
     // the address ranges, in the table's memory before the table takes it
-    static_assert(3 * sizeof(GradSpan) <= sizeof(AdamEntry), "three ranges for an entry");
-    GradSpan *span = static_cast<GradSpan *>(table_host);
+    static_assert(3 * sizeof(AdamSpan) <= sizeof(AdamEntry), "three ranges for an entry");
+    AdamSpan *span = static_cast<AdamSpan *>(table_host);
     int64_t n_span = 0;
     for (int64_t i = 0; i < n; ++i) {
         const logra_adamw_tensor &t = tensors[i];
@@ -1096,14 +1134,12 @@ logra_status logra_adamw_list_pack(int64_t n, const logra_adamw_tensor *tensors,
         for (int a = 0; a < 3; ++a) {
             if (a == 2 && !t.copy) continue;
             if (arrays[a].ld > kMost / t.rows) return LOGRA_ERR_UNSUPPORTED;
-            uint64_t end = 0;
-            if (!adam_array(arrays[a].p, t.rows, t.cols, arrays[a].ld, arrays[a].dtype, &end)) return LOGRA_ERR_INVALID_ARGUMENT;
-            span[n_span++] = GradSpan{reinterpret_cast<uint64_t>(arrays[a].p), end};
+            if (!adam_array(arrays[a].p, t.rows, t.cols, arrays[a].ld, arrays[a].dtype, span + n_span++))
+                return LOGRA_ERR_INVALID_ARGUMENT;
         }
     }
-    std::sort(span, span + n_span);
-    for (int64_t i = 1; i < n_span; ++i)
-        if (span[i].begin < span[i - 1].end) return LOGRA_ERR_INVALID_ARGUMENT;
+    const logra_status apart = adam_apart(span, n_span);
+    if (apart != LOGRA_OK) return apart;
     AdamEntry *table = static_cast<AdamEntry *>(table_host);
     logra_adamw_list out = {};
     for (int64_t i = 0; i < n; ++i) {
