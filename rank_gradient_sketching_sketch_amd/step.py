@@ -449,13 +449,17 @@ class Step:
         given to Step, on the caller's stream. After `clip` (or a replay of a
         graph that holds one), a norm that is not finite leaves parameters and
         moments as they are: the host that reads the norm does not count that
-        step. The step's seed keys the rounding of 8-bit moments."""
+        step. The step's seed keys the rounding of 8-bit moments. After a
+        gradient in `grads` was replaced, give `adamw` a list that has the new
+        one (with the old list's state): ValueError until then."""
         if self.adamw is None:
             raise ValueError("the step was given no dense parameters")
         a = self.adamw
         if not a.describes(a.params, a.grads, a.copies):
             raise ValueError("a dense parameter or gradient has other memory than its list was made with")
         clipped = self._clipped or self._clip_captured
+        if clipped and not {id(g) for g in a.grads} <= {id(g) for g in self.grads}:
+            raise ValueError("a dense parameter's gradient is not among those that clip takes: give the step a list of what it has now")
         B.logra_adamw(a, lr, beta1, beta2, eps, weight_decay, step, norm=self.norm if clipped else None,
                       seed=self.seed, stream=self.main)
 
