@@ -898,7 +898,10 @@ logra_status logra_route_backward(int64_t T, int n_experts, int topk, int dtype,
  *   row stride ldy) is rounded once. With LOGRA_F32 a block's sum is fp32, at
  *   half the rate; with LOGRA_BF16 the matrix cores' 8-bit products add eight
  *   neighbouring ones at a time, off by at most 7 2^-13 of the largest of
- *   them, then the groups in fp32. Codes outside a row's k do not enter. Forward: w of W; input gradient: x of dY, w of W transposed.
+ *   them, then the groups in fp32: where large products cancel that is far
+ *   above the rounding of Y, and a caller who needs more takes Y in fp32 and
+ *   rounds it afterwards. Codes outside a row's k do not enter. Forward: w of
+ *   W; input gradient: x of dY, w of W transposed.
  *   k, ldx, ldw multiples of 16; x, w 16-byte aligned; arrays of w follow
  *   each other after n row strides; n and M as they are.
  * Limits: M <= 2^26, n, k, ldx, ldw <= 2^22, n_experts <= 1024; with order x
@@ -950,7 +953,9 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
  *     scale. A block's scale is its largest magnitude / 448 (0, with codes 0,
  *     below 2^-100; NaN if the block holds a value that is not finite). Codes
  *     are rounded up or down with the chance that makes the rounding
- *     unbiased (below 2^-6 of a code's range in steps of 2^-9), by 16 bits of
+ *     unbiased, of m and of the root (v, the root's square, comes out some
+ *     percent high over many steps; values below 2^-6 of a scale are rounded in
+ *     steps of 2^-9 of it), by 16 bits of
  *     the library's counter hash each: elements 2 j and 2 j + 1 of the state
  *     take bits 0..15 and 32..47 (m), 16..31 and 48..63 (root) of
  *     mix(key + (j + 1) 0x9E3779B97F4A7C15), key of (seed, step, matrix_id
@@ -958,7 +963,9 @@ logra_status logra_fp8_matmul(int64_t M, int64_t n, int64_t k, int n_experts, co
  *     the smallest code.
  *   eps 0: an element whose moments are both zero becomes NaN (0 / 0).
  *   step: 1 for the first step; it must grow by one with every step that is
- *   applied, and must not repeat (the rounding's chances would).
+ *   applied, and must not repeat (the rounding's chances would). step, lr and
+ *   the rest are the host's: a graph that holds the call repeats the captured
+ *   step, so a step that is replayed leaves this call outside its graph.
  * Errors of pack: as logra_grad_list_pack (UNSUPPORTED too for more arrays
  *   between each other's rows). Errors of the step:
  *   INVALID_ARGUMENT (nulls, misaligned table or moments (16 bytes), lr, eps or
