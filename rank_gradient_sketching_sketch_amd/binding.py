@@ -866,8 +866,9 @@ def logra_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
     highest of score + bias, among the topk_groups best groups of experts
     (score: LOGRA_SOFTMAX or LOGRA_SIGMOID; weights: scale times the scores
     without the bias, over their sum if renormalize). -1 with weight 0 where no
-    expert is left, as in a row of -inf. The ids are what logra_expert_sort
-    takes, the weights what gather and combine take."""
+    expert is left, as in a row of -inf; NaN weights where a logit is NaN or,
+    with softmax, +inf (the experts then by their logits). The ids are what
+    logra_expert_sort takes, the weights what gather and combine take."""
     where = "logra_route"
     T, E, ld = _rows(where, logits)
     K = _choices(where, ids, torch.int32, T, "ids")
@@ -977,7 +978,9 @@ class AdamWList:
     it as long as a graph that was captured from its calls.
 
     params   float32 or bfloat16 tensors on one GPU, contiguous of any shape or
-             2-D with unit column stride and a longer row stride.
+             2-D with unit column stride and a longer row stride (column slices
+             of one buffer too; gradients that Step clips may not lie between
+             each other's rows, see GradList).
     grads    their gradients, of the same shapes, float32 or bfloat16, written
              in place every step.
     copies   tensors of the same shapes that are given the new parameters too
@@ -1090,7 +1093,12 @@ def logra_adamw(tensors: AdamWList, lr: float, beta1: float, beta2: float, eps: 
     """One AdamW step over the list's tensors, in place: parameters, copies and
     moments. step counts from 1. norm (of logra_grad_norm): gradients are taken
     times max_norm / norm where norm is above max_norm; a norm that is not
-    finite leaves everything as it is. seed keys the rounding of 8-bit moments."""
+    finite leaves everything as it is. seed keys the rounding of 8-bit moments.
+    The call works on the memory that the list was made with and does not look
+    whether its tensors still have it (`tensors.describes` does, in about a
+    microsecond a tensor). Its numbers are the host's: captured in a graph it
+    repeats that very step, so a program that replays its steps calls it
+    between the replays."""
     where = "logra_adamw"
     if norm is not None:
         _one_float(where, norm)

@@ -22,11 +22,13 @@
 // groups in doubt). Weights are fp32, as ratios of exponentials of differences
 // that cannot overflow or all vanish.
 //
-// A wave per token: up to some thousand tokens the time is one wave's chain of
+// A wave per token. Up to some thousand tokens the time is one wave's chain of
 // choices, not memory (4 MB of logits are 1 us). 4096 tokens to 8 of 256
-// experts, four of eight groups: 9.2 us (a token or two in doubt, at the end of
-// it all, are 1.7 of them), 10.6 with fp64 keys for all; 16384 tokens 22.9 and
-// 29.1; 65536 tokens 75 and 96.
+// experts, four of eight groups: 9.3 us (a token or two in doubt, at the end of
+// it all, are 1.7 of them), 10.6 with fp64 keys for all. Above that it is the
+// instructions that a whole wave spends on every choice of one token: 16384
+// tokens 23.6 us and 29.1, 65536 tokens 77 and 96, where the logits are 3.5 and
+// 14 us.
 #include <math.h>
 
 #include <type_traits>
@@ -431,7 +433,8 @@ struct RouteBackwardArgs {
 // another's lane (an expert chosen twice) are the choices gone through one by
 // one. 16384 tokens, 8 of 128 experts: 6.9 us, 9.3 before the look-up and with
 // loads one after the other; the rows read and written are 16.8 MB, 3.4 us at a
-// copy's rate.
+// copy's rate. The chosen logits are read after the ids, also where the wave has
+// the whole row in registers already: a second wait for memory.
 template <int N, int BF16>
 __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteBackwardArgs a) {
     __shared__ uint8_t owner[kRouteTokens][64 * N];

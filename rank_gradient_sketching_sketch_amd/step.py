@@ -449,9 +449,11 @@ class Step:
         given to Step, on the caller's stream. After `clip` (or a replay of a
         graph that holds one), a norm that is not finite leaves parameters and
         moments as they are: the host that reads the norm does not count that
-        step. The step's seed keys the rounding of 8-bit moments. After a
-        gradient in `grads` was replaced, give `adamw` a list that has the new
-        one (with the old list's state): ValueError until then."""
+        step. Called eagerly, also between the replays of a captured step: in a
+        graph it would repeat one step's number and learning rate. The step's
+        seed keys the rounding of 8-bit moments. After a gradient in `grads` was
+        replaced, give `adamw` a list that has the new one (with the old list's
+        state): ValueError until then."""
         if self.adamw is None:
             raise ValueError("the step was given no dense parameters")
         a = self.adamw
