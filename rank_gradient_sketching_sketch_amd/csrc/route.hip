@@ -24,10 +24,10 @@
 //
 // A wave per token. Up to some thousand tokens the time is one wave's chain of
 // choices, not memory (4 MB of logits are 1 us). 4096 tokens to 8 of 256
-// experts, four of eight groups: 9.3 us (a token or two in doubt, at the end of
+// experts, four of eight groups: 9.2 us (a token or two in doubt, at the end of
 // it all, are 1.7 of them), 10.6 with fp64 keys for all. Above that it is the
 // instructions that a whole wave spends on every choice of one token: 16384
-// tokens 23.6 us and 29.1, 65536 tokens 77 and 96, where the logits are 3.5 and
+// tokens 23.2 us and 29.1, 65536 tokens 76 and 96, where the logits are 3.5 and
 // 14 us.
 #include <math.h>
 
@@ -223,8 +223,9 @@ __device__ __forceinline__ RouteTold route_choose(const RouteArgs &a, typename P
             const Key high = P::lane(sum, __builtin_ctzll(__ballot(better == a.kept)));
             if (high > P::none()) {
                 if (a.best == 2) {
+                    // by every group's size, so by the largest
                     const float size = (one > P::none() ? fabsf(P::value(one)) : 0.f) + (two > P::none() ? fabsf(P::value(two)) : 0.f);
-                    if (doubt.near_sums(P::value(low), P::value(high), wave_max_f32(size))) return kRouteNothing;
+                    if (__ballot(doubt.near_sums(P::value(low), P::value(high), size)) != 0) return kRouteNothing;
                 } else if (doubt.near(P::value(low), P::value(high))) {
                     return kRouteNothing;
                 }
